@@ -1,0 +1,100 @@
+// C-ABI entry points of the grouped operations (trellis_grouped.h): argument
+// validation on the host, then launches on the caller's stream.
+#include <stdint.h>
+
+#include "checks.hpp"
+#include "groups.hpp"
+#include "launch.hpp"
+#include "trellis_grouped.h"
+
+using trellis::aligned;
+using trellis::status_of;
+
+static_assert(trellis::kMaxGroups == TRELLIS_MAX_GROUPS, "the header's limit");
+
+namespace {
+
+constexpr int32_t kMaxWidth = 1 << 19;
+
+// tokens x top_k slots of rows of `width` values.
+int check_slots(int32_t tokens, int32_t top_k) {
+    if (tokens < 0 || top_k < 1) return TRELLIS_ERR_GEOMETRY;
+    if (static_cast<int64_t>(tokens) * top_k > TRELLIS_MAX_SLOTS) return TRELLIS_ERR_GEOMETRY;
+    return TRELLIS_OK;
+}
+
+int check_moves(int32_t tokens, int32_t top_k, int32_t width) {
+    if (width < 1 || width > kMaxWidth) return TRELLIS_ERR_GEOMETRY;
+    return check_slots(tokens, top_k);
+}
+
+int check_groups(int32_t groups) {
+    return groups < 1 || groups > trellis::kMaxGroups ? TRELLIS_ERR_GEOMETRY : TRELLIS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t trellis_route_workspace_bytes(int32_t tokens, int32_t top_k, int32_t groups) {
+    if (check_slots(tokens, top_k) || check_groups(groups)) return static_cast<size_t>(-1);
+    return trellis::route_workspace_bytes(tokens * top_k, groups);
+}
+
+int trellis_route(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t groups,
+                  int32_t* offsets, int32_t* order, int32_t* position, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+    int st = check_slots(tokens, top_k);
+    if (st || (st = check_groups(groups))) return st;
+    const int slots = tokens * top_k;
+    if (!offsets || (slots && (!ids || !order || !position))) return TRELLIS_ERR_NULL;
+    if (!aligned(offsets, 4) || !aligned(ids, 4) || !aligned(order, 4) || !aligned(position, 4) ||
+        !aligned(workspace, 16))
+        return TRELLIS_ERR_ALIGN;
+    const size_t need = trellis::route_workspace_bytes(slots, groups);
+    if (need && (!workspace || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
+    return status_of(trellis::launch_route(ids, slots, groups, false, offsets, order, position,
+                                           static_cast<int32_t*>(workspace), stream));
+}
+
+int trellis_dispatch(const uint16_t* x, const int32_t* position, int32_t tokens, int32_t top_k,
+                     int32_t width, uint16_t* out, hipStream_t stream) {
+    const int st = check_moves(tokens, top_k, width);
+    if (st) return st;
+    if (tokens == 0) return TRELLIS_OK;
+    if (!x || !position || !out) return TRELLIS_ERR_NULL;
+    if (!aligned(x, 2) || !aligned(position, 4) || !aligned(out, 2)) return TRELLIS_ERR_ALIGN;
+    const bool vec = width % 8 == 0 && aligned(x, 16) && aligned(out, 16);
+    return status_of(trellis::launch_dispatch(x, position, tokens, top_k, width, out, vec, stream));
+}
+
+int trellis_combine(const uint16_t* y, const float* weights, const int32_t* position,
+                    int32_t tokens, int32_t top_k, int32_t width, uint16_t* out,
+                    hipStream_t stream) {
+    const int st = check_moves(tokens, top_k, width);
+    if (st) return st;
+    if (tokens == 0) return TRELLIS_OK;
+    if (!y || !position || !out) return TRELLIS_ERR_NULL;
+    if (!aligned(y, 2) || !aligned(weights, 4) || !aligned(position, 4) || !aligned(out, 2))
+        return TRELLIS_ERR_ALIGN;
+    const bool vec = width % 8 == 0 && aligned(y, 16) && aligned(out, 16);
+    return status_of(trellis::launch_combine(y, weights, position, tokens, top_k, width, out, vec,
+                                             stream));
+}
+
+int trellis_combine_backward(const uint16_t* dout, const uint16_t* y, const float* weights,
+                             const int32_t* position, int32_t tokens, int32_t top_k,
+                             int32_t width, uint16_t* dy, float* dweights, hipStream_t stream) {
+    const int st = check_moves(tokens, top_k, width);
+    if (st) return st;
+    if (tokens == 0) return TRELLIS_OK;
+    if (!dout || !y || !weights || !position || !dy || !dweights) return TRELLIS_ERR_NULL;
+    if (!aligned(dout, 2) || !aligned(y, 2) || !aligned(weights, 4) || !aligned(position, 4) ||
+        !aligned(dy, 2) || !aligned(dweights, 4))
+        return TRELLIS_ERR_ALIGN;
+    const bool vec = width % 8 == 0 && aligned(dout, 16) && aligned(y, 16) && aligned(dy, 16);
+    return status_of(trellis::launch_combine_backward(dout, y, weights, position, tokens, top_k,
+                                                      width, dy, dweights, vec, stream));
+}
+
+}  // extern "C"

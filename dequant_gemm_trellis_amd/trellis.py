@@ -1,4 +1,4 @@
-"""ctypes binding over libtrellis.so (include/trellis.h).
+"""ctypes binding over libtrellis.so (include/trellis.h, trellis_grouped.h).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI. PyTorch supplies device memory and the stream.
@@ -7,8 +7,10 @@ is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -40,7 +42,9 @@ EXPORTED = ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_
             "trellis_prefill", "trellis_prefill_dual", "trellis_gate_up_swiglu",
             "trellis_gemv_scatter_static", "trellis_static_scratch_bytes", "trellis_workspace_bytes",
             "trellis_expand", "trellis_repack", "trellis_strerror", "trellis_gather_probe",
-            "trellis_gather_probe_values", "trellis_gather_probe_out_floats")
+            "trellis_gather_probe_values", "trellis_gather_probe_out_floats", "trellis_route",
+            "trellis_route_workspace_bytes", "trellis_dispatch", "trellis_combine",
+            "trellis_combine_backward")
 PROBE_PAIR_B64, PROBE_COPIES8_B32, PROBE_SINGLE_B32 = 0, 1, 2
 
 
@@ -81,9 +85,17 @@ _lib.trellis_gather_probe_values.argtypes = [C.c_int32, C.c_int32]
 _lib.trellis_gather_probe_values.restype = C.c_uint64
 _lib.trellis_gather_probe_out_floats.argtypes = []
 _lib.trellis_gather_probe_out_floats.restype = C.c_size_t
+_i32 = C.c_int32
+_lib.trellis_route.argtypes = [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
+_lib.trellis_route_workspace_bytes.argtypes = [_i32, _i32, _i32]
+_lib.trellis_route_workspace_bytes.restype = C.c_size_t
+_lib.trellis_dispatch.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp]
+_lib.trellis_combine.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]
+_lib.trellis_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]
 for _f in ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_gemv_scatter",
            "trellis_prefill", "trellis_prefill_dual", "trellis_gate_up_swiglu", "trellis_expand",
-           "trellis_repack", "trellis_gemv_scatter_static"):
+           "trellis_repack", "trellis_gemv_scatter_static", "trellis_route", "trellis_dispatch",
+           "trellis_combine", "trellis_combine_backward"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -284,3 +296,140 @@ def gather_probe(kind: int, rounds: int, out: torch.Tensor, stream=None) -> int:
 
 def gather_probe_out_floats() -> int:
     return int(_lib.trellis_gather_probe_out_floats())
+
+
+# ---- grouped operations (trellis_grouped.h) ---------------------------------
+#
+# Every tensor is checked here (type, shape, contiguity, device): the C ABI sees
+# only addresses. Outputs and workspaces that a call allocates belong to the
+# stream it runs on.
+
+
+class Route(NamedTuple):
+    """Slots sorted by group (trellis_route), int32 on the GPU."""
+
+    offsets: torch.Tensor   # [groups + 1] first place of each group
+    order: torch.Tensor     # [tokens * top_k] slot at each place, -1 behind the last
+    position: torch.Tensor  # [tokens, top_k] place of each slot, -1 if dropped
+
+
+def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: device tensors must be contiguous and on the GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t
+
+
+def _dims(name: str, t: torch.Tensor, n: int) -> tuple:
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return tuple(t.shape)
+
+
+def _apart(outputs: dict, inputs: dict) -> None:
+    """Refuse an output that shares memory with an input or another output."""
+    spans = [(name, t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), out)
+             for out, group in ((True, outputs), (False, inputs))
+             for name, t in group.items() if t is not None and t.numel()]
+    for i, (a, a0, a1, out) in enumerate(spans):
+        for b, b0, b1, _ in spans[i + 1:]:
+            if out and a0 < b1 and b0 < a1:
+                raise ValueError(f"{a} overlaps {b}")
+
+
+def _on(stream: torch.cuda.Stream | None):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(fn: str, nbytes: int, given: torch.Tensor | None, device) -> tuple:
+    """(address, bytes, tensor) of the caller's workspace or of a new one."""
+    if nbytes == C.c_size_t(-1).value:
+        raise TrellisError(fn, ERR_GEOMETRY)
+    if given is None and nbytes:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _dev(given), 0 if given is None else given.numel() * given.element_size(), given
+
+
+def route(ids, groups: int, workspace=None, stream=None) -> Route:
+    """Sort the slots of ids (int32 [tokens, top_k]) by group, equal ids in slot
+    order; ids outside [0, groups) are dropped."""
+    tokens, top_k = _dims("ids", ids, 2)
+    _want("ids", ids, torch.int32, (tokens, top_k))
+    fn = "trellis_route"
+    with _on(stream):
+        nbytes = _lib.trellis_route_workspace_bytes(tokens, top_k, groups)
+        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, ids.device)
+        r = Route(torch.empty(groups + 1, dtype=torch.int32, device=ids.device),
+                  torch.empty(tokens * top_k, dtype=torch.int32, device=ids.device),
+                  torch.empty((tokens, top_k), dtype=torch.int32, device=ids.device))
+        _check(fn, _lib.trellis_route(_dev(ids), tokens, top_k, groups, _dev(r.offsets),
+                                      _dev(r.order), _dev(r.position), ws, ws_bytes,
+                                      _stream(None)))
+    return r
+
+
+def dispatch(x, route: Route, out=None, stream=None) -> torch.Tensor:
+    """Rows of x [tokens, width] at the places of their slots ([tokens * top_k,
+    width]); rows of `out` behind the last placed slot are left as they were.
+    Its gradient is combine(dout, None, route)."""
+    tokens, width = _dims("x", x, 2)
+    top_k = _dims("position", route.position, 2)[1]
+    _want("x", x, torch.bfloat16, (tokens, width))
+    _want("position", route.position, torch.int32, (tokens, top_k))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((tokens * top_k, width), dtype=torch.bfloat16, device=x.device)
+        _want("out", out, torch.bfloat16, (tokens * top_k, width))
+        _apart({"out": out}, {"x": x, "position": route.position})
+        _check("trellis_dispatch", _lib.trellis_dispatch(
+            _dev(x), _dev(route.position), tokens, top_k, width, _dev(out), _stream(None)))
+    return out
+
+
+def combine(y, weights, route: Route, out=None, stream=None) -> torch.Tensor:
+    """Every token's weighted sum of its slots' rows of y [tokens * top_k, width];
+    weights: float32 [tokens, top_k], or None for the plain sum."""
+    tokens, top_k = _dims("position", route.position, 2)
+    width = _dims("y", y, 2)[1]
+    _want("y", y, torch.bfloat16, (tokens * top_k, width))
+    _want("position", route.position, torch.int32, (tokens, top_k))
+    if weights is not None:
+        _want("weights", weights, torch.float32, (tokens, top_k))
+    with _on(stream):
+        if out is None:
+            out = torch.empty((tokens, width), dtype=torch.bfloat16, device=y.device)
+        _want("out", out, torch.bfloat16, (tokens, width))
+        _apart({"out": out}, {"y": y, "weights": weights, "position": route.position})
+        _check("trellis_combine", _lib.trellis_combine(
+            _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width, _dev(out),
+            _stream(None)))
+    return out
+
+
+def combine_backward(dout, y, weights, route: Route, dy=None, dweights=None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradients (dy, dweights) of combine(y, weights, route) from dout [tokens,
+    width]; rows of `dy` behind the last placed slot are left as they were."""
+    tokens, top_k = _dims("position", route.position, 2)
+    width = _dims("y", y, 2)[1]
+    _want("dout", dout, torch.bfloat16, (tokens, width))
+    _want("y", y, torch.bfloat16, (tokens * top_k, width))
+    _want("weights", weights, torch.float32, (tokens, top_k))
+    _want("position", route.position, torch.int32, (tokens, top_k))
+    with _on(stream):
+        if dy is None:
+            dy = torch.empty_like(y)
+        if dweights is None:
+            dweights = torch.empty_like(weights)
+        _want("dy", dy, torch.bfloat16, (tokens * top_k, width))
+        _want("dweights", dweights, torch.float32, (tokens, top_k))
+        _apart({"dy": dy, "dweights": dweights},
+               {"dout": dout, "y": y, "weights": weights, "position": route.position})
+        _check("trellis_combine_backward", _lib.trellis_combine_backward(
+            _dev(dout), _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width,
+            _dev(dy), _dev(dweights), _stream(None)))
+    return dy, dweights

@@ -1,0 +1,97 @@
+/*
+ * trellis_grouped.h -- operations of libtrellis.so whose rows are grouped by
+ * an index per row: tokens sorted by expert and back, the experts' coded
+ * products, and low-rank adapters of many requests beside one shared
+ * projection. The conventions of trellis.h hold (device pointers owned by the
+ * caller, dense row-major arrays, outputs overlapping nothing else, work
+ * enqueued on `stream`, nothing enqueued on a negative status), with these
+ * additions:
+ *   - Arrays of bf16, float32 and int32 need the alignment of their element;
+ *     workspaces, codes and codebooks need 16 bytes. Rows whose length is a
+ *     multiple of 8 in arrays aligned to 16 bytes are moved 16 bytes at a time.
+ *   - Group indexes, offsets and positions are read on the device and never
+ *     trusted as addresses: an index outside its range selects no row.
+ *   - Every sum runs in float32 in an order that the sizes and the indexes
+ *     fix, so repeated calls give identical bits.
+ *   - No call reads what an earlier call left in its workspace, and every
+ *     call may be captured into a graph and replayed with other indexes of
+ *     the same sizes. Calls (and graphs) that share a workspace must not
+ *     overlap in time.
+ */
+#ifndef TRELLIS_GROUPED_H
+#define TRELLIS_GROUPED_H
+
+#include "trellis.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Largest number of groups (experts, adapters) of one call. */
+#define TRELLIS_MAX_GROUPS 1024
+
+/* Largest number of slots (tokens x top_k) or rows of one call. */
+#define TRELLIS_MAX_SLOTS (1 << 24)
+
+/*
+ * Sort slots by group. ids: int32 [tokens][top_k]; slot i = token * top_k +
+ * choice. Slots with 0 <= ids[i] < groups are placed in ascending order of
+ * their id, slots of one id in ascending order of i; all other slots are
+ * dropped.
+ *   offsets  int32 [groups + 1]  first place of each group; the last entry is
+ *                                the number of placed slots
+ *   order    int32 [slots]       the slot at each place, -1 behind the last
+ *   position int32 [slots]       the place of each slot, -1 if dropped
+ * 0 <= tokens, 1 <= top_k, 1 <= groups <= TRELLIS_MAX_GROUPS, tokens * top_k
+ * <= TRELLIS_MAX_SLOTS. An id may occur more than once in a token. With no
+ * tokens only `offsets` is written (zeros). workspace: 16-byte aligned, at
+ * least trellis_route_workspace_bytes (0 for few slots: may be null then).
+ */
+int trellis_route(const int32_t *ids, int32_t tokens, int32_t top_k, int32_t groups,
+                  int32_t *offsets, int32_t *order, int32_t *position, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of trellis_route; (size_t)-1 if the sizes are not supported. */
+size_t trellis_route_workspace_bytes(int32_t tokens, int32_t top_k, int32_t groups);
+
+/*
+ * Copy every token's row to the places of its slots:
+ *   out[position[m][j]][:] = x[m][:]   for every slot with a place.
+ * x: bf16 [tokens][width]; position: int32 [tokens][top_k] of trellis_route;
+ * out: bf16 [tokens * top_k][width], whose rows behind the last placed slot
+ * are left as they were. Gradient: trellis_combine of the gradient of `out`
+ * without weights. 1 <= width <= 2^19.
+ */
+int trellis_dispatch(const uint16_t *x, const int32_t *position, int32_t tokens, int32_t top_k,
+                     int32_t width, uint16_t *out, hipStream_t stream);
+
+/*
+ * Bring the slots' rows back to their tokens and add them up:
+ *   out[m][:] = bf16( sum_j weights[m][j] * y[position[m][j]][:] ),
+ * j ascending over the slots with a place; a token without any gets zeros.
+ * Rows of dropped slots are not read and their weights do not enter (also
+ * where either is not finite). y: bf16 [tokens * top_k][width]; weights:
+ * float32 [tokens][top_k], or null for the plain sum; out: bf16
+ * [tokens][width].
+ */
+int trellis_combine(const uint16_t *y, const float *weights, const int32_t *position,
+                    int32_t tokens, int32_t top_k, int32_t width, uint16_t *out,
+                    hipStream_t stream);
+
+/*
+ * Gradient of trellis_combine with weights, from dout: bf16 [tokens][width]:
+ *   dy[position[m][j]][:] = bf16( weights[m][j] * dout[m][:] )
+ *   dweights[m][j]        = sum_h dout[m][h] * y[position[m][j]][h]
+ * for every slot with a place; dweights is 0 for dropped slots, and rows of
+ * dy behind the last placed slot are left as they were. dy: bf16
+ * [tokens * top_k][width]; dweights: float32 [tokens][top_k].
+ */
+int trellis_combine_backward(const uint16_t *dout, const uint16_t *y, const float *weights,
+                             const int32_t *position, int32_t tokens, int32_t top_k,
+                             int32_t width, uint16_t *dy, float *dweights, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TRELLIS_GROUPED_H */

@@ -1,0 +1,123 @@
+"""Host-side argument checks of the grouped operations (no GPU): sizes, null and
+misaligned pointers and workspaces are refused before anything is enqueued, and
+the binding refuses tensors of a wrong type, shape or place."""
+import ctypes as C
+import os
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x10000  # 16-byte aligned, never dereferenced: every call below is refused or has no rows
+
+
+@pytest.fixture(scope="module")
+def T():
+    if not os.path.exists(os.path.join(ROOT, "dequant_gemm_trellis_amd", "libtrellis.so")):
+        import __graft_entry__
+
+        __graft_entry__.build()
+    from dequant_gemm_trellis_amd import trellis
+
+    return trellis
+
+
+def call(T, name, params, defaults, **kw):
+    """Call an entry point with the defaults overridden by kw; integers named in
+    `params` with a leading '#' are sizes, the rest addresses."""
+    a = dict(defaults, **kw)
+    args = [a[n[1:]] if n[0] == "#" else C.c_void_p(a[n]) for n in params]
+    return getattr(T.raw(), name)(*args, C.c_void_p(0))
+
+
+ROUTE = ("ids", "#tokens", "#top_k", "#groups", "offsets", "order", "position", "ws", "#ws_bytes")
+ROUTE_ARGS = dict(ids=FAKE, tokens=5, top_k=2, groups=4, offsets=FAKE, order=FAKE, position=FAKE,
+                  ws=0, ws_bytes=0)
+
+
+def test_route_validation(T):
+    def route(**kw):
+        return call(T, "trellis_route", ROUTE, ROUTE_ARGS, **kw)
+
+    for kw in (dict(tokens=-1), dict(top_k=0), dict(groups=0), dict(groups=1025),
+               dict(tokens=1 << 24, top_k=2), dict(tokens=2 ** 31 - 1, top_k=2 ** 31 - 1)):
+        assert route(**kw) == T.ERR_GEOMETRY, kw
+    for arg in ("ids", "offsets", "order", "position"):
+        assert route(**{arg: 0}) == T.ERR_NULL, arg
+        assert route(**{arg: FAKE + 2}) == T.ERR_ALIGN, arg
+    assert route(ws=FAKE + 8) == T.ERR_ALIGN
+    need = T.raw().trellis_route_workspace_bytes(100000, 2, 4)
+    assert need > 0
+    assert route(tokens=100000) == T.ERR_WORKSPACE
+    assert route(tokens=100000, ws=FAKE, ws_bytes=need - 1) == T.ERR_WORKSPACE
+
+
+def test_route_workspace_bytes(T):
+    f = T.raw().trellis_route_workspace_bytes
+    none = C.c_size_t(-1).value
+    assert f(4096, 2, 128) == 0                      # one workgroup sorts these
+    assert f(4097, 2, 128) == 5 * 128 * 4            # five chunks of 2048 slots
+    assert f(1 << 24, 1, 1024) == 256 * 1024 * 4     # never more than 256 chunks
+    for bad in ((-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 1025), (1 << 24, 2, 1)):
+        assert f(*bad) == none, bad
+
+
+MOVES = {
+    "trellis_dispatch": (("x", "position", "#tokens", "#top_k", "#width", "out"), ()),
+    "trellis_combine": (("y", "weights", "position", "#tokens", "#top_k", "#width", "out"),
+                        ("weights",)),
+    "trellis_combine_backward": (("dout", "y", "weights", "position", "#tokens", "#top_k",
+                                  "#width", "dy", "dweights"), ()),
+}
+
+
+@pytest.mark.parametrize("name", sorted(MOVES))
+def test_moves_validation(T, name):
+    order, optional = MOVES[name]
+    args = {n.lstrip("#"): FAKE for n in order} | dict(tokens=5, top_k=2, width=64)
+
+    def move(**kw):
+        return call(T, name, order, args, **kw)
+
+    for kw in (dict(tokens=-1), dict(top_k=0), dict(width=0), dict(width=(1 << 19) + 1),
+               dict(tokens=1 << 23, top_k=3)):
+        assert move(**kw) == T.ERR_GEOMETRY, kw
+    for arg in order:
+        if arg[0] == "#":
+            continue
+        if arg not in optional:
+            assert move(**{arg: 0}) == T.ERR_NULL, arg
+        assert move(**{arg: FAKE + 1}) == T.ERR_ALIGN, arg
+    assert move(tokens=0) == T.OK  # nothing to do, nothing enqueued
+    assert move(tokens=0, **{order[0]: 0}) == T.OK
+
+
+def test_binding_refuses_host_and_mistyped_tensors(T):
+    ids = torch.zeros((3, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the GPU"):
+        T.route(ids, 4)
+    with pytest.raises(ValueError, match="int32"):
+        T.route(ids.long(), 4)
+    with pytest.raises(ValueError, match="2 dimensions"):
+        T.route(ids.reshape(-1), 4)
+    r = T.Route(torch.zeros(5, dtype=torch.int32), torch.zeros(6, dtype=torch.int32), ids)
+    x = torch.zeros((3, 8), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="on the GPU"):
+        T.dispatch(x, r)
+    with pytest.raises(ValueError, match="bfloat16"):
+        T.dispatch(x.float(), r)
+    with pytest.raises(ValueError):
+        T.combine(x, None, r)  # 3 rows where 6 slots are
+    with pytest.raises(ValueError):
+        T.combine_backward(x, x, torch.zeros((3, 2)), r)
+
+
+def test_overlap_check(T):
+    a = torch.zeros(64, dtype=torch.bfloat16)
+    T._apart({"out": a[:32]}, {"x": a[32:], "none": None})
+    with pytest.raises(ValueError, match="out overlaps x"):
+        T._apart({"out": a[:33]}, {"x": a[32:]})
+    with pytest.raises(ValueError, match="dy overlaps dw"):
+        T._apart({"dy": a, "dw": a[63:]}, {})
+    T._apart({"out": a[:0]}, {"x": a})                # nothing written
+    T._apart({"out": a[:8]}, {"x": a[16:], "y": a[16:]})  # inputs may share
