@@ -1,0 +1,697 @@
+// Low-rank adapters of many requests beside one shared projection
+// (trellis_adapters, trellis_adapters_backward). With a = ids[m]:
+//   u[m] = A[a] x[m],              y[m] = base[m] + s[a] B[a]^T u[m]
+//   g[m] = s[a] B[a] dy[m],        dx[m] = base[m] + A[a]^T g[m]
+//   dA[a] = sum_m g[m] x[m]^T,     dB[a] = sum_m s[a] u[m] dy[m]^T
+// A is [count][rank][in], B [count][rank][out]: stored alike, so three
+// products serve both directions: "inner" (a wide row times a factor's rows),
+// "expand" (a rank-long row times a factor, added to a wide row) and "outer"
+// (the sum over an adapter's rows of a rank-long times a wide row). Each reads
+// or writes the wide rows once and does little with them, so the memory bounds
+// them all.
+//
+// Few rows (kDirectRows): two launches that follow each row's own adapter.
+// Many rows: the rows are sorted by adapter and cut into tiles of 64 rows of
+// one adapter, which share the factor's values in bf16 matrix instructions.
+// There a rank-long float32 value w (u or g) enters as two bf16 parts, hi =
+// bf16(w) and lo = bf16(w - hi): 16 bits of mantissa, where one part alone
+// would add as much error as the rounding of the output. The two parts of 16
+// ranks fill the 32 contraction slots of one 16x16x32 instruction.
+//
+// A matrix instruction contracts over 8 consecutive values per lane. Where the
+// contraction runs across stored rows (ranks in expand, tokens in outer), a
+// lane loads an 8 x 8 patch, 16 bytes from each of 8 rows, and transposes it
+// in registers (one byte permute per output word): operand q then holds column
+// 8 j + q, and the eight results give a lane 8 adjacent columns to store.
+#include "common.hpp"
+#include "groups.hpp"
+#include "launch.hpp"
+
+namespace trellis {
+namespace {
+
+constexpr int kTileRows = 64;          // rows per tile: four 16-row operands
+constexpr int kSubs = kTileRows / 16;
+constexpr int kWgThreads = 256;
+constexpr int kWgWaves = kWgThreads / kWave;
+constexpr int kStrip = 128;            // columns per wave: 16 lanes x 8
+
+// The place of tile (or segment) t in a list that holds, group by group,
+// ceil(rows of the group / per) entries. Each wave searches for itself, 64
+// groups at a time; with `at_least_one` a group without rows has one entry.
+struct Found {
+    int group;   // -1: past the end
+    int index;   // entry within its group
+    int first;   // the group's first place, and the place after its last
+    int end;
+    int tiles;   // tiles of kTileRows rows of the groups before
+    int shared;  // entries of those groups before that have more than one
+};
+
+__device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets, int groups, int rows,
+                                            int per, bool at_least_one, int t) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, tiles = 0, shared = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        const int g = g0 + lane;
+        int first = 0, end = 0, n = 0, nt = 0;
+        if (g < groups) {
+            first = min(max(offsets[g], 0), rows);
+            end = min(max(offsets[g + 1], first), rows);
+            n = (end - first + per - 1) / per;
+            if (at_least_one && n == 0) n = 1;
+            nt = (end - first + kTileRows - 1) / kTileRows;
+        }
+        const int ns = n > 1 ? n : 0;
+        int inc = n, tinc = nt, sinc = ns;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int a = __shfl_up(inc, d), b = __shfl_up(tinc, d), e = __shfl_up(sinc, d);
+            if (lane >= d) {
+                inc += a;
+                tinc += b;
+                sinc += e;
+            }
+        }
+        const uint64_t past = __ballot(before + inc > t);
+        if (past) {
+            const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
+            return {g0 + l, t - before - __shfl(inc - n, l), __shfl(first, l), __shfl(end, l),
+                    tiles + __shfl(tinc - nt, l), shared + __shfl(sinc - ns, l)};
+        }
+        before += __shfl(inc, 63);
+        tiles += __shfl(tinc, 63);
+        shared += __shfl(sinc, 63);
+    }
+    return {-1, 0, 0, 0, 0, 0};
+}
+
+// 8 values of a row from column `col` on, zeros past `width` and where !live.
+// VEC: rows are multiples of 8 values and 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ row, int col, int width, bool live) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+        if (live && col < width) v = *reinterpret_cast<const u32x4*>(row + col);
+    } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t lo = live && col + 2 * d < width ? row[col + 2 * d] : 0u;
+            const uint32_t hi = live && col + 2 * d + 1 < width ? row[col + 2 * d + 1] : 0u;
+            v[d] = lo | (hi << 16);
+        }
+    }
+    return v;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t* __restrict__ row, int col, int width, u32x4 v) {
+    if constexpr (VEC) {
+        if (col < width) *reinterpret_cast<u32x4*>(row + col) = v;
+    } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if (col + 2 * d < width) row[col + 2 * d] = static_cast<uint16_t>(v[d]);
+            if (col + 2 * d + 1 < width) row[col + 2 * d + 1] = static_cast<uint16_t>(v[d] >> 16);
+        }
+    }
+}
+
+// Column q of an 8 x 8 patch (word d: rows 2d and 2d + 1), q known at compile time.
+template <int Q>
+__device__ __forceinline__ u32x4 patch_column(const u32x4 (&row)[8]) {
+    constexpr uint32_t sel = Q & 1 ? 0x07060302u : 0x05040100u;
+    u32x4 r;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        r[d] = __builtin_amdgcn_perm(row[2 * d + 1][Q / 2], row[2 * d][Q / 2], sel);
+    return r;
+}
+
+__device__ __forceinline__ float part_high(float w) {
+    return static_cast<float>(static_cast<__bf16>(w));
+}
+// The rest of w (none behind an infinity or a NaN, which the high part holds).
+__device__ __forceinline__ float part_low(float w, float high) {
+    return __builtin_isfinite(high) ? w - high : 0.f;
+}
+
+// ---- few rows ----------------------------------------------------------------
+
+constexpr int kDirectCols = 512;  // columns of x per workgroup: 64 lanes x 8
+
+// partial[split][m][r]: the workgroup's columns of u[m][r]; wave w takes ranks
+// w, w + 4, ... Grid: (splits, rows).
+template <bool VEC>
+__global__ __launch_bounds__(kWgThreads) void direct_inner_kernel(
+    const uint16_t* __restrict__ x, const int32_t* __restrict__ ids,
+    const uint16_t* __restrict__ factor, int width, int rank, int count,
+    float* __restrict__ partial) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int m = blockIdx.y, col = blockIdx.x * kDirectCols + 8 * lane;
+    const int a = ids[m];
+    if (static_cast<uint32_t>(a) >= static_cast<uint32_t>(count)) return;
+    const u32x4 xv = load8<VEC>(x + static_cast<size_t>(m) * width, col, width, true);
+    const uint16_t* f = factor + static_cast<size_t>(a) * rank * width;
+    float* out = partial + (static_cast<size_t>(blockIdx.x) * gridDim.y + m) * rank;
+#pragma unroll 4
+    for (int r = wave; r < rank; r += kWgWaves) {
+        const u32x4 w = load8<VEC>(f + static_cast<size_t>(r) * width, col, width, true);
+        float s = 0.f;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            s = fmaf(bf16_low(xv[d]), bf16_low(w[d]), s);
+            s = fmaf(bf16_high(xv[d]), bf16_high(w[d]), s);
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+        if (lane == 0) out[r] = s;
+    }
+}
+
+// y[m] = base[m] + s u[m] B. Each workgroup sums u[m] from the splits (ascending),
+// then its 2048 columns; the first one writes u. Grid: (column chunks, rows).
+template <bool VEC>
+__global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
+    const float* __restrict__ partial, int splits, const int32_t* __restrict__ ids,
+    const uint16_t* __restrict__ factor, const float* __restrict__ scales, int width, int rank,
+    int count, const uint16_t* base, uint16_t* y, float* __restrict__ u) {
+    __shared__ float us[kMaxRank];
+    const int m = blockIdx.y, tid = threadIdx.x, rows = gridDim.y;
+    const int a = ids[m];
+    const bool has = static_cast<uint32_t>(a) < static_cast<uint32_t>(count);
+    const int col = (blockIdx.x * kWgThreads + tid) * 8;
+    const uint16_t* brow = base + static_cast<size_t>(m) * width;
+    uint16_t* yrow = y + static_cast<size_t>(m) * width;
+    if (!has) {
+        if (u && blockIdx.x == 0)
+            for (int r = tid; r < rank; r += kWgThreads) u[static_cast<size_t>(m) * rank + r] = 0.f;
+        if (base != y && col < width) store8<VEC>(yrow, col, width, load8<VEC>(brow, col, width, base != nullptr));
+        return;
+    }
+    const u32x4 b = load8<VEC>(brow, col, width, base != nullptr);
+    for (int r = tid; r < rank; r += kWgThreads) {
+        float s = 0.f;
+        for (int k = 0; k < splits; ++k) s += partial[(static_cast<size_t>(k) * rows + m) * rank + r];
+        if (u && blockIdx.x == 0) u[static_cast<size_t>(m) * rank + r] = s;
+        us[r] = s * scales[a];
+    }
+    __syncthreads();
+    if (col >= width) return;
+    const uint16_t* f = factor + static_cast<size_t>(a) * rank * width;
+    float acc[8] = {};
+#pragma unroll 8
+    for (int r = 0; r < rank; ++r) {
+        const u32x4 w = load8<VEC>(f + static_cast<size_t>(r) * width, col, width, true);
+        const float ur = us[r];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            acc[2 * d] = fmaf(ur, bf16_low(w[d]), acc[2 * d]);
+            acc[2 * d + 1] = fmaf(ur, bf16_high(w[d]), acc[2 * d + 1]);
+        }
+    }
+    u32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        o[d] = pack_bf16(bf16_low(b[d]) + acc[2 * d], bf16_high(b[d]) + acc[2 * d + 1]);
+    store8<VEC>(yrow, col, width, o);
+}
+
+// ---- many rows ----------------------------------------------------------------
+
+// partial[split][tile][64][16 R]: this split's columns of the tile's inner
+// products. The four waves take the split's 32-column steps in turn and are
+// summed in wave order. Grid: (splits, tiles).
+template <int R, bool VEC>
+__global__ __launch_bounds__(kWgThreads) void inner_kernel(
+    const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ order, const uint16_t* __restrict__ factor, int rows, int width,
+    int rank, int count, int split_cols, float* __restrict__ partial) {
+    __shared__ float sum[kTileRows * 16 * R];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int j = lane & 15, c = lane >> 4;
+    const Found at = find_entry(offsets, count, rows, kTileRows, false, blockIdx.y);
+    if (at.group < 0) return;
+    const int p0 = at.first + at.index * kTileRows;
+    const uint16_t* xr[kSubs];
+#pragma unroll
+    for (int s = 0; s < kSubs; ++s)  // rows past the group's last read the last one again
+        xr[s] = x + static_cast<size_t>(order[min(p0 + 16 * s + j, at.end - 1)]) * width;
+    const uint16_t* f = factor + static_cast<size_t>(at.group) * rank * width;
+    const uint16_t* fr[R];
+#pragma unroll
+    for (int s = 0; s < R; ++s) fr[s] = f + static_cast<size_t>(min(16 * s + j, rank - 1)) * width;
+    floatx4 acc[kSubs][R] = {};
+    const int k0 = blockIdx.x * split_cols, k1 = min(width, k0 + split_cols);
+#pragma unroll 2
+    for (int k = k0 + 32 * wave; k < k1; k += 32 * kWgWaves) {
+        u32x4 xv[kSubs], fv[R];
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) xv[s] = load8<VEC>(xr[s], k + 8 * c, k1, true);
+#pragma unroll
+        for (int s = 0; s < R; ++s) fv[s] = load8<VEC>(fr[s], k + 8 * c, k1, true);
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                acc[s][r] = mfma16x16x32(as_bf16x8(xv[s]), as_bf16x8(fv[r]), acc[s][r]);
+    }
+    for (int w = 0; w < kWgWaves; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float* o = sum + (16 * s + 4 * c + i) * (16 * R) + 16 * r + j;
+                        *o = w ? *o + acc[s][r][i] : acc[s][r][i];
+                    }
+        }
+        __syncthreads();
+    }
+    floatx4* out = reinterpret_cast<floatx4*>(
+        partial + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * (kTileRows * 16 * R));
+    for (int i = tid; i < kTileRows * 16 * R / 4; i += kWgThreads)
+        out[i] = reinterpret_cast<const floatx4*>(sum)[i];
+}
+
+// What the later launches read of a tile.
+struct TileInfo {
+    int32_t group;  // its adapter; count: rows without one; -1: no tile
+    int32_t rows;
+};
+
+// One workgroup per tile: its rows' numbers and group, the inner products from
+// the splits (ascending), and their operand forms.
+//   by_row [tile][64][R][hi 16 | lo 16]    (expand; scaled)
+//   by_rank[tile][R][hi | lo][16][64]      (outer; scaled)
+//   u_rank                                 the same of the forward pass's u
+// Rows past the tile's last and ranks past the last are zeros there.
+__global__ __launch_bounds__(kWgThreads) void tile_kernel(
+    const float* __restrict__ partial, int splits, int tiles, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ order, const float* __restrict__ scales, int rows, int rank, int r16,
+    int count, TileInfo* __restrict__ info, int32_t* __restrict__ tile_rows,
+    uint16_t* __restrict__ by_row, uint16_t* __restrict__ by_rank, float* __restrict__ u_out,
+    const float* __restrict__ u_in, uint16_t* __restrict__ u_rank) {
+    const int t = blockIdx.x, tid = threadIdx.x;
+    const Found at = find_entry(offsets, count + 1, rows, kTileRows, false, t);
+    const int p0 = at.first + at.index * kTileRows;
+    const int n = at.group < 0 ? 0 : min(kTileRows, at.end - p0);
+    if (tid == 0) info[t] = {at.group, n};
+    if (at.group < 0) return;
+    if (tid < kTileRows) tile_rows[t * kTileRows + tid] = tid < n ? order[p0 + tid] : -1;
+    const int ranks = 16 * r16;
+    if (at.group == count) {
+        if (u_out)
+            for (int i = tid; i < n * rank; i += kWgThreads)
+                u_out[static_cast<size_t>(order[p0 + i / rank]) * rank + i % rank] = 0.f;
+        return;
+    }
+    const float scale = scales[at.group];
+    for (int i = tid; i < kTileRows * ranks; i += kWgThreads) {
+        const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
+        const bool live = row < n && r < rank;
+        const size_t orig = live ? order[p0 + row] : 0;
+        const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * 2 * 16 + rr) * kTileRows + row;
+        float v = 0.f;
+        if (live)
+            for (int k = 0; k < splits; ++k)
+                v += partial[(static_cast<size_t>(k) * tiles + t) * (kTileRows * ranks) + i];
+        if (u_out && live) u_out[orig * rank + r] = v;
+        const float w = v * scale, hi = part_high(w), lo = part_low(w, hi);
+        uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * 32 + rr;
+        q[0] = round_bf16(hi);
+        q[16] = round_bf16(lo);
+        if (by_rank) {
+            by_rank[rank_at] = round_bf16(hi);
+            by_rank[rank_at + 16 * kTileRows] = round_bf16(lo);
+            const float uw = live ? u_in[orig * rank + r] * scale : 0.f;
+            const float uh = part_high(uw), ul = part_low(uw, uh);
+            u_rank[rank_at] = round_bf16(uh);
+            u_rank[rank_at + 16 * kTileRows] = round_bf16(ul);
+        }
+    }
+}
+
+// y[row] = base[row] + (scaled rank-long row) * factor. A wave takes 128
+// columns of a tile, two 16-row operands at a time. Grid: (column chunks, tiles).
+template <bool VEC>
+__global__ __launch_bounds__(kWgThreads) void expand_kernel(
+    const TileInfo* __restrict__ info, const int32_t* __restrict__ tile_rows,
+    const uint16_t* __restrict__ by_row, const uint16_t* __restrict__ factor, int width, int rank,
+    int r16, int count, const uint16_t* base, uint16_t* y) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int j = lane & 15, c = lane >> 4;
+    const int t = blockIdx.y;
+    const TileInfo ti = info[t];
+    const int col = (blockIdx.x * kWgWaves + wave) * kStrip + 8 * j;
+    if (ti.group < 0 || col - 8 * j >= width) return;
+    const int32_t* trow = tile_rows + t * kTileRows;
+    if (ti.group == count) {  // rows without an adapter
+        if (base == y) return;
+        for (int i = c; i < ti.rows; i += 4) {
+            const size_t at = static_cast<size_t>(trow[i]) * width;
+            store8<VEC>(y + at, col, width, load8<VEC>(base + at, col, width, base != nullptr));
+        }
+        return;
+    }
+    const uint16_t* f = factor + static_cast<size_t>(ti.group) * rank * width;
+    const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * 32;
+    for (int s0 = 0; s0 < kSubs; s0 += 2) {
+        if (16 * s0 >= ti.rows) return;
+        int row[2][4];
+        u32x4 bv[2][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                row[s][i] = trow[16 * (s0 + s) + 4 * c + i];
+                bv[s][i] = load8<VEC>(base + static_cast<size_t>(max(row[s][i], 0)) * width, col, width,
+                                      base && row[s][i] >= 0);
+            }
+        floatx4 acc[2][8] = {};
+        for (int r = 0; r < r16; ++r) {
+            u32x4 patch[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // lanes c and c + 2: the ranks of the hi and of the lo parts
+                const int rr = 16 * r + 8 * (c & 1) + i;
+                patch[i] = load8<VEC>(f + static_cast<size_t>(min(rr, rank - 1)) * width, col, width,
+                                      rr < rank);
+            }
+            u32x4 a[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                a[s] = *reinterpret_cast<const u32x4*>(
+                    rows_op + (static_cast<size_t>(16 * (s0 + s) + j) * r16 + r) * 32 + 8 * c);
+            static_for<0, 8>([&](auto qc) {
+                constexpr int q = decltype(qc)::value;
+                const u32x4 b = patch_column<q>(patch);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    acc[s][q] = mfma16x16x32(as_bf16x8(a[s]), as_bf16x8(b), acc[s][q]);
+            });
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (row[s][i] < 0) continue;
+                u32x4 o;
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    o[d] = pack_bf16(bf16_low(bv[s][i][d]) + acc[s][2 * d][i],
+                                     bf16_high(bv[s][i][d]) + acc[s][2 * d + 1][i]);
+                store8<VEC>(y + static_cast<size_t>(row[s][i]) * width, col, width, o);
+            }
+    }
+}
+
+// Sum over a segment's rows of (rank-long column) x (wide row): the segment's
+// tiles go to the four waves in turn, which are summed in wave order. An
+// adapter of one segment (or without rows) is written to `grad` in bf16; the
+// float32 sums of the others' segments go to `sums`, [shared segment][rank]
+// [width]. Grid: (strips, segments, rank pairs).
+template <int R, bool VEC>
+__global__ __launch_bounds__(kWgThreads) void outer_kernel(
+    const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ tile_rows, const uint16_t* __restrict__ by_rank, int rows, int width,
+    int rank, int r16, int count, int seg_tiles, float* __restrict__ sums,
+    uint16_t* __restrict__ grad) {
+    __shared__ float sum[16 * R * kStrip];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int j = lane & 15, c = lane >> 4;
+    const int r0 = blockIdx.z * R;  // this workgroup's 16-rank operands: r0 .. r0 + R - 1
+    const Found at = find_entry(offsets, count, rows, seg_tiles * kTileRows, true, blockIdx.y);
+    if (at.group < 0) return;
+    const int col = blockIdx.x * kStrip + 8 * j;
+    const int group_tiles = (at.end - at.first + kTileRows - 1) / kTileRows;
+    const int t0 = at.tiles + at.index * seg_tiles;
+    const int t1 = at.tiles + min(group_tiles, (at.index + 1) * seg_tiles);
+    floatx4 acc[R][8] = {};
+    for (int t = t0 + wave; t < t1; t += kWgWaves) {
+#pragma unroll
+        for (int h = 0; h < kTileRows / 32; ++h) {
+            const int32_t* trow = tile_rows + t * kTileRows + 32 * h + 8 * c;
+            u32x4 patch[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                patch[i] = load8<VEC>(x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
+                                      trow[i] >= 0);
+            u32x4 a[R][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    a[r][part] = r0 + r < r16
+                                     ? *reinterpret_cast<const u32x4*>(
+                                           by_rank + (((static_cast<size_t>(t) * r16 + r0 + r) * 2 + part) *
+                                                          16 + j) * kTileRows + 32 * h + 8 * c)
+                                     : u32x4{0u, 0u, 0u, 0u};
+            static_for<0, 8>([&](auto qc) {
+                constexpr int q = decltype(qc)::value;
+                const u32x4 b = patch_column<q>(patch);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    acc[r][q] = mfma16x16x32(as_bf16x8(a[r][0]), as_bf16x8(b), acc[r][q]);
+                    acc[r][q] = mfma16x16x32(as_bf16x8(a[r][1]), as_bf16x8(b), acc[r][q]);
+                }
+            });
+        }
+    }
+    for (int w = 0; w < kWgWaves; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float* o = sum + (16 * r + 4 * c + i) * kStrip + 8 * j;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) o[q] = w ? o[q] + acc[r][q][i] : acc[r][q][i];
+                }
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < 16 * R * kStrip; i += kWgThreads) {
+        const int r = 16 * r0 + i / kStrip, k = blockIdx.x * kStrip + i % kStrip;
+        if (r >= rank || k >= width) continue;
+        if (group_tiles > seg_tiles)
+            sums[(static_cast<size_t>(at.shared + at.index) * rank + r) * width + k] = sum[i];
+        else
+            grad[(static_cast<size_t>(at.group) * rank + r) * width + k] = round_bf16(sum[i]);
+    }
+}
+
+// The segments' sums of an adapter of several, ascending, rounded to bf16.
+// Grid: (column chunks, ranks, adapters).
+__global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
+    const float* __restrict__ sums, const int32_t* __restrict__ offsets, int rows, int width,
+    int rank, int seg_tiles, uint16_t* __restrict__ grad) {
+    const int a = blockIdx.z, r = blockIdx.y;
+    const int k = blockIdx.x * kWgThreads + threadIdx.x;
+    const int lane = threadIdx.x & 63, per = seg_tiles * kTileRows;
+    int before = 0, mine = 0;  // shared segments of the adapters before, and this one's segments
+    for (int g0 = 0; g0 <= a; g0 += 64) {
+        const int g = g0 + lane;
+        int n = 0;
+        if (g <= a) {
+            const int first = min(max(offsets[g], 0), rows);
+            n = (min(max(offsets[g + 1], first), rows) - first + per - 1) / per;
+        }
+        int s = g < a && n > 1 ? n : 0;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+        before += s;
+        mine = __shfl(n, a & 63);
+    }
+    if (mine <= 1 || k >= width) return;
+    float v = 0.f;
+    for (int q = 0; q < mine; ++q)
+        v += sums[(static_cast<size_t>(before + q) * rank + r) * width + k];
+    grad[(static_cast<size_t>(a) * rank + r) * width + k] = round_bf16(v);
+}
+
+// ---- plans and launches ---------------------------------------------------------
+
+// Rows up to which each row follows its own adapter (two launches, the factors
+// read again by rows that share one).
+constexpr int kDirectRows = 64;
+constexpr int kTargetGroups = 1024;  // workgroups that fill the compute units a few times
+constexpr int kSegTiles = 16;        // tiles of one segment of the outer sums: 1024 rows
+
+struct Plan {
+    int r16, tiles;             // 16-rank operands; tiles at most
+    int splits, split_cols;     // column splits of the inner products
+    int segments;               // segments of the outer sums, at most
+    int shared;                 // those of adapters with several, at most
+    size_t offsets, order, counts, partial, info, tile_rows, by_row, by_rank, u_rank, sums, bytes;
+};
+
+int inner_splits(int tiles, int width) {
+    const int most = (width + 255) / 256;
+    const int want = tiles ? (kTargetGroups + tiles - 1) / tiles : 1;
+    const int n = want < most ? want : most;
+    return n < 1 ? 1 : n > 32 ? 32 : n;
+}
+
+// Columns of one split: a multiple of 128 (a 32-column step per wave).
+int split_columns(int width, int splits) {
+    return ((width + splits - 1) / splits + 127) / 128 * 128;
+}
+
+Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
+    Plan p{};
+    p.r16 = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
+    p.tiles = (rows + kTileRows - 1) / kTileRows + (count + 1 < rows ? count + 1 : rows);
+    const int width = backward ? out : in;
+    p.split_cols = split_columns(width, inner_splits(p.tiles, width));
+    p.splits = (width + p.split_cols - 1) / p.split_cols;
+    const int per = kSegTiles * kTileRows;
+    p.segments = count + rows / per;             // sum of max(1, ceil(n / per)), at most
+    p.shared = rows > per ? 2 * (rows / per) : 0;  // n > per: ceil(n / per) <= 2 floor(n / per)
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    const size_t tiles = p.tiles, ranks = 16 * static_cast<size_t>(p.r16);
+    p.offsets = take((static_cast<size_t>(count) + 2) * 4);
+    p.order = take(static_cast<size_t>(rows) * 4);
+    p.counts = take(route_workspace_bytes(rows, count + 1));
+    p.partial = take(p.splits * tiles * kTileRows * ranks * 4);
+    p.info = take(tiles * sizeof(TileInfo));
+    p.tile_rows = take(tiles * kTileRows * 4);
+    p.by_row = take(tiles * kTileRows * ranks * 2 * 2);
+    if (backward) {
+        p.by_rank = take(tiles * kTileRows * ranks * 2 * 2);
+        p.u_rank = take(tiles * kTileRows * ranks * 2 * 2);
+        p.sums = take(static_cast<size_t>(p.shared) * rank * (in > out ? in : out) * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+template <typename T>
+T* at(void* ws, size_t offset) {
+    return reinterpret_cast<T*>(static_cast<char*>(ws) + offset);
+}
+
+template <bool VEC>
+hipError_t launch_inner(const Plan& p, const uint16_t* x, const uint16_t* factor, int rows, int width,
+                        int rank, int count, void* ws, hipStream_t st) {
+    auto kernel = p.r16 == 1   ? inner_kernel<1, VEC>
+                  : p.r16 == 2 ? inner_kernel<2, VEC>
+                  : p.r16 <= 4 ? inner_kernel<4, VEC>
+                               : inner_kernel<8, VEC>;
+    return launch_kernel(kernel, dim3(p.splits, p.tiles), dim3(kWgThreads), st, x,
+                         at<int32_t>(ws, p.offsets), at<int32_t>(ws, p.order), factor, rows, width,
+                         rank, count, p.split_cols, at<float>(ws, p.partial));
+}
+
+hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int rank, int count,
+                         const uint16_t* base, uint16_t* y, bool vec, void* ws, hipStream_t st) {
+    const int chunk = kWgWaves * kStrip;
+    return launch_kernel(vec ? expand_kernel<true> : expand_kernel<false>,
+                         dim3((width + chunk - 1) / chunk, p.tiles), dim3(kWgThreads), st,
+                         at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
+                         at<uint16_t>(ws, p.by_row), factor, width, rank, p.r16, count, base, y);
+}
+
+template <int R>
+hipError_t launch_outer_r(const Plan& p, const uint16_t* x, const uint16_t* by_rank, int rows,
+                          int width, int rank, int count, uint16_t* grad, bool vec, void* ws,
+                          hipStream_t st) {
+    float* sums = at<float>(ws, p.sums);
+    const hipError_t e = launch_kernel(
+        vec ? outer_kernel<R, true> : outer_kernel<R, false>,
+        dim3((width + kStrip - 1) / kStrip, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, x,
+        at<int32_t>(ws, p.offsets), at<int32_t>(ws, p.tile_rows), by_rank, rows, width, rank, p.r16,
+        count, kSegTiles, sums, grad);
+    if (e != hipSuccess || !p.shared) return e;
+    return launch_kernel(outer_sum_kernel, dim3((width + kWgThreads - 1) / kWgThreads, rank, count),
+                         dim3(kWgThreads), st, sums, at<int32_t>(ws, p.offsets), rows, width, rank,
+                         kSegTiles, grad);
+}
+
+hipError_t launch_outer(const Plan& p, const uint16_t* x, const uint16_t* by_rank, int rows,
+                        int width, int rank, int count, uint16_t* grad, bool vec, void* ws,
+                        hipStream_t st) {
+    return p.r16 == 1 ? launch_outer_r<1>(p, x, by_rank, rows, width, rank, count, grad, vec, ws, st)
+                      : launch_outer_r<2>(p, x, by_rank, rows, width, rank, count, grad, vec, ws, st);
+}
+
+int direct_splits(int width) { return (width + kDirectCols - 1) / kDirectCols; }
+
+}  // namespace
+
+size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, bool backward) {
+    if (!backward && rows <= kDirectRows)
+        return static_cast<size_t>(direct_splits(in)) * rows * rank * sizeof(float);
+    return make_plan(rows, in, out, rank, count, backward).bytes;
+}
+
+hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterFactors& f,
+                           int rows, const uint16_t* base, uint16_t* y, float* u, bool vec_in,
+                           bool vec_out, void* ws, hipStream_t st) {
+    hipError_t e;
+    if (rows == 0) return hipSuccess;
+    if (rows <= kDirectRows) {
+        const int splits = direct_splits(f.in);
+        e = launch_kernel(vec_in ? direct_inner_kernel<true> : direct_inner_kernel<false>,
+                          dim3(splits, rows), dim3(kWgThreads), st, x, ids, f.a, f.in, f.rank,
+                          f.count, static_cast<float*>(ws));
+        if (e != hipSuccess) return e;
+        const int chunk = kWgThreads * 8;
+        return launch_kernel(vec_out ? direct_expand_kernel<true> : direct_expand_kernel<false>,
+                             dim3((f.out + chunk - 1) / chunk, rows), dim3(kWgThreads), st,
+                             static_cast<const float*>(ws), splits, ids, f.b, f.scales, f.out,
+                             f.rank, f.count, base, y, u);
+    }
+    const Plan p = make_plan(rows, f.in, f.out, f.rank, f.count, false);
+    if ((e = launch_route(ids, rows, f.count, true, at<int32_t>(ws, p.offsets),
+                          at<int32_t>(ws, p.order), nullptr, at<int32_t>(ws, p.counts), st)))
+        return e;
+    if ((e = vec_in ? launch_inner<true>(p, x, f.a, rows, f.in, f.rank, f.count, ws, st)
+                    : launch_inner<false>(p, x, f.a, rows, f.in, f.rank, f.count, ws, st)))
+        return e;
+    if ((e = launch_kernel(tile_kernel, dim3(p.tiles), dim3(kWgThreads), st,
+                           at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
+                           at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
+                           at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
+                           at<uint16_t>(ws, p.by_row), nullptr, u, nullptr, nullptr)))
+        return e;
+    return launch_expand(p, f.b, f.out, f.rank, f.count, base, y, vec_out, ws, st);
+}
+
+hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* u,
+                                    const int32_t* ids, const AdapterFactors& f, int rows,
+                                    const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
+                                    bool vec_in, bool vec_out, void* ws, hipStream_t st) {
+    hipError_t e;
+    const Plan p = make_plan(rows, f.in, f.out, f.rank, f.count, true);
+    if ((e = launch_route(ids, rows, f.count, true, at<int32_t>(ws, p.offsets),
+                          at<int32_t>(ws, p.order), nullptr, at<int32_t>(ws, p.counts), st)))
+        return e;
+    // without rows the outer sums write zeros, and nothing else is left to do
+    if (rows && (e = vec_out ? launch_inner<true>(p, dy, f.b, rows, f.out, f.rank, f.count, ws, st)
+                             : launch_inner<false>(p, dy, f.b, rows, f.out, f.rank, f.count, ws, st)))
+        return e;
+    if (rows && (e = launch_kernel(tile_kernel, dim3(p.tiles), dim3(kWgThreads), st,
+                           at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
+                           at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
+                           at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
+                           at<uint16_t>(ws, p.by_row), at<uint16_t>(ws, p.by_rank), nullptr, u,
+                           at<uint16_t>(ws, p.u_rank))))
+        return e;
+    if ((e = launch_outer(p, dy, at<uint16_t>(ws, p.u_rank), rows, f.out, f.rank, f.count, db,
+                          vec_out, ws, st)))
+        return e;
+    if ((e = launch_outer(p, x, at<uint16_t>(ws, p.by_rank), rows, f.in, f.rank, f.count, da, vec_in,
+                          ws, st)))
+        return e;
+    if (rows == 0) return hipSuccess;
+    return launch_expand(p, f.a, f.in, f.rank, f.count, base, dx, vec_in, ws, st);
+}
+
+}  // namespace trellis

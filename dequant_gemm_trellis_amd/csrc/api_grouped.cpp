@@ -11,6 +11,7 @@ using trellis::aligned;
 using trellis::status_of;
 
 static_assert(trellis::kMaxGroups == TRELLIS_MAX_GROUPS, "the header's limit");
+static_assert(trellis::kMaxRank == TRELLIS_MAX_RANK, "the header's limit");
 
 namespace {
 
@@ -32,6 +33,35 @@ int check_groups(int32_t groups) {
     return groups < 1 || groups > trellis::kMaxGroups ? TRELLIS_ERR_GEOMETRY : TRELLIS_OK;
 }
 
+// The sizes of an adapter set and of the rows it is applied to.
+int check_adapters(const trellis_adapter_set* f, int32_t rows) {
+    if (!f) return TRELLIS_ERR_NULL;
+    if (check_groups(f->count) || f->rank < 1 || f->rank > TRELLIS_MAX_RANK ||
+        f->in_features < 1 || f->in_features > kMaxWidth || f->out_features < 1 ||
+        f->out_features > kMaxWidth || rows < 0 || rows > TRELLIS_MAX_ADAPTER_ROWS)
+        return TRELLIS_ERR_GEOMETRY;
+    return TRELLIS_OK;
+}
+
+int check_factors(const trellis_adapter_set* f) {
+    if (!f->a || !f->b || !f->scales) return TRELLIS_ERR_NULL;
+    if (!aligned(f->a, 2) || !aligned(f->b, 2) || !aligned(f->scales, 4)) return TRELLIS_ERR_ALIGN;
+    return TRELLIS_OK;
+}
+
+trellis::AdapterFactors factors(const trellis_adapter_set* f) {
+    return {f->a, f->b, f->scales, f->in_features, f->out_features, f->rank, f->count};
+}
+
+bool all16(const void* p, const void* q, const void* r) {
+    return aligned(p, 16) && aligned(q, 16) && aligned(r, 16);
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (!aligned(workspace, 16)) return TRELLIS_ERR_ALIGN;
+    return need && (!workspace || bytes < need) ? TRELLIS_ERR_WORKSPACE : TRELLIS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -48,11 +78,11 @@ int trellis_route(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t gro
     if (st || (st = check_groups(groups))) return st;
     const int slots = tokens * top_k;
     if (!offsets || (slots && (!ids || !order || !position))) return TRELLIS_ERR_NULL;
-    if (!aligned(offsets, 4) || !aligned(ids, 4) || !aligned(order, 4) || !aligned(position, 4) ||
-        !aligned(workspace, 16))
+    if (!aligned(offsets, 4) || !aligned(ids, 4) || !aligned(order, 4) || !aligned(position, 4))
         return TRELLIS_ERR_ALIGN;
-    const size_t need = trellis::route_workspace_bytes(slots, groups);
-    if (need && (!workspace || workspace_bytes < need)) return TRELLIS_ERR_WORKSPACE;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              trellis::route_workspace_bytes(slots, groups))))
+        return st;
     return status_of(trellis::launch_route(ids, slots, groups, false, offsets, order, position,
                                            static_cast<int32_t*>(workspace), stream));
 }
@@ -95,6 +125,52 @@ int trellis_combine_backward(const uint16_t* dout, const uint16_t* y, const floa
     const bool vec = width % 8 == 0 && aligned(dout, 16) && aligned(y, 16) && aligned(dy, 16);
     return status_of(trellis::launch_combine_backward(dout, y, weights, position, tokens, top_k,
                                                       width, dy, dweights, vec, stream));
+}
+
+size_t trellis_adapters_workspace_bytes(const trellis_adapter_set* f, int32_t rows,
+                                        int32_t backward) {
+    if (check_adapters(f, rows)) return static_cast<size_t>(-1);
+    return trellis::adapters_workspace_bytes(rows, f->in_features, f->out_features, f->rank,
+                                             f->count, backward != 0);
+}
+
+int trellis_adapters(const uint16_t* x, const int32_t* ids, int32_t rows,
+                     const trellis_adapter_set* f, const uint16_t* base, uint16_t* y, float* u,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_adapters(f, rows);
+    if (st) return st;
+    if (rows == 0) return TRELLIS_OK;
+    if (!x || !ids || !y) return TRELLIS_ERR_NULL;
+    if ((st = check_factors(f))) return st;
+    if (!aligned(x, 2) || !aligned(ids, 4) || !aligned(base, 2) || !aligned(y, 2) || !aligned(u, 4))
+        return TRELLIS_ERR_ALIGN;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              trellis_adapters_workspace_bytes(f, rows, 0))))
+        return st;
+    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, nullptr);
+    const bool vec_out = f->out_features % 8 == 0 && all16(base, y, f->b);
+    return status_of(trellis::launch_adapters(x, ids, factors(f), rows, base, y, u, vec_in, vec_out,
+                                              workspace, stream));
+}
+
+int trellis_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* u,
+                              const int32_t* ids, int32_t rows, const trellis_adapter_set* f,
+                              const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_adapters(f, rows);
+    if (st) return st;
+    if (!da || !db || (rows && (!dy || !x || !u || !ids || !dx))) return TRELLIS_ERR_NULL;
+    if ((st = check_factors(f))) return st;
+    if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(u, 4) || !aligned(ids, 4) ||
+        !aligned(base, 2) || !aligned(dx, 2) || !aligned(da, 2) || !aligned(db, 2))
+        return TRELLIS_ERR_ALIGN;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              trellis_adapters_workspace_bytes(f, rows, 1))))
+        return st;
+    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && aligned(dx, 16);
+    const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, nullptr);
+    return status_of(trellis::launch_adapters_backward(dy, x, u, ids, factors(f), rows, base, dx, da,
+                                                       db, vec_in, vec_out, workspace, stream));
 }
 
 }  // extern "C"

@@ -9,6 +9,7 @@ namespace trellis {
 
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxKeys = kMaxGroups + 1;  // one more for the slots outside every group
+constexpr int kMaxRank = 128;             // of an adapter
 
 // Sort of `slots` ids (route.hip). With `tail`, slots outside [0, groups) form
 // one more group behind the others (offsets then has groups + 2 entries) and
@@ -29,6 +30,25 @@ hipError_t launch_combine(const uint16_t* y, const float* weights, const int32_t
 hipError_t launch_combine_backward(const uint16_t* dout, const uint16_t* y, const float* weights,
                                    const int32_t* position, int tokens, int top_k, int width,
                                    uint16_t* dy, float* dweights, bool vec, hipStream_t st);
+
+// Low-rank adapters (adapters.hip): a [count][rank][in], b [count][rank][out].
+// `vec_in` (`vec_out`): in (out) is a multiple of 8 and every array with rows
+// of that length is 16-byte aligned. `base` may be null (zeros) or y (dx)
+// itself; u may be null in launch_adapters.
+struct AdapterFactors {
+    const uint16_t* a;
+    const uint16_t* b;
+    const float* scales;
+    int in, out, rank, count;
+};
+size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, bool backward);
+hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterFactors& f, int rows,
+                           const uint16_t* base, uint16_t* y, float* u, bool vec_in, bool vec_out,
+                           void* ws, hipStream_t st);
+hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* u,
+                                    const int32_t* ids, const AdapterFactors& f, int rows,
+                                    const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
+                                    bool vec_in, bool vec_out, void* ws, hipStream_t st);
 
 #ifdef __HIP__
 

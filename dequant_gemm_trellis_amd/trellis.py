@@ -44,7 +44,8 @@ EXPORTED = ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_
             "trellis_expand", "trellis_repack", "trellis_strerror", "trellis_gather_probe",
             "trellis_gather_probe_values", "trellis_gather_probe_out_floats", "trellis_route",
             "trellis_route_workspace_bytes", "trellis_dispatch", "trellis_combine",
-            "trellis_combine_backward")
+            "trellis_combine_backward", "trellis_adapters", "trellis_adapters_backward",
+            "trellis_adapters_workspace_bytes")
 PROBE_PAIR_B64, PROBE_COPIES8_B32, PROBE_SINGLE_B32 = 0, 1, 2
 
 
@@ -85,7 +86,19 @@ _lib.trellis_gather_probe_values.argtypes = [C.c_int32, C.c_int32]
 _lib.trellis_gather_probe_values.restype = C.c_uint64
 _lib.trellis_gather_probe_out_floats.argtypes = []
 _lib.trellis_gather_probe_out_floats.restype = C.c_size_t
+class AdapterSet(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scales", C.c_void_p),
+                ("count", C.c_int32), ("rank", C.c_int32), ("in_features", C.c_int32),
+                ("out_features", C.c_int32)]
+
+
+_AP = C.POINTER(AdapterSet)
 _i32 = C.c_int32
+_lib.trellis_adapters.argtypes = [_vp, _vp, _i32, _AP, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
+_lib.trellis_adapters_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _AP, _vp, _vp, _vp, _vp, _vp,
+                                           C.c_size_t, _vp]
+_lib.trellis_adapters_workspace_bytes.argtypes = [_AP, _i32, _i32]
+_lib.trellis_adapters_workspace_bytes.restype = C.c_size_t
 _lib.trellis_route.argtypes = [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
 _lib.trellis_route_workspace_bytes.argtypes = [_i32, _i32, _i32]
 _lib.trellis_route_workspace_bytes.restype = C.c_size_t
@@ -95,7 +108,8 @@ _lib.trellis_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _i32, _i32, 
 for _f in ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_gemv_scatter",
            "trellis_prefill", "trellis_prefill_dual", "trellis_gate_up_swiglu", "trellis_expand",
            "trellis_repack", "trellis_gemv_scatter_static", "trellis_route", "trellis_dispatch",
-           "trellis_combine", "trellis_combine_backward"):
+           "trellis_combine", "trellis_combine_backward", "trellis_adapters",
+           "trellis_adapters_backward"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -433,3 +447,86 @@ def combine_backward(dout, y, weights, route: Route, dy=None, dweights=None,
             _dev(dout), _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width,
             _dev(dy), _dev(dweights), _stream(None)))
     return dy, dweights
+
+
+def _adapter_set(a, b, scales) -> AdapterSet:
+    count, rank, i = _dims("a", a, 3)
+    o = _dims("b", b, 3)[2]
+    _want("a", a, torch.bfloat16, (count, rank, i))
+    _want("b", b, torch.bfloat16, (count, rank, o))
+    _want("scales", scales, torch.float32, (count,))
+    return AdapterSet(a.data_ptr(), b.data_ptr(), scales.data_ptr(), count, rank, i, o)
+
+
+def adapters_workspace_bytes(f: AdapterSet, rows: int, backward: bool) -> int:
+    n = _lib.trellis_adapters_workspace_bytes(C.byref(f), rows, int(backward))
+    if n == C.c_size_t(-1).value:
+        raise TrellisError("trellis_adapters_workspace_bytes", ERR_GEOMETRY)
+    return n
+
+
+def adapters(x, ids, a, b, scales, base=None, y=None, u=None, keep_inner=False, workspace=None,
+             stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(y, u): y = base + scales[i] * b[i]^T (a[i] x) for every row with i = ids[m]
+    in [0, count), and base for the others. x: bf16 [rows, in]; a: bf16 [count,
+    rank, in]; b: bf16 [count, rank, out]; base: bf16 [rows, out] (None: zeros),
+    which y may be. u: float32 [rows, rank] of inner products, None unless given
+    or keep_inner (the backward pass needs it)."""
+    f = _adapter_set(a, b, scales)
+    rows = _dims("x", x, 2)[0]
+    _want("x", x, torch.bfloat16, (rows, f.in_features))
+    _want("ids", ids, torch.int32, (rows,))
+    if base is not None:
+        _want("base", base, torch.bfloat16, (rows, f.out_features))
+    with _on(stream):
+        if y is None:
+            y = torch.empty((rows, f.out_features), dtype=torch.bfloat16, device=x.device)
+        if u is None and keep_inner:
+            u = torch.empty((rows, f.rank), dtype=torch.float32, device=x.device)
+        _want("y", y, torch.bfloat16, (rows, f.out_features))
+        if u is not None:
+            _want("u", u, torch.float32, (rows, f.rank))
+        ws, ws_bytes, keep = _workspace("trellis_adapters", adapters_workspace_bytes(f, rows, False),
+                                        workspace, x.device)
+        same = base is not None and base.data_ptr() == y.data_ptr()
+        _apart({"y": y, "u": u, "workspace": keep},
+               {"x": x, "ids": ids, "a": a, "b": b, "scales": scales, "base": None if same else base})
+        _check("trellis_adapters", _lib.trellis_adapters(
+            _dev(x), _dev(ids), rows, C.byref(f), _dev(base), _dev(y), _dev(u), ws, ws_bytes,
+            _stream(None)))
+    return y, u
+
+
+def adapters_backward(dy, x, u, ids, a, b, scales, base=None, dx=None, da=None, db=None,
+                      workspace=None, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients (dx, da, db) of adapters from dy [rows, out] with the forward
+    pass's u: dx = base + a[i]^T g with g = scales[i] * b[i] dy, da and db whole
+    (zeros for adapters without rows), all bf16. dx may be `base`."""
+    f = _adapter_set(a, b, scales)
+    rows = _dims("x", x, 2)[0]
+    _want("dy", dy, torch.bfloat16, (rows, f.out_features))
+    _want("x", x, torch.bfloat16, (rows, f.in_features))
+    _want("u", u, torch.float32, (rows, f.rank))
+    _want("ids", ids, torch.int32, (rows,))
+    if base is not None:
+        _want("base", base, torch.bfloat16, (rows, f.in_features))
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty_like(x)
+        if da is None:
+            da = torch.empty_like(a)
+        if db is None:
+            db = torch.empty_like(b)
+        _want("dx", dx, torch.bfloat16, (rows, f.in_features))
+        _want("da", da, torch.bfloat16, a.shape)
+        _want("db", db, torch.bfloat16, b.shape)
+        ws, ws_bytes, keep = _workspace("trellis_adapters_backward",
+                                        adapters_workspace_bytes(f, rows, True), workspace, x.device)
+        same = base is not None and base.data_ptr() == dx.data_ptr()
+        _apart({"dx": dx, "da": da, "db": db, "workspace": keep},
+               {"dy": dy, "x": x, "u": u, "ids": ids, "a": a, "b": b, "scales": scales,
+                "base": None if same else base})
+        _check("trellis_adapters_backward", _lib.trellis_adapters_backward(
+            _dev(dy), _dev(x), _dev(u), _dev(ids), rows, C.byref(f), _dev(base), _dev(dx), _dev(da),
+            _dev(db), ws, ws_bytes, _stream(None)))
+    return dx, da, db

@@ -90,6 +90,68 @@ int trellis_combine_backward(const uint16_t *dout, const uint16_t *y, const floa
                              const int32_t *position, int32_t tokens, int32_t top_k,
                              int32_t width, uint16_t *dy, float *dweights, hipStream_t stream);
 
+/* Largest rank of an adapter, and number of rows of one adapter call. */
+#define TRELLIS_MAX_RANK 128
+#define TRELLIS_MAX_ADAPTER_ROWS (1 << 20)
+
+/*
+ * Low-rank adapters of one projection in -> out, all of one rank (smaller ones
+ * are padded with zero rows). Both factors are stored by rank:
+ *   a: bf16 [count][rank][in_features], b: bf16 [count][rank][out_features]
+ *   (the transpose of a matrix [out][rank]); scales: float32 [count].
+ */
+typedef struct trellis_adapter_set {
+    const uint16_t *a;
+    const uint16_t *b;
+    const float *scales;
+    int32_t count;         /* 1 .. TRELLIS_MAX_GROUPS */
+    int32_t rank;          /* 1 .. TRELLIS_MAX_RANK */
+    int32_t in_features;   /* 1 .. 2^19, any */
+    int32_t out_features;  /* 1 .. 2^19, any */
+} trellis_adapter_set;
+
+/*
+ * Every row's own adapter beside a projection that all rows share. With
+ * i = ids[m] (int32 [rows]):
+ *   u[m] = a[i] x[m],   y[m] = bf16( base[m] + scales[i] * b[i]^T u[m] )
+ * and y[m] = base[m], u[m] = 0 for rows whose id is outside [0, count).
+ * x: bf16 [rows][in]; base: bf16 [rows][out], the shared projection's output
+ * (trellis_prefill or trellis_gemv of x), or null for zeros; y: bf16
+ * [rows][out], which may be `base` itself (rows without an adapter are then
+ * not touched); u: float32 [rows][rank], kept for the backward pass, or null.
+ * u and the sum are float32; up to 64 rows every product is a float32 one,
+ * beyond that u enters the second product as two bf16 parts (an error of at
+ * most 2^-16 of it). workspace: 16-byte aligned, at least
+ * trellis_adapters_workspace_bytes(f, rows, 0) bytes.
+ */
+int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
+                     const trellis_adapter_set *f, const uint16_t *base, uint16_t *y, float *u,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradients of trellis_adapters from dy: bf16 [rows][out], with x, ids and the
+ * forward pass's u:
+ *   g[m]  = scales[i] * b[i] dy[m]
+ *   dx[m] = bf16( base[m] + a[i]^T g[m] )     (base[m] without an adapter)
+ *   da[i] = bf16( sum over the rows m of adapter i of g[m] x[m]^T )
+ *   db[i] = bf16( sum over the same rows of scales[i] * u[m] dy[m]^T )
+ * base: bf16 [rows][in], the shared projection's own gradient (the product of
+ * dy with the same codes on the other axis), or null for zeros; dx may be
+ * `base` itself. da and db have the factors' layout and are written whole:
+ * zeros for adapters without rows (also for rows = 0). Sums run in float32; g
+ * and u enter the second products as two bf16 parts. workspace: 16-byte
+ * aligned, at least trellis_adapters_workspace_bytes(f, rows, 1) bytes.
+ */
+int trellis_adapters_backward(const uint16_t *dy, const uint16_t *x, const float *u,
+                              const int32_t *ids, int32_t rows, const trellis_adapter_set *f,
+                              const uint16_t *base, uint16_t *dx, uint16_t *da, uint16_t *db,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of trellis_adapters (backward = 0) or of its gradient; only
+ * the sizes in f are read. (size_t)-1 if they are not supported. */
+size_t trellis_adapters_workspace_bytes(const trellis_adapter_set *f, int32_t rows,
+                                        int32_t backward);
+
 #ifdef __cplusplus
 }
 #endif

@@ -121,3 +121,77 @@ def test_overlap_check(T):
         T._apart({"dy": a, "dw": a[63:]}, {})
     T._apart({"out": a[:0]}, {"x": a})                # nothing written
     T._apart({"out": a[:8]}, {"x": a[16:], "y": a[16:]})  # inputs may share
+
+
+ADAPTERS = {
+    "trellis_adapters": ("x", "ids", "#rows", "set", "base", "y", "u", "ws", "#ws_bytes"),
+    "trellis_adapters_backward": ("dy", "x", "u", "ids", "#rows", "set", "base", "dx", "da", "db",
+                                  "ws", "#ws_bytes"),
+}
+
+
+@pytest.mark.parametrize("name", sorted(ADAPTERS))
+def test_adapters_validation(T, name):
+    order, backward = ADAPTERS[name], name.endswith("backward")
+    f = T.AdapterSet(FAKE, FAKE, FAKE, 4, 16, 256, 300)
+    need = T.adapters_workspace_bytes(f, 100, backward)
+    args = {n.lstrip("#"): FAKE for n in order} | dict(rows=100, ws_bytes=need)
+
+    def apply(f=f, **kw):
+        a = dict(args, **kw)
+        return getattr(T.raw(), name)(*[
+            a[n[1:]] if n[0] == "#" else (C.byref(f) if f is not None else None) if n == "set"
+            else C.c_void_p(a[n]) for n in order], C.c_void_p(0))
+
+    def other(**kw):
+        g = T.AdapterSet(FAKE, FAKE, FAKE, 4, 16, 256, 300)
+        for k, v in kw.items():
+            setattr(g, k, v)
+        return g
+
+    assert apply(None) == T.ERR_NULL
+    for kw in (dict(count=0), dict(count=1025), dict(rank=0), dict(rank=129), dict(in_features=0),
+               dict(in_features=(1 << 19) + 1), dict(out_features=0),
+               dict(out_features=(1 << 19) + 1)):
+        assert apply(other(**kw)) == T.ERR_GEOMETRY, kw
+        assert T.raw().trellis_adapters_workspace_bytes(C.byref(other(**kw)), 100, backward) == \
+            C.c_size_t(-1).value
+    for rows in (-1, (1 << 20) + 1):
+        assert apply(rows=rows) == T.ERR_GEOMETRY
+    for kw in (dict(a=0), dict(b=0), dict(scales=0)):
+        assert apply(other(**kw)) == T.ERR_NULL, kw
+    for kw in (dict(a=FAKE + 1), dict(b=FAKE + 1), dict(scales=FAKE + 2)):
+        assert apply(other(**kw)) == T.ERR_ALIGN, kw
+    for arg in order:
+        if arg[0] == "#" or arg in ("set", "ws"):
+            continue
+        if arg not in ("base",) and not (arg == "u" and not backward):
+            assert apply(**{arg: 0}) == T.ERR_NULL, arg
+        assert apply(**{arg: FAKE + 1}) == T.ERR_ALIGN, arg
+    assert apply(ws=FAKE + 8) == T.ERR_ALIGN
+    assert apply(ws=0) == T.ERR_WORKSPACE
+    assert apply(ws_bytes=need - 1) == T.ERR_WORKSPACE
+    if not backward:
+        assert apply(rows=0, x=0, ids=0, y=0) == T.OK  # nothing to do, nothing enqueued
+
+
+def test_adapters_workspace_stays_small(T):
+    """The gradient's float32 sums are kept for adapters of over 1024 rows only:
+    many adapters of a wide projection do not multiply the workspace."""
+    f = T.AdapterSet(0, 0, 0, 1024, 64, 5120, 17408)
+    assert T.adapters_workspace_bytes(f, 1000, True) < 1 << 30
+    few = T.AdapterSet(0, 0, 0, 2, 64, 5120, 17408)
+    shared = 2 * 4 * 64 * 17408 * 4  # at 4096 rows: at most 8 segments
+    assert shared < T.adapters_workspace_bytes(few, 4096, True) < 3 * shared
+
+
+def test_binding_refuses_mismatched_adapters(T):
+    x, ids = torch.zeros((3, 8), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    a, b = torch.zeros((2, 4, 8), dtype=torch.bfloat16), torch.zeros((2, 5, 6), dtype=torch.bfloat16)
+    s = torch.ones(2)
+    with pytest.raises(ValueError, match="a: device tensors"):
+        T.adapters(x, ids, a, b, s)
+    with pytest.raises(ValueError, match="a: expected"):
+        T.adapters(x, ids, a.float(), b, s)
+    with pytest.raises(ValueError, match="3 dimensions"):
+        T.adapters(x, ids, a[0], b, s)
