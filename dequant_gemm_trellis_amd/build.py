@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtrellis.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["gemv.hip", "axis1.hip", "axis0.hip", "layout.hip", "probe.hip", "route.hip", "adapters.hip",
+SOURCES = ["gemv.hip", "axis1.hip", "axis0.hip", "layout.hip", "probe.hip", "route.hip", "adapters.hip", "experts.hip",
            "api.cpp", "api_grouped.cpp"]
 ARCH = "gfx950"
 

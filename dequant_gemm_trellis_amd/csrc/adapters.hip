@@ -30,79 +30,10 @@
 namespace trellis {
 namespace {
 
-constexpr int kTileRows = 64;          // rows per tile: four 16-row operands
 constexpr int kSubs = kTileRows / 16;
 constexpr int kWgThreads = 256;
 constexpr int kWgWaves = kWgThreads / kWave;
 constexpr int kStrip = 128;            // columns per wave: 16 lanes x 8
-
-// The place of tile (or segment) t in a list that holds, group by group,
-// ceil(rows of the group / per) entries. Each wave searches for itself, 64
-// groups at a time; with `at_least_one` a group without rows has one entry.
-struct Found {
-    int group;   // -1: past the end
-    int index;   // entry within its group
-    int first;   // the group's first place, and the place after its last
-    int end;
-    int tiles;   // tiles of kTileRows rows of the groups before
-    int shared;  // entries of those groups before that have more than one
-};
-
-__device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets, int groups, int rows,
-                                            int per, bool at_least_one, int t) {
-    const int lane = threadIdx.x & 63;
-    int before = 0, tiles = 0, shared = 0;
-    for (int g0 = 0; g0 < groups; g0 += 64) {
-        const int g = g0 + lane;
-        int first = 0, end = 0, n = 0, nt = 0;
-        if (g < groups) {
-            first = min(max(offsets[g], 0), rows);
-            end = min(max(offsets[g + 1], first), rows);
-            n = (end - first + per - 1) / per;
-            if (at_least_one && n == 0) n = 1;
-            nt = (end - first + kTileRows - 1) / kTileRows;
-        }
-        const int ns = n > 1 ? n : 0;
-        int inc = n, tinc = nt, sinc = ns;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int a = __shfl_up(inc, d), b = __shfl_up(tinc, d), e = __shfl_up(sinc, d);
-            if (lane >= d) {
-                inc += a;
-                tinc += b;
-                sinc += e;
-            }
-        }
-        const uint64_t past = __ballot(before + inc > t);
-        if (past) {
-            const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
-            return {g0 + l, t - before - __shfl(inc - n, l), __shfl(first, l), __shfl(end, l),
-                    tiles + __shfl(tinc - nt, l), shared + __shfl(sinc - ns, l)};
-        }
-        before += __shfl(inc, 63);
-        tiles += __shfl(tinc, 63);
-        shared += __shfl(sinc, 63);
-    }
-    return {-1, 0, 0, 0, 0, 0};
-}
-
-// 8 values of a row from column `col` on, zeros past `width` and where !live.
-// VEC: rows are multiples of 8 values and 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ row, int col, int width, bool live) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-        if (live && col < width) v = *reinterpret_cast<const u32x4*>(row + col);
-    } else {
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const uint32_t lo = live && col + 2 * d < width ? row[col + 2 * d] : 0u;
-            const uint32_t hi = live && col + 2 * d + 1 < width ? row[col + 2 * d + 1] : 0u;
-            v[d] = lo | (hi << 16);
-        }
-    }
-    return v;
-}
 
 template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t* __restrict__ row, int col, int width, u32x4 v) {

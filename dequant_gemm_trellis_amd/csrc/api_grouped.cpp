@@ -173,4 +173,31 @@ int trellis_adapters_backward(const uint16_t* dy, const uint16_t* x, const float
                                                        db, vec_in, vec_out, workspace, stream));
 }
 
+size_t trellis_experts_workspace_bytes(const trellis_geometry* g, int32_t rows, int32_t experts) {
+    trellis::Dims d;
+    if (trellis::check_geometry(g, &d) || check_groups(experts) || check_slots(rows, 1))
+        return static_cast<size_t>(-1);
+    return rows ? trellis::experts_workspace_bytes(g->axis, g->in_features, rows, experts) : 0;
+}
+
+int trellis_experts(const uint16_t* x, int32_t rows, const int32_t* offsets, int32_t experts,
+                    const uint32_t* codes, const float* scales, const float* lut,
+                    const trellis_geometry* g, uint16_t* y, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+    trellis::Dims d;
+    int st = trellis::check_geometry(g, &d);
+    if (st || (st = check_groups(experts)) || (st = check_slots(rows, 1))) return st;
+    if (rows == 0) return TRELLIS_OK;
+    if (!offsets) return TRELLIS_ERR_NULL;
+    if ((st = trellis::check_operands(codes, scales, lut)) || (st = trellis::check_io(x, y))) return st;
+    if (!aligned(offsets, 4)) return TRELLIS_ERR_ALIGN;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              trellis_experts_workspace_bytes(g, rows, experts))))
+        return st;
+    const size_t words = static_cast<size_t>(d.rows) * d.nb * 8 * g->k;
+    const trellis::ExpertWeights w{codes,  scales, lut, d.lay, words, g->axis, g->k,
+                                   g->in_features, g->out_features, experts};
+    return status_of(trellis::launch_experts(x, rows, offsets, w, y, workspace, stream));
+}
+
 }  // extern "C"

@@ -5,11 +5,14 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include "launch.hpp"
+
 namespace trellis {
 
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxKeys = kMaxGroups + 1;  // one more for the slots outside every group
 constexpr int kMaxRank = 128;             // of an adapter
+constexpr int kTileRows = 64;             // rows of an adapter's tile: four 16-row operands
 
 // Sort of `slots` ids (route.hip). With `tail`, slots outside [0, groups) form
 // one more group behind the others (offsets then has groups + 2 entries) and
@@ -50,6 +53,20 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                                     const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                                     bool vec_in, bool vec_out, void* ws, hipStream_t st);
 
+// The experts' coded products (experts.hip): y[s] = W_e x[s] for the rows s of
+// [offsets[e], offsets[e + 1]). Codes [experts] of `lay`, each `words` words.
+struct ExpertWeights {
+    const uint32_t* codes;
+    const float* scales;  // [experts][stored rows]
+    const float* lut;
+    CodeLayout lay;
+    size_t words;
+    int axis, k, in, out, experts;
+};
+size_t experts_workspace_bytes(int axis, int in, int rows, int experts);
+hipError_t launch_experts(const uint16_t* x, int rows, const int32_t* offsets,
+                          const ExpertWeights& w, uint16_t* y, void* ws, hipStream_t st);
+
 #ifdef __HIP__
 
 // The float32 values of the low and the high bf16 of a word.
@@ -60,6 +77,74 @@ __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     floatx2 p = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+}
+
+// The place of tile (or segment) t in a list that holds, group by group,
+// ceil(rows of the group / per) entries. Each wave searches for itself, 64
+// groups at a time; with `at_least_one` a group without rows has one entry.
+struct Found {
+    int group;   // -1: past the end
+    int index;   // entry within its group
+    int first;   // the group's first place, and the place after its last
+    int end;
+    int tiles;   // tiles of kTileRows rows of the groups before
+    int shared;  // entries of those groups before that have more than one
+};
+
+__device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets, int groups, int rows,
+                                            int per, bool at_least_one, int t) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, tiles = 0, shared = 0;
+    for (int g0 = 0; g0 < groups; g0 += 64) {
+        const int g = g0 + lane;
+        int first = 0, end = 0, n = 0, nt = 0;
+        if (g < groups) {
+            first = min(max(offsets[g], 0), rows);
+            end = min(max(offsets[g + 1], first), rows);
+            n = (end - first + per - 1) / per;
+            if (at_least_one && n == 0) n = 1;
+            nt = (end - first + kTileRows - 1) / kTileRows;
+        }
+        const int ns = n > 1 ? n : 0;
+        int inc = n, tinc = nt, sinc = ns;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int a = __shfl_up(inc, d), b = __shfl_up(tinc, d), e = __shfl_up(sinc, d);
+            if (lane >= d) {
+                inc += a;
+                tinc += b;
+                sinc += e;
+            }
+        }
+        const uint64_t past = __ballot(before + inc > t);
+        if (past) {
+            const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
+            return {g0 + l, t - before - __shfl(inc - n, l), __shfl(first, l), __shfl(end, l),
+                    tiles + __shfl(tinc - nt, l), shared + __shfl(sinc - ns, l)};
+        }
+        before += __shfl(inc, 63);
+        tiles += __shfl(tinc, 63);
+        shared += __shfl(sinc, 63);
+    }
+    return {-1, 0, 0, 0, 0, 0};
+}
+
+// 8 values of a row from column `col` on, zeros past `width` and where !live.
+// VEC: rows are multiples of 8 values and 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ row, int col, int width, bool live) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+        if (live && col < width) v = *reinterpret_cast<const u32x4*>(row + col);
+    } else {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t lo = live && col + 2 * d < width ? row[col + 2 * d] : 0u;
+            const uint32_t hi = live && col + 2 * d + 1 < width ? row[col + 2 * d + 1] : 0u;
+            v[d] = lo | (hi << 16);
+        }
+    }
+    return v;
 }
 
 #endif  // __HIP__

@@ -45,7 +45,8 @@ EXPORTED = ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_
             "trellis_gather_probe_values", "trellis_gather_probe_out_floats", "trellis_route",
             "trellis_route_workspace_bytes", "trellis_dispatch", "trellis_combine",
             "trellis_combine_backward", "trellis_adapters", "trellis_adapters_backward",
-            "trellis_adapters_workspace_bytes")
+            "trellis_adapters_workspace_bytes", "trellis_experts",
+            "trellis_experts_workspace_bytes")
 PROBE_PAIR_B64, PROBE_COPIES8_B32, PROBE_SINGLE_B32 = 0, 1, 2
 
 
@@ -99,6 +100,9 @@ _lib.trellis_adapters_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _AP, _vp, _
                                            C.c_size_t, _vp]
 _lib.trellis_adapters_workspace_bytes.argtypes = [_AP, _i32, _i32]
 _lib.trellis_adapters_workspace_bytes.restype = C.c_size_t
+_lib.trellis_experts.argtypes = [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _GP, _vp, _vp, C.c_size_t, _vp]
+_lib.trellis_experts_workspace_bytes.argtypes = [_GP, _i32, _i32]
+_lib.trellis_experts_workspace_bytes.restype = C.c_size_t
 _lib.trellis_route.argtypes = [_vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
 _lib.trellis_route_workspace_bytes.argtypes = [_i32, _i32, _i32]
 _lib.trellis_route_workspace_bytes.restype = C.c_size_t
@@ -109,7 +113,7 @@ for _f in ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_g
            "trellis_prefill", "trellis_prefill_dual", "trellis_gate_up_swiglu", "trellis_expand",
            "trellis_repack", "trellis_gemv_scatter_static", "trellis_route", "trellis_dispatch",
            "trellis_combine", "trellis_combine_backward", "trellis_adapters",
-           "trellis_adapters_backward"):
+           "trellis_adapters_backward", "trellis_experts"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -447,6 +451,41 @@ def combine_backward(dout, y, weights, route: Route, dy=None, dweights=None,
             _dev(dout), _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width,
             _dev(dy), _dev(dweights), _stream(None)))
     return dy, dweights
+
+
+def experts(x, offsets, codes, scales, lut, g, y=None, workspace=None, stream=None) -> torch.Tensor:
+    """y [rows, out]: every row of x [rows, in] times the weights of its expert,
+    rows [offsets[e], offsets[e + 1]) being expert e's (Route.offsets). codes:
+    int32 [experts, ...], each expert's as for prefill with geometry g; scales:
+    float32 [experts, stored rows]; lut: float32 [4096], shared. Rows of `y`
+    outside every expert are left as they were. The gradient with respect to x
+    is the same call with the geometry's axis flipped and in/out exchanged."""
+    geom = _geom(g)
+    rows = _dims("x", x, 2)[0]
+    n = _dims("offsets", offsets, 1)[0] - 1
+    stored, cols = ((geom.out_features, geom.in_features) if geom.axis == 1
+                    else (geom.in_features, geom.out_features))
+    _want("x", x, torch.bfloat16, (rows, geom.in_features))
+    _want("offsets", offsets, torch.int32, (n + 1,))
+    _want("scales", scales, torch.float32, (n, stored))
+    _want("lut", lut, torch.float32, (1 << 12,))
+    _want("codes", codes, torch.int32, codes.shape)
+    if codes.dim() < 1 or codes.shape[0] != n or codes.numel() != n * stored * cols * geom.k // 32:
+        raise ValueError(f"codes: expected {n} experts of {stored} x {cols} weights of {geom.k} "
+                         f"bits, got {tuple(codes.shape)}")
+    with _on(stream):
+        if y is None:
+            y = torch.empty((rows, geom.out_features), dtype=torch.bfloat16, device=x.device)
+        _want("y", y, torch.bfloat16, (rows, geom.out_features))
+        fn = "trellis_experts"
+        nbytes = _lib.trellis_experts_workspace_bytes(C.byref(geom), rows, n)
+        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, x.device)
+        _apart({"y": y, "workspace": keep},
+               {"x": x, "offsets": offsets, "codes": codes, "scales": scales, "lut": lut})
+        _check(fn, _lib.trellis_experts(_dev(x), rows, _dev(offsets), n, _dev(codes), _dev(scales),
+                                        _dev(lut), C.byref(geom), _dev(y), ws, ws_bytes,
+                                        _stream(None)))
+    return y
 
 
 def _adapter_set(a, b, scales) -> AdapterSet:

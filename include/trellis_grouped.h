@@ -90,6 +90,30 @@ int trellis_combine_backward(const uint16_t *dout, const uint16_t *y, const floa
                              const int32_t *position, int32_t tokens, int32_t top_k,
                              int32_t width, uint16_t *dy, float *dweights, hipStream_t stream);
 
+/*
+ * The experts' products over rows sorted by expert (trellis_dispatch):
+ *   y[s] = bf16( W_e x[s] )  for the rows s of [offsets[e], offsets[e + 1]),
+ * with W_e decoded as in trellis_prefill (axis 1: y = x W^T, axis 0: y = x W;
+ * the product of one axis is the gradient with respect to x of the other's,
+ * with the same codes, scales and codebook and in/out exchanged).
+ * x: bf16 [rows][in]; offsets: int32 [experts + 1] of trellis_route, on the
+ * device; codes: uint32 [experts][...], every expert's in the layout of `g`
+ * (g describes one expert); scales: float32 [experts][stored rows]; lut:
+ * float32 [4096], shared by the experts; y: bf16 [rows][out], whose rows
+ * outside every expert are left as they were. Offsets are taken as ascending
+ * and clamped to [0, rows]. rows <= TRELLIS_MAX_SLOTS. x, codes, lut and y
+ * need 16-byte alignment. workspace: 16-byte aligned, at least
+ * trellis_experts_workspace_bytes(g, rows, experts) bytes (0 for few rows per
+ * expert and on axis 0: may be null then).
+ */
+int trellis_experts(const uint16_t *x, int32_t rows, const int32_t *offsets, int32_t experts,
+                    const uint32_t *codes, const float *scales, const float *lut,
+                    const trellis_geometry *g, uint16_t *y, void *workspace,
+                    size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of trellis_experts; (size_t)-1 if the sizes are not supported. */
+size_t trellis_experts_workspace_bytes(const trellis_geometry *g, int32_t rows, int32_t experts);
+
 /* Largest rank of an adapter, and number of rows of one adapter call. */
 #define TRELLIS_MAX_RANK 128
 #define TRELLIS_MAX_ADAPTER_ROWS (1 << 20)

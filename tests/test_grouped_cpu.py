@@ -195,3 +195,38 @@ def test_binding_refuses_mismatched_adapters(T):
         T.adapters(x, ids, a.float(), b, s)
     with pytest.raises(ValueError, match="3 dimensions"):
         T.adapters(x, ids, a[0], b, s)
+
+
+EXPERTS = ("x", "#rows", "offsets", "#experts", "codes", "scales", "lut", "geom", "y", "ws",
+           "#ws_bytes")
+
+
+@pytest.mark.parametrize("axis", [0, 1])
+def test_experts_validation(T, axis):
+    g = T.Geometry(axis, 256, 12, 3, 512, 256, 0)
+    need = T.raw().trellis_experts_workspace_bytes(C.byref(g), 1000, 4)
+    assert (need > 0) == (axis == 1)
+    args = dict(x=FAKE, rows=1000, offsets=FAKE, experts=4, codes=FAKE, scales=FAKE, lut=FAKE,
+                y=FAKE, ws=FAKE, ws_bytes=need)
+
+    def experts(g=g, **kw):
+        a = dict(args, **kw)
+        return T.raw().trellis_experts(*[
+            a[n[1:]] if n[0] == "#" else (C.byref(g) if g is not None else None) if n == "geom"
+            else C.c_void_p(a[n]) for n in EXPERTS], C.c_void_p(0))
+
+    assert experts(None) == T.ERR_NULL
+    for bad in (T.Geometry(2, 256, 12, 3, 512, 256, 0), T.Geometry(axis, 256, 12, 5, 512, 256, 0),
+                T.Geometry(axis, 256, 12, 3, 0, 256, 0), T.Geometry(axis, 256, 12, 3, 300, 300, 0)):
+        assert experts(bad) == T.ERR_GEOMETRY
+        assert T.raw().trellis_experts_workspace_bytes(C.byref(bad), 10, 4) == C.c_size_t(-1).value
+    for kw in (dict(rows=-1), dict(rows=(1 << 24) + 1), dict(experts=0), dict(experts=1025)):
+        assert experts(**kw) == T.ERR_GEOMETRY, kw
+    for arg in ("x", "offsets", "codes", "scales", "lut", "y"):
+        assert experts(**{arg: 0}) == T.ERR_NULL, arg
+        assert experts(**{arg: FAKE + 2}) == T.ERR_ALIGN, arg
+    assert experts(ws=FAKE + 8) == T.ERR_ALIGN
+    if need:
+        assert experts(ws=0) == T.ERR_WORKSPACE
+        assert experts(ws_bytes=need - 1) == T.ERR_WORKSPACE
+    assert experts(rows=0, x=0, y=0) == T.OK  # nothing to do, nothing enqueued
