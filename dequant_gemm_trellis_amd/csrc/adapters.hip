@@ -100,48 +100,69 @@ __global__ __launch_bounds__(kWgThreads) void direct_inner_kernel(
     }
 }
 
-// y[m] = base[m] + s u[m] B. Each workgroup sums u[m] from the splits (ascending),
-// then its 2048 columns; the first one writes u. Grid: (column chunks, rows).
+// y[m] = base[m] + s u[m] B over 512 columns: wave w sums u[m][r] from the
+// splits for its ranks r = w, w + 4, ... (lanes over splits, then a fixed tree),
+// multiplies, and the four waves' sums meet in LDS in wave order. The first
+// workgroup of a row writes u. Grid: (column chunks, rows).
 template <bool VEC>
 __global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
     const float* __restrict__ partial, int splits, const int32_t* __restrict__ ids,
     const uint16_t* __restrict__ factor, const float* __restrict__ scales, int width, int rank,
     int count, const uint16_t* base, uint16_t* y, float* __restrict__ u) {
-    __shared__ float us[kMaxRank];
-    const int m = blockIdx.y, tid = threadIdx.x, rows = gridDim.y;
+    __shared__ float sums[kWgWaves][8][kWave];
+    const int m = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rows = gridDim.y;
     const int a = ids[m];
     const bool has = static_cast<uint32_t>(a) < static_cast<uint32_t>(count);
-    const int col = (blockIdx.x * kWgThreads + tid) * 8;
+    const int col = blockIdx.x * kDirectCols + 8 * lane;
     const uint16_t* brow = base + static_cast<size_t>(m) * width;
     uint16_t* yrow = y + static_cast<size_t>(m) * width;
     if (!has) {
         if (u && blockIdx.x == 0)
-            for (int r = tid; r < rank; r += kWgThreads) u[static_cast<size_t>(m) * rank + r] = 0.f;
-        if (base != y && col < width) store8<VEC>(yrow, col, width, load8<VEC>(brow, col, width, base != nullptr));
+            for (int r = threadIdx.x; r < rank; r += kWgThreads) u[static_cast<size_t>(m) * rank + r] = 0.f;
+        if (base != y && wave == 0)
+            store8<VEC>(yrow, col, width, load8<VEC>(brow, col, width, base != nullptr));
         return;
     }
-    const u32x4 b = load8<VEC>(brow, col, width, base != nullptr);
-    for (int r = tid; r < rank; r += kWgThreads) {
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k) s += partial[(static_cast<size_t>(k) * rows + m) * rank + r];
-        if (u && blockIdx.x == 0) u[static_cast<size_t>(m) * rank + r] = s;
-        us[r] = s * scales[a];
-    }
-    __syncthreads();
-    if (col >= width) return;
+    const float scale = scales[a];
     const uint16_t* f = factor + static_cast<size_t>(a) * rank * width;
+    u32x4 b = {0u, 0u, 0u, 0u};
+    if (wave == 0) b = load8<VEC>(brow, col, width, base != nullptr);
     float acc[8] = {};
-#pragma unroll 8
-    for (int r = 0; r < rank; ++r) {
-        const u32x4 w = load8<VEC>(f + static_cast<size_t>(r) * width, col, width, true);
-        const float ur = us[r];
+    // kRanks of a wave's ranks at a time: their loads are in flight together
+    constexpr int kRanks = 4;
+    for (int r0 = wave; r0 < rank; r0 += kRanks * kWgWaves) {
+        u32x4 w[kRanks];
+        float s[kRanks];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            acc[2 * d] = fmaf(ur, bf16_low(w[d]), acc[2 * d]);
-            acc[2 * d + 1] = fmaf(ur, bf16_high(w[d]), acc[2 * d + 1]);
+        for (int i = 0; i < kRanks; ++i) {
+            const int r = r0 + i * kWgWaves;
+            w[i] = load8<VEC>(f + static_cast<size_t>(min(r, rank - 1)) * width, col, width, r < rank);
+            s[i] = 0.f;
+            for (int k = lane; r < rank && k < splits; k += kWave)
+                s[i] += partial[(static_cast<size_t>(k) * rows + m) * rank + r];
+        }
+#pragma unroll
+        for (int i = 0; i < kRanks; ++i) {
+            const int r = r0 + i * kWgWaves;
+#pragma unroll
+            for (int d = 32; d; d >>= 1) s[i] += __shfl_xor(s[i], d);
+            if (u && blockIdx.x == 0 && lane == 0 && r < rank) u[static_cast<size_t>(m) * rank + r] = s[i];
+            const float us = s[i] * scale;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                acc[2 * d] = r < rank ? fmaf(us, bf16_low(w[i][d]), acc[2 * d]) : acc[2 * d];
+                acc[2 * d + 1] = r < rank ? fmaf(us, bf16_high(w[i][d]), acc[2 * d + 1]) : acc[2 * d + 1];
+            }
         }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave][e][lane] = acc[e];
+    __syncthreads();
+    if (wave) return;
     u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        acc[e] = ((sums[0][e][lane] + sums[1][e][lane]) + sums[2][e][lane]) + sums[3][e][lane];
 #pragma unroll
     for (int d = 0; d < 4; ++d)
         o[d] = pack_bf16(bf16_low(b[d]) + acc[2 * d], bf16_high(b[d]) + acc[2 * d + 1]);
@@ -151,8 +172,8 @@ __global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
 // ---- many rows ----------------------------------------------------------------
 
 // partial[split][tile][64][16 R]: this split's columns of the tile's inner
-// products. The four waves take the split's 32-column steps in turn and are
-// summed in wave order. Grid: (splits, tiles).
+// products. The four waves take the split's 64-column steps (a 128-byte line of
+// each row) in turn and are summed in wave order. Grid: (splits, tiles).
 template <int R, bool VEC>
 __global__ __launch_bounds__(kWgThreads) void inner_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets,
@@ -174,18 +195,22 @@ __global__ __launch_bounds__(kWgThreads) void inner_kernel(
     for (int s = 0; s < R; ++s) fr[s] = f + static_cast<size_t>(min(16 * s + j, rank - 1)) * width;
     floatx4 acc[kSubs][R] = {};
     const int k0 = blockIdx.x * split_cols, k1 = min(width, k0 + split_cols);
-#pragma unroll 2
-    for (int k = k0 + 32 * wave; k < k1; k += 32 * kWgWaves) {
-        u32x4 xv[kSubs], fv[R];
+    for (int k = k0 + 64 * wave; k < k1; k += 64 * kWgWaves) {
+        u32x4 xv[2][kSubs], fv[2][R];
 #pragma unroll
-        for (int s = 0; s < kSubs; ++s) xv[s] = load8<VEC>(xr[s], k + 8 * c, k1, true);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int s = 0; s < R; ++s) fv[s] = load8<VEC>(fr[s], k + 8 * c, k1, true);
+            for (int s = 0; s < kSubs; ++s) xv[h][s] = load8<VEC>(xr[s], k + 32 * h + 8 * c, k1, true);
 #pragma unroll
-        for (int s = 0; s < kSubs; ++s)
+            for (int s = 0; s < R; ++s) fv[h][s] = load8<VEC>(fr[s], k + 32 * h + 8 * c, k1, true);
+        }
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                acc[s][r] = mfma16x16x32(as_bf16x8(xv[s]), as_bf16x8(fv[r]), acc[s][r]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[s][r] = mfma16x16x32(as_bf16x8(xv[h][s]), as_bf16x8(fv[h][r]), acc[s][r]);
     }
     for (int w = 0; w < kWgWaves; ++w) {
         if (wave == w) {
@@ -213,61 +238,77 @@ struct TileInfo {
     int32_t rows;
 };
 
-// One workgroup per tile: its rows' numbers and group, the inner products from
-// the splits (ascending), and their operand forms.
+// A tile's row numbers and group, its inner products summed from the splits
+// (ascending), and their operand forms; a thread per row and rank.
 //   by_row [tile][64][R][hi 16 | lo 16]    (expand; scaled)
 //   by_rank[tile][R][hi | lo][16][64]      (outer; scaled)
 //   u_rank                                 the same of the forward pass's u
 // Rows past the tile's last and ranks past the last are zeros there.
+// Grid: (tiles, 4 r16): 256 of the tile's 64 x 16 r16 values each.
 __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const float* __restrict__ partial, int splits, int tiles, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ order, const float* __restrict__ scales, int rows, int rank, int r16,
     int count, TileInfo* __restrict__ info, int32_t* __restrict__ tile_rows,
     uint16_t* __restrict__ by_row, uint16_t* __restrict__ by_rank, float* __restrict__ u_out,
     const float* __restrict__ u_in, uint16_t* __restrict__ u_rank) {
-    const int t = blockIdx.x, tid = threadIdx.x;
+    const int t = blockIdx.x, ranks = 16 * r16;
+    const int i = blockIdx.y * kWgThreads + threadIdx.x;
+    const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
     const Found at = find_entry(offsets, count + 1, rows, kTileRows, false, t);
     const int p0 = at.first + at.index * kTileRows;
     const int n = at.group < 0 ? 0 : min(kTileRows, at.end - p0);
-    if (tid == 0) info[t] = {at.group, n};
+    if (i == 0) info[t] = {at.group, n};
     if (at.group < 0) return;
-    if (tid < kTileRows) tile_rows[t * kTileRows + tid] = tid < n ? order[p0 + tid] : -1;
-    const int ranks = 16 * r16;
+    const int orig = row < n ? order[p0 + row] : -1;
+    if (r == 0) tile_rows[t * kTileRows + row] = orig;
+    const bool live = row < n && r < rank;
+    const size_t u_at = static_cast<size_t>(max(orig, 0)) * rank + r;
     if (at.group == count) {
-        if (u_out)
-            for (int i = tid; i < n * rank; i += kWgThreads)
-                u_out[static_cast<size_t>(order[p0 + i / rank]) * rank + i % rank] = 0.f;
+        if (u_out && live) u_out[u_at] = 0.f;
         return;
     }
     const float scale = scales[at.group];
-    for (int i = tid; i < kTileRows * ranks; i += kWgThreads) {
-        const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
-        const bool live = row < n && r < rank;
-        const size_t orig = live ? order[p0 + row] : 0;
-        const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * 2 * 16 + rr) * kTileRows + row;
-        float v = 0.f;
-        if (live)
-            for (int k = 0; k < splits; ++k)
-                v += partial[(static_cast<size_t>(k) * tiles + t) * (kTileRows * ranks) + i];
-        if (u_out && live) u_out[orig * rank + r] = v;
-        const float w = v * scale, hi = part_high(w), lo = part_low(w, hi);
-        uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * 32 + rr;
-        q[0] = round_bf16(hi);
-        q[16] = round_bf16(lo);
-        if (by_rank) {
-            by_rank[rank_at] = round_bf16(hi);
-            by_rank[rank_at + 16 * kTileRows] = round_bf16(lo);
-            const float uw = live ? u_in[orig * rank + r] * scale : 0.f;
-            const float uh = part_high(uw), ul = part_low(uw, uh);
-            u_rank[rank_at] = round_bf16(uh);
-            u_rank[rank_at + 16 * kTileRows] = round_bf16(ul);
-        }
+    float v = 0.f;
+    if (live) {
+        const float* p = partial + static_cast<size_t>(t) * (kTileRows * ranks) + i;
+        const size_t step = static_cast<size_t>(tiles) * (kTileRows * ranks);
+#pragma unroll 8
+        for (int k = 0; k < splits; ++k) v += p[k * step];
+        if (u_out) u_out[u_at] = v;
     }
+    const float w = v * scale, hi = part_high(w), lo = part_low(w, hi);
+    uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * 32 + rr;
+    q[0] = round_bf16(hi);
+    q[16] = round_bf16(lo);
+    if (!by_rank) return;
+    const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * 2 * 16 + rr) * kTileRows + row;
+    by_rank[rank_at] = round_bf16(hi);
+    by_rank[rank_at + 16 * kTileRows] = round_bf16(lo);
+    const float uw = live ? u_in[u_at] * scale : 0.f;
+    const float uh = part_high(uw), ul = part_low(uw, uh);
+    u_rank[rank_at] = round_bf16(uh);
+    u_rank[rank_at + 16 * kTileRows] = round_bf16(ul);
 }
 
-// y[row] = base[row] + (scaled rank-long row) * factor. A wave takes 128
-// columns of a tile, two 16-row operands at a time. Grid: (column chunks, tiles).
+// The eight operands (column 8 j + q each) of 16 ranks of a factor's strip:
+// lanes c and c + 2 hold the ranks of the hi and of the lo parts alike.
 template <bool VEC>
+__device__ __forceinline__ void factor_operands(const uint16_t* f, int r, int rank, int col, int width,
+                                                int c, u32x4 (&op)[8]) {
+    u32x4 patch[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int rr = 16 * r + 8 * (c & 1) + i;
+        patch[i] = load8<VEC>(f + static_cast<size_t>(min(rr, rank - 1)) * width, col, width, rr < rank);
+    }
+    static_for<0, 8>([&](auto qc) { op[decltype(qc)::value] = patch_column<decltype(qc)::value>(patch); });
+}
+
+// y[row] = base[row] + (scaled rank-long row) * factor. A wave takes 128 columns
+// of a tile, 16 rows at a time; with R > 0 (r16 = R) the strip's operands stay
+// in registers for all of them, else (R = 0) they are loaded again.
+// Grid: (column chunks, tiles).
+template <int R, bool VEC>
 __global__ __launch_bounds__(kWgThreads) void expand_kernel(
     const TileInfo* __restrict__ info, const int32_t* __restrict__ tile_rows,
     const uint16_t* __restrict__ by_row, const uint16_t* __restrict__ factor, int width, int rank,
@@ -289,52 +330,46 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
     }
     const uint16_t* f = factor + static_cast<size_t>(ti.group) * rank * width;
     const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * 32;
-    for (int s0 = 0; s0 < kSubs; s0 += 2) {
-        if (16 * s0 >= ti.rows) return;
-        int row[2][4];
-        u32x4 bv[2][4];
+    u32x4 op[R ? R : 1][8];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+    for (int r = 0; r < R; ++r) factor_operands<VEC>(f, r, rank, col, width, c, op[r]);
+    for (int s = 0; 16 * s < ti.rows; ++s) {
+        int row[4];
+        u32x4 bv[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                row[s][i] = trow[16 * (s0 + s) + 4 * c + i];
-                bv[s][i] = load8<VEC>(base + static_cast<size_t>(max(row[s][i], 0)) * width, col, width,
-                                      base && row[s][i] >= 0);
+        for (int i = 0; i < 4; ++i) row[i] = trow[16 * s + 4 * c + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            bv[i] = load8<VEC>(base + static_cast<size_t>(max(row[i], 0)) * width, col, width,
+                               base && row[i] >= 0);
+        const uint16_t* a_at = rows_op + static_cast<size_t>(16 * s + j) * r16 * 32 + 8 * c;
+        floatx4 acc[8] = {};
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const u32x4 a = *reinterpret_cast<const u32x4*>(a_at + 32 * r);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    acc[q] = mfma16x16x32(as_bf16x8(a), as_bf16x8(op[r][q]), acc[q]);
             }
-        floatx4 acc[2][8] = {};
-        for (int r = 0; r < r16; ++r) {
-            u32x4 patch[8];
+        } else {
+            for (int r = 0; r < r16; ++r) {
+                const u32x4 a = *reinterpret_cast<const u32x4*>(a_at + 32 * r);
+                factor_operands<VEC>(f, r, rank, col, width, c, op[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // lanes c and c + 2: the ranks of the hi and of the lo parts
-                const int rr = 16 * r + 8 * (c & 1) + i;
-                patch[i] = load8<VEC>(f + static_cast<size_t>(min(rr, rank - 1)) * width, col, width,
-                                      rr < rank);
+                for (int q = 0; q < 8; ++q)
+                    acc[q] = mfma16x16x32(as_bf16x8(a), as_bf16x8(op[0][q]), acc[q]);
             }
-            u32x4 a[2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                a[s] = *reinterpret_cast<const u32x4*>(
-                    rows_op + (static_cast<size_t>(16 * (s0 + s) + j) * r16 + r) * 32 + 8 * c);
-            static_for<0, 8>([&](auto qc) {
-                constexpr int q = decltype(qc)::value;
-                const u32x4 b = patch_column<q>(patch);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    acc[s][q] = mfma16x16x32(as_bf16x8(a[s]), as_bf16x8(b), acc[s][q]);
-            });
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int i = 0; i < 4; ++i) {
+            if (row[i] < 0) continue;
+            u32x4 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (row[s][i] < 0) continue;
-                u32x4 o;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    o[d] = pack_bf16(bf16_low(bv[s][i][d]) + acc[s][2 * d][i],
-                                     bf16_high(bv[s][i][d]) + acc[s][2 * d + 1][i]);
-                store8<VEC>(y + static_cast<size_t>(row[s][i]) * width, col, width, o);
-            }
+            for (int d = 0; d < 4; ++d)
+                o[d] = pack_bf16(bf16_low(bv[i][d]) + acc[2 * d][i], bf16_high(bv[i][d]) + acc[2 * d + 1][i]);
+            store8<VEC>(y + static_cast<size_t>(row[i]) * width, col, width, o);
+        }
     }
 }
 
@@ -359,36 +394,46 @@ __global__ __launch_bounds__(kWgThreads) void outer_kernel(
     const int group_tiles = (at.end - at.first + kTileRows - 1) / kTileRows;
     const int t0 = at.tiles + at.index * seg_tiles;
     const int t1 = at.tiles + min(group_tiles, (at.index + 1) * seg_tiles);
+    // This wave's 32-row halves of tiles t0 + wave, t0 + wave + 4, ...; the next
+    // half's rows are loaded while one is multiplied.
+    struct Half {
+        u32x4 patch[8], a[R][2];
+    };
+    auto load = [&](Half& q, int step) {
+        const int t = t0 + wave + kWgWaves * (step >> 1), h = step & 1;
+        const int32_t* trow = tile_rows + t * kTileRows + 32 * h + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q.patch[i] = load8<VEC>(x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
+                                    trow[i] >= 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+                q.a[r][part] = *reinterpret_cast<const u32x4*>(
+                    by_rank + (((static_cast<size_t>(t) * r16 + r0 + r) * 2 + part) * 16 + j) * kTileRows +
+                    32 * h + 8 * c);
+    };
     floatx4 acc[R][8] = {};
-    for (int t = t0 + wave; t < t1; t += kWgWaves) {
+    auto multiply = [&](const Half& q) {
+        static_for<0, 8>([&](auto qc) {
+            constexpr int e = decltype(qc)::value;
+            const u32x4 b = patch_column<e>(q.patch);
 #pragma unroll
-        for (int h = 0; h < kTileRows / 32; ++h) {
-            const int32_t* trow = tile_rows + t * kTileRows + 32 * h + 8 * c;
-            u32x4 patch[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                patch[i] = load8<VEC>(x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
-                                      trow[i] >= 0);
-            u32x4 a[R][2];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-                    a[r][part] = r0 + r < r16
-                                     ? *reinterpret_cast<const u32x4*>(
-                                           by_rank + (((static_cast<size_t>(t) * r16 + r0 + r) * 2 + part) *
-                                                          16 + j) * kTileRows + 32 * h + 8 * c)
-                                     : u32x4{0u, 0u, 0u, 0u};
-            static_for<0, 8>([&](auto qc) {
-                constexpr int q = decltype(qc)::value;
-                const u32x4 b = patch_column<q>(patch);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    acc[r][q] = mfma16x16x32(as_bf16x8(a[r][0]), as_bf16x8(b), acc[r][q]);
-                    acc[r][q] = mfma16x16x32(as_bf16x8(a[r][1]), as_bf16x8(b), acc[r][q]);
-                }
-            });
-        }
+            for (int r = 0; r < R; ++r) {
+                acc[r][e] = mfma16x16x32(as_bf16x8(q.a[r][0]), as_bf16x8(b), acc[r][e]);
+                acc[r][e] = mfma16x16x32(as_bf16x8(q.a[r][1]), as_bf16x8(b), acc[r][e]);
+            }
+        });
+    };
+    const int steps = t1 - t0 > wave ? 2 * ((t1 - t0 - wave + kWgWaves - 1) / kWgWaves) : 0;
+    Half q[2];
+    if (steps) load(q[0], 0);
+    for (int step = 0; step < steps; step += 2) {
+        load(q[1], step + 1);
+        multiply(q[0]);
+        if (step + 2 < steps) load(q[0], step + 2);
+        multiply(q[1]);
     }
     for (int w = 0; w < kWgWaves; ++w) {
         if (wave == w) {
@@ -465,9 +510,9 @@ int inner_splits(int tiles, int width) {
     return n < 1 ? 1 : n > 32 ? 32 : n;
 }
 
-// Columns of one split: a multiple of 128 (a 32-column step per wave).
+// Columns of one split: a multiple of 256 (a 64-column step per wave).
 int split_columns(int width, int splits) {
-    return ((width + splits - 1) / splits + 127) / 128 * 128;
+    return ((width + splits - 1) / splits + 255) / 256 * 256;
 }
 
 Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
@@ -523,7 +568,10 @@ hipError_t launch_inner(const Plan& p, const uint16_t* x, const uint16_t* factor
 hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int rank, int count,
                          const uint16_t* base, uint16_t* y, bool vec, void* ws, hipStream_t st) {
     const int chunk = kWgWaves * kStrip;
-    return launch_kernel(vec ? expand_kernel<true> : expand_kernel<false>,
+    auto kernel = p.r16 == 1   ? (vec ? expand_kernel<1, true> : expand_kernel<1, false>)
+                  : p.r16 == 2 ? (vec ? expand_kernel<2, true> : expand_kernel<2, false>)
+                               : (vec ? expand_kernel<0, true> : expand_kernel<0, false>);
+    return launch_kernel(kernel,
                          dim3((width + chunk - 1) / chunk, p.tiles), dim3(kWgThreads), st,
                          at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
                          at<uint16_t>(ws, p.by_row), factor, width, rank, p.r16, count, base, y);
@@ -573,9 +621,8 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
                           dim3(splits, rows), dim3(kWgThreads), st, x, ids, f.a, f.in, f.rank,
                           f.count, static_cast<float*>(ws));
         if (e != hipSuccess) return e;
-        const int chunk = kWgThreads * 8;
         return launch_kernel(vec_out ? direct_expand_kernel<true> : direct_expand_kernel<false>,
-                             dim3((f.out + chunk - 1) / chunk, rows), dim3(kWgThreads), st,
+                             dim3(direct_splits(f.out), rows), dim3(kWgThreads), st,
                              static_cast<const float*>(ws), splits, ids, f.b, f.scales, f.out,
                              f.rank, f.count, base, y, u);
     }
@@ -586,7 +633,7 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
     if ((e = vec_in ? launch_inner<true>(p, x, f.a, rows, f.in, f.rank, f.count, ws, st)
                     : launch_inner<false>(p, x, f.a, rows, f.in, f.rank, f.count, ws, st)))
         return e;
-    if ((e = launch_kernel(tile_kernel, dim3(p.tiles), dim3(kWgThreads), st,
+    if ((e = launch_kernel(tile_kernel, dim3(p.tiles, 4 * p.r16), dim3(kWgThreads), st,
                            at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
@@ -608,7 +655,7 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
     if (rows && (e = vec_out ? launch_inner<true>(p, dy, f.b, rows, f.out, f.rank, f.count, ws, st)
                              : launch_inner<false>(p, dy, f.b, rows, f.out, f.rank, f.count, ws, st)))
         return e;
-    if (rows && (e = launch_kernel(tile_kernel, dim3(p.tiles), dim3(kWgThreads), st,
+    if (rows && (e = launch_kernel(tile_kernel, dim3(p.tiles, 4 * p.r16), dim3(kWgThreads), st,
                            at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),

@@ -79,6 +79,10 @@ __global__ __launch_bounds__(kSortThreads) void route_count_kernel(
         counts[static_cast<size_t>(blockIdx.x) * keys + g] = hist[g];
 }
 
+// The ids of a wave's first kKeptSteps steps stay in registers between counting
+// and placing: one memory round trip for all of them instead of two per step.
+constexpr int kKeptSteps = kSingleSlots / kSortThreads;
+
 // Places of one chunk's slots. keys = groups, or groups + 1 where the slots
 // outside every group are kept as one more group behind the others (then
 // offsets has keys + 1 entries). counts: every chunk's ids (null for one
@@ -96,9 +100,18 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
     // each wave takes a contiguous part of the chunk, in steps of 64 slots
     const int steps = (s1 - s0 + kSortThreads - 1) / kSortThreads;
     const int w0 = s0 + wave * steps * kWave, w1 = min(s1, w0 + steps * kWave);
+    int kept[kKeptSteps];
+#pragma unroll
+    for (int s = 0; s < kKeptSteps; ++s) {
+        const int i = w0 + s * kWave + lane;
+        kept[s] = i < w1 ? slot_key(ids, i, groups) : keys;
+    }
     for (int g = tid; g < kSortWaves * keys; g += kSortThreads) next[g] = 0;
     __syncthreads();
-    for (int i = w0 + lane; i < w1; i += kWave) {
+#pragma unroll
+    for (int s = 0; s < kKeptSteps; ++s)
+        if (kept[s] < keys) atomicAdd(&next[wave * keys + kept[s]], 1);
+    for (int i = w0 + kKeptSteps * kWave + lane; i < w1; i += kWave) {
         const int key = slot_key(ids, i, groups);
         if (key < keys) atomicAdd(&next[wave * keys + key], 1);
     }
@@ -117,6 +130,7 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
             all = mine;
             if (counts) {
                 all = 0;
+#pragma unroll 8
                 for (int q = 0; q < chunks; ++q) {
                     const int n = counts[static_cast<size_t>(q) * keys + g];
                     if (q < static_cast<int>(blockIdx.x)) earlier += n;
@@ -135,9 +149,7 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
     }
     if (blockIdx.x == 0 && tid == 0) offsets[keys] = base;
     const int bits = 32 - __clz(keys);
-    for (int i0 = w0; i0 < w1; i0 += kWave) {
-        const int i = i0 + lane;
-        const int key = i < w1 ? slot_key(ids, i, groups) : keys;
+    auto place_step = [&](int i, int key) {
         const bool live = key < keys;
         const uint64_t same = same_key(key, live, bits);
         int place = -1;
@@ -147,7 +159,12 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
         wave_lds_sync();
         if (i < w1 && position) position[i] = place;
         if (live) order[place] = i;
-    }
+    };
+#pragma unroll
+    for (int s = 0; s < kKeptSteps; ++s)
+        if (w0 + s * kWave < w1) place_step(w0 + s * kWave + lane, kept[s]);
+    for (int i0 = w0 + kKeptSteps * kWave; i0 < w1; i0 += kWave)
+        place_step(i0 + lane, i0 + lane < w1 ? slot_key(ids, i0 + lane, groups) : keys);
     for (int p = max(base, s0) + tid; p < s1; p += kSortThreads) order[p] = -1;
 }
 

@@ -331,62 +331,89 @@ class Route(NamedTuple):
     position: torch.Tensor  # [tokens, top_k] place of each slot, -1 if dropped
 
 
-def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: device tensors must be contiguous and on the GPU")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return t
+def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    """Refuse a tensor that is not dense, of this type and shape, and on `device`."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != device):
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}: device tensors must be contiguous and on the GPU")
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
 
 
-def _dims(name: str, t: torch.Tensor, n: int) -> tuple:
+def _dims(name: str, t: torch.Tensor, n: int) -> torch.Size:
     if t.dim() != n:
         raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _device(t: torch.Tensor) -> int:
+    """The current device, which every tensor of a call has to be on."""
+    return torch.cuda.current_device() if t.is_cuda else -2
+
+
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _apart(outputs: dict, inputs: dict) -> None:
     """Refuse an output that shares memory with an input or another output."""
-    spans = [(name, t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), out)
-             for out, group in ((True, outputs), (False, inputs))
-             for name, t in group.items() if t is not None and t.numel()]
-    for i, (a, a0, a1, out) in enumerate(spans):
-        for b, b0, b1, _ in spans[i + 1:]:
-            if out and a0 < b1 and b0 < a1:
+    outs = [(name, t.data_ptr(), t.nbytes) for name, t in outputs.items() if t is not None]
+    ins = [(name, t.data_ptr(), t.nbytes) for name, t in inputs.items() if t is not None]
+    for i, (a, a0, an) in enumerate(outs):
+        for b, b0, bn in outs[i + 1:] + ins:
+            if a0 < b0 + bn and b0 < a0 + an and an and bn:
                 raise ValueError(f"{a} overlaps {b}")
 
 
-def _on(stream: torch.cuda.Stream | None):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+_NO_STREAM = contextlib.nullcontext()
 
 
-def _workspace(fn: str, nbytes: int, given: torch.Tensor | None, device) -> tuple:
+def _on(stream: torch.cuda.Stream | None, device: int):
+    if stream is None:
+        return _NO_STREAM
+    if stream.device.index != device:
+        raise ValueError(f"stream: of {stream.device}, but the current device is cuda:{device}")
+    return torch.cuda.stream(stream)
+
+
+def _handle(device: int) -> int:
+    """The current stream's handle (torch.cuda.current_stream().cuda_stream, which
+    builds a Stream object first: 2.8 against 0.1 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _workspace(fn: str, nbytes: int, given: torch.Tensor | None, like: torch.Tensor) -> tuple:
     """(address, bytes, tensor) of the caller's workspace or of a new one."""
     if nbytes == C.c_size_t(-1).value:
         raise TrellisError(fn, ERR_GEOMETRY)
-    if given is None and nbytes:
-        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _dev(given), 0 if given is None else given.numel() * given.element_size(), given
+    if given is not None:
+        if not given.is_contiguous() or given.get_device() != like.get_device():
+            raise ValueError("workspace: expected a contiguous tensor on the device of the others")
+        return given.data_ptr(), given.nbytes, given
+    if not nbytes:
+        return None, 0, None
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    return ws.data_ptr(), nbytes, ws
 
 
 def route(ids, groups: int, workspace=None, stream=None) -> Route:
     """Sort the slots of ids (int32 [tokens, top_k]) by group, equal ids in slot
     order; ids outside [0, groups) are dropped."""
     tokens, top_k = _dims("ids", ids, 2)
-    _want("ids", ids, torch.int32, (tokens, top_k))
+    dev = _device(ids)
+    _want("ids", ids, torch.int32, (tokens, top_k), dev)
     fn = "trellis_route"
-    with _on(stream):
-        nbytes = _lib.trellis_route_workspace_bytes(tokens, top_k, groups)
-        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, ids.device)
-        r = Route(torch.empty(groups + 1, dtype=torch.int32, device=ids.device),
-                  torch.empty(tokens * top_k, dtype=torch.int32, device=ids.device),
-                  torch.empty((tokens, top_k), dtype=torch.int32, device=ids.device))
-        _check(fn, _lib.trellis_route(_dev(ids), tokens, top_k, groups, _dev(r.offsets),
-                                      _dev(r.order), _dev(r.position), ws, ws_bytes,
-                                      _stream(None)))
+    nbytes = _lib.trellis_route_workspace_bytes(tokens, top_k, groups)
+    with _on(stream, dev):
+        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, ids)
+        if workspace is not None:
+            _apart({"workspace": workspace}, {"ids": ids})
+        r = Route(ids.new_empty(groups + 1), ids.new_empty(tokens * top_k), torch.empty_like(ids))
+        _check(fn, _lib.trellis_route(ids.data_ptr(), tokens, top_k, groups, r.offsets.data_ptr(),
+                                      r.order.data_ptr(), r.position.data_ptr(), ws, ws_bytes,
+                                      _handle(dev)))
     return r
 
 
@@ -396,15 +423,18 @@ def dispatch(x, route: Route, out=None, stream=None) -> torch.Tensor:
     Its gradient is combine(dout, None, route)."""
     tokens, width = _dims("x", x, 2)
     top_k = _dims("position", route.position, 2)[1]
-    _want("x", x, torch.bfloat16, (tokens, width))
-    _want("position", route.position, torch.int32, (tokens, top_k))
-    with _on(stream):
+    dev = _device(x)
+    _want("x", x, torch.bfloat16, (tokens, width), dev)
+    _want("position", route.position, torch.int32, (tokens, top_k), dev)
+    with _on(stream, dev):
         if out is None:
-            out = torch.empty((tokens * top_k, width), dtype=torch.bfloat16, device=x.device)
-        _want("out", out, torch.bfloat16, (tokens * top_k, width))
-        _apart({"out": out}, {"x": x, "position": route.position})
+            out = x.new_empty((tokens * top_k, width))
+        else:
+            _want("out", out, torch.bfloat16, (tokens * top_k, width), dev)
+            _apart({"out": out}, {"x": x, "position": route.position})
         _check("trellis_dispatch", _lib.trellis_dispatch(
-            _dev(x), _dev(route.position), tokens, top_k, width, _dev(out), _stream(None)))
+            x.data_ptr(), route.position.data_ptr(), tokens, top_k, width, out.data_ptr(),
+            _handle(dev)))
     return out
 
 
@@ -413,18 +443,20 @@ def combine(y, weights, route: Route, out=None, stream=None) -> torch.Tensor:
     weights: float32 [tokens, top_k], or None for the plain sum."""
     tokens, top_k = _dims("position", route.position, 2)
     width = _dims("y", y, 2)[1]
-    _want("y", y, torch.bfloat16, (tokens * top_k, width))
-    _want("position", route.position, torch.int32, (tokens, top_k))
+    dev = _device(y)
+    _want("y", y, torch.bfloat16, (tokens * top_k, width), dev)
+    _want("position", route.position, torch.int32, (tokens, top_k), dev)
     if weights is not None:
-        _want("weights", weights, torch.float32, (tokens, top_k))
-    with _on(stream):
+        _want("weights", weights, torch.float32, (tokens, top_k), dev)
+    with _on(stream, dev):
         if out is None:
-            out = torch.empty((tokens, width), dtype=torch.bfloat16, device=y.device)
-        _want("out", out, torch.bfloat16, (tokens, width))
-        _apart({"out": out}, {"y": y, "weights": weights, "position": route.position})
+            out = y.new_empty((tokens, width))
+        else:
+            _want("out", out, torch.bfloat16, (tokens, width), dev)
+            _apart({"out": out}, {"y": y, "weights": weights, "position": route.position})
         _check("trellis_combine", _lib.trellis_combine(
-            _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width, _dev(out),
-            _stream(None)))
+            y.data_ptr(), _ptr(weights), route.position.data_ptr(), tokens, top_k, width,
+            out.data_ptr(), _handle(dev)))
     return out
 
 
@@ -434,22 +466,23 @@ def combine_backward(dout, y, weights, route: Route, dy=None, dweights=None,
     width]; rows of `dy` behind the last placed slot are left as they were."""
     tokens, top_k = _dims("position", route.position, 2)
     width = _dims("y", y, 2)[1]
-    _want("dout", dout, torch.bfloat16, (tokens, width))
-    _want("y", y, torch.bfloat16, (tokens * top_k, width))
-    _want("weights", weights, torch.float32, (tokens, top_k))
-    _want("position", route.position, torch.int32, (tokens, top_k))
-    with _on(stream):
+    dev = _device(y)
+    _want("dout", dout, torch.bfloat16, (tokens, width), dev)
+    _want("y", y, torch.bfloat16, (tokens * top_k, width), dev)
+    _want("weights", weights, torch.float32, (tokens, top_k), dev)
+    _want("position", route.position, torch.int32, (tokens, top_k), dev)
+    with _on(stream, dev):
+        given = {"dy": dy, "dweights": dweights}
         if dy is None:
             dy = torch.empty_like(y)
         if dweights is None:
             dweights = torch.empty_like(weights)
-        _want("dy", dy, torch.bfloat16, (tokens * top_k, width))
-        _want("dweights", dweights, torch.float32, (tokens, top_k))
-        _apart({"dy": dy, "dweights": dweights},
-               {"dout": dout, "y": y, "weights": weights, "position": route.position})
+        _want("dy", dy, torch.bfloat16, (tokens * top_k, width), dev)
+        _want("dweights", dweights, torch.float32, (tokens, top_k), dev)
+        _apart(given, {"dout": dout, "y": y, "weights": weights, "position": route.position})
         _check("trellis_combine_backward", _lib.trellis_combine_backward(
-            _dev(dout), _dev(y), _dev(weights), _dev(route.position), tokens, top_k, width,
-            _dev(dy), _dev(dweights), _stream(None)))
+            dout.data_ptr(), y.data_ptr(), weights.data_ptr(), route.position.data_ptr(), tokens,
+            top_k, width, dy.data_ptr(), dweights.data_ptr(), _handle(dev)))
     return dy, dweights
 
 
@@ -465,35 +498,36 @@ def experts(x, offsets, codes, scales, lut, g, y=None, workspace=None, stream=No
     n = _dims("offsets", offsets, 1)[0] - 1
     stored, cols = ((geom.out_features, geom.in_features) if geom.axis == 1
                     else (geom.in_features, geom.out_features))
-    _want("x", x, torch.bfloat16, (rows, geom.in_features))
-    _want("offsets", offsets, torch.int32, (n + 1,))
-    _want("scales", scales, torch.float32, (n, stored))
-    _want("lut", lut, torch.float32, (1 << 12,))
-    _want("codes", codes, torch.int32, codes.shape)
+    dev = _device(x)
+    _want("x", x, torch.bfloat16, (rows, geom.in_features), dev)
+    _want("offsets", offsets, torch.int32, (n + 1,), dev)
+    _want("scales", scales, torch.float32, (n, stored), dev)
+    _want("lut", lut, torch.float32, (1 << 12,), dev)
+    _want("codes", codes, torch.int32, codes.shape, dev)
     if codes.dim() < 1 or codes.shape[0] != n or codes.numel() != n * stored * cols * geom.k // 32:
         raise ValueError(f"codes: expected {n} experts of {stored} x {cols} weights of {geom.k} "
                          f"bits, got {tuple(codes.shape)}")
-    with _on(stream):
+    fn = "trellis_experts"
+    nbytes = _lib.trellis_experts_workspace_bytes(C.byref(geom), rows, n)
+    with _on(stream, dev):
+        given = {"y": y, "workspace": workspace}
         if y is None:
-            y = torch.empty((rows, geom.out_features), dtype=torch.bfloat16, device=x.device)
-        _want("y", y, torch.bfloat16, (rows, geom.out_features))
-        fn = "trellis_experts"
-        nbytes = _lib.trellis_experts_workspace_bytes(C.byref(geom), rows, n)
-        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, x.device)
-        _apart({"y": y, "workspace": keep},
-               {"x": x, "offsets": offsets, "codes": codes, "scales": scales, "lut": lut})
-        _check(fn, _lib.trellis_experts(_dev(x), rows, _dev(offsets), n, _dev(codes), _dev(scales),
-                                        _dev(lut), C.byref(geom), _dev(y), ws, ws_bytes,
-                                        _stream(None)))
+            y = x.new_empty((rows, geom.out_features))
+        _want("y", y, torch.bfloat16, (rows, geom.out_features), dev)
+        ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, x)
+        _apart(given, {"x": x, "offsets": offsets, "codes": codes, "scales": scales, "lut": lut})
+        _check(fn, _lib.trellis_experts(
+            x.data_ptr(), rows, offsets.data_ptr(), n, codes.data_ptr(), scales.data_ptr(),
+            lut.data_ptr(), C.byref(geom), y.data_ptr(), ws, ws_bytes, _handle(dev)))
     return y
 
 
-def _adapter_set(a, b, scales) -> AdapterSet:
+def _adapter_set(a, b, scales, device: int) -> AdapterSet:
     count, rank, i = _dims("a", a, 3)
     o = _dims("b", b, 3)[2]
-    _want("a", a, torch.bfloat16, (count, rank, i))
-    _want("b", b, torch.bfloat16, (count, rank, o))
-    _want("scales", scales, torch.float32, (count,))
+    _want("a", a, torch.bfloat16, (count, rank, i), device)
+    _want("b", b, torch.bfloat16, (count, rank, o), device)
+    _want("scales", scales, torch.float32, (count,), device)
     return AdapterSet(a.data_ptr(), b.data_ptr(), scales.data_ptr(), count, rank, i, o)
 
 
@@ -511,28 +545,31 @@ def adapters(x, ids, a, b, scales, base=None, y=None, u=None, keep_inner=False, 
     rank, in]; b: bf16 [count, rank, out]; base: bf16 [rows, out] (None: zeros),
     which y may be. u: float32 [rows, rank] of inner products, None unless given
     or keep_inner (the backward pass needs it)."""
-    f = _adapter_set(a, b, scales)
+    dev = _device(x)
+    f = _adapter_set(a, b, scales, dev)
     rows = _dims("x", x, 2)[0]
-    _want("x", x, torch.bfloat16, (rows, f.in_features))
-    _want("ids", ids, torch.int32, (rows,))
+    _want("x", x, torch.bfloat16, (rows, f.in_features), dev)
+    _want("ids", ids, torch.int32, (rows,), dev)
     if base is not None:
-        _want("base", base, torch.bfloat16, (rows, f.out_features))
-    with _on(stream):
+        _want("base", base, torch.bfloat16, (rows, f.out_features), dev)
+    nbytes = adapters_workspace_bytes(f, rows, False)
+    with _on(stream, dev):
+        given = {"y": y, "u": u, "workspace": workspace}
         if y is None:
-            y = torch.empty((rows, f.out_features), dtype=torch.bfloat16, device=x.device)
-        if u is None and keep_inner:
-            u = torch.empty((rows, f.rank), dtype=torch.float32, device=x.device)
-        _want("y", y, torch.bfloat16, (rows, f.out_features))
+            y = x.new_empty((rows, f.out_features))
+        else:
+            _want("y", y, torch.bfloat16, (rows, f.out_features), dev)
         if u is not None:
-            _want("u", u, torch.float32, (rows, f.rank))
-        ws, ws_bytes, keep = _workspace("trellis_adapters", adapters_workspace_bytes(f, rows, False),
-                                        workspace, x.device)
+            _want("u", u, torch.float32, (rows, f.rank), dev)
+        elif keep_inner:
+            u = x.new_empty((rows, f.rank), dtype=torch.float32)
+        ws, ws_bytes, keep = _workspace("trellis_adapters", nbytes, workspace, x)
         same = base is not None and base.data_ptr() == y.data_ptr()
-        _apart({"y": y, "u": u, "workspace": keep},
-               {"x": x, "ids": ids, "a": a, "b": b, "scales": scales, "base": None if same else base})
+        _apart(given, {"x": x, "ids": ids, "a": a, "b": b, "scales": scales,
+                       "base": None if same else base})
         _check("trellis_adapters", _lib.trellis_adapters(
-            _dev(x), _dev(ids), rows, C.byref(f), _dev(base), _dev(y), _dev(u), ws, ws_bytes,
-            _stream(None)))
+            x.data_ptr(), ids.data_ptr(), rows, C.byref(f), _ptr(base), y.data_ptr(), _ptr(u), ws,
+            ws_bytes, _handle(dev)))
     return y, u
 
 
@@ -541,31 +578,32 @@ def adapters_backward(dy, x, u, ids, a, b, scales, base=None, dx=None, da=None, 
     """Gradients (dx, da, db) of adapters from dy [rows, out] with the forward
     pass's u: dx = base + a[i]^T g with g = scales[i] * b[i] dy, da and db whole
     (zeros for adapters without rows), all bf16. dx may be `base`."""
-    f = _adapter_set(a, b, scales)
+    dev = _device(x)
+    f = _adapter_set(a, b, scales, dev)
     rows = _dims("x", x, 2)[0]
-    _want("dy", dy, torch.bfloat16, (rows, f.out_features))
-    _want("x", x, torch.bfloat16, (rows, f.in_features))
-    _want("u", u, torch.float32, (rows, f.rank))
-    _want("ids", ids, torch.int32, (rows,))
+    _want("dy", dy, torch.bfloat16, (rows, f.out_features), dev)
+    _want("x", x, torch.bfloat16, (rows, f.in_features), dev)
+    _want("u", u, torch.float32, (rows, f.rank), dev)
+    _want("ids", ids, torch.int32, (rows,), dev)
     if base is not None:
-        _want("base", base, torch.bfloat16, (rows, f.in_features))
-    with _on(stream):
+        _want("base", base, torch.bfloat16, (rows, f.in_features), dev)
+    nbytes = adapters_workspace_bytes(f, rows, True)
+    with _on(stream, dev):
+        given = {"dx": dx, "da": da, "db": db, "workspace": workspace}
         if dx is None:
             dx = torch.empty_like(x)
         if da is None:
             da = torch.empty_like(a)
         if db is None:
             db = torch.empty_like(b)
-        _want("dx", dx, torch.bfloat16, (rows, f.in_features))
-        _want("da", da, torch.bfloat16, a.shape)
-        _want("db", db, torch.bfloat16, b.shape)
-        ws, ws_bytes, keep = _workspace("trellis_adapters_backward",
-                                        adapters_workspace_bytes(f, rows, True), workspace, x.device)
+        _want("dx", dx, torch.bfloat16, (rows, f.in_features), dev)
+        _want("da", da, torch.bfloat16, a.shape, dev)
+        _want("db", db, torch.bfloat16, b.shape, dev)
+        ws, ws_bytes, keep = _workspace("trellis_adapters_backward", nbytes, workspace, x)
         same = base is not None and base.data_ptr() == dx.data_ptr()
-        _apart({"dx": dx, "da": da, "db": db, "workspace": keep},
-               {"dy": dy, "x": x, "u": u, "ids": ids, "a": a, "b": b, "scales": scales,
-                "base": None if same else base})
+        _apart(given, {"dy": dy, "x": x, "u": u, "ids": ids, "a": a, "b": b, "scales": scales,
+                       "base": None if same else base})
         _check("trellis_adapters_backward", _lib.trellis_adapters_backward(
-            _dev(dy), _dev(x), _dev(u), _dev(ids), rows, C.byref(f), _dev(base), _dev(dx), _dev(da),
-            _dev(db), ws, ws_bytes, _stream(None)))
+            dy.data_ptr(), x.data_ptr(), u.data_ptr(), ids.data_ptr(), rows, C.byref(f), _ptr(base),
+            dx.data_ptr(), da.data_ptr(), db.data_ptr(), ws, ws_bytes, _handle(dev)))
     return dx, da, db
