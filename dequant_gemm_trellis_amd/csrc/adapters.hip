@@ -34,11 +34,24 @@ constexpr int kSubs = kTileRows / 16;
 constexpr int kWgThreads = 256;
 constexpr int kWgWaves = kWgThreads / kWave;
 constexpr int kStrip = 128;            // columns per wave: 16 lanes x 8
+constexpr int kMaxSegTiles = 16;       // tiles of one segment of the outer sums: 1024 rows
 
+// 8 values to a row from column `col` on (none past `width`); see load8.
 template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t* __restrict__ row, int col, int width, u32x4 v) {
     if constexpr (VEC) {
         if (col < width) *reinterpret_cast<u32x4*>(row + col) = v;
+    } else if (col + 8 <= width) {
+        uint16_t* p = row + col;
+        if (reinterpret_cast<uintptr_t>(p) & 2) {
+            p[0] = static_cast<uint16_t>(v[0]);
+            uint32_t* w = reinterpret_cast<uint32_t*>(p + 1);
+#pragma unroll
+            for (int d = 0; d < 3; ++d) w[d] = __builtin_amdgcn_alignbit(v[d + 1], v[d], 16);
+            p[7] = static_cast<uint16_t>(v[3] >> 16);
+        } else {
+            *reinterpret_cast<u32x4_a4*>(p) = v;
+        }
     } else {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -195,22 +208,47 @@ __global__ __launch_bounds__(kWgThreads) void inner_kernel(
     for (int s = 0; s < R; ++s) fr[s] = f + static_cast<size_t>(min(16 * s + j, rank - 1)) * width;
     floatx4 acc[kSubs][R] = {};
     const int k0 = blockIdx.x * split_cols, k1 = min(width, k0 + split_cols);
-    for (int k = k0 + 64 * wave; k < k1; k += 64 * kWgWaves) {
-        u32x4 xv[2][kSubs], fv[2][R];
+    struct Step {
+        u32x4 x[2][kSubs], f[2][R];
+    };
+    auto load = [&](Step& q, int k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int s = 0; s < kSubs; ++s) xv[h][s] = load8<VEC>(xr[s], k + 32 * h + 8 * c, k1, true);
+            for (int s = 0; s < kSubs; ++s) q.x[h][s] = load8<VEC>(xr[s], k + 32 * h + 8 * c, k1, true);
 #pragma unroll
-            for (int s = 0; s < R; ++s) fv[h][s] = load8<VEC>(fr[s], k + 32 * h + 8 * c, k1, true);
+            for (int r = 0; r < R; ++r) q.f[h][r] = load8<VEC>(fr[r], k + 32 * h + 8 * c, k1, true);
         }
+    };
+    auto multiply = [&](const Step& q) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int s = 0; s < kSubs; ++s)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    acc[s][r] = mfma16x16x32(as_bf16x8(xv[h][s]), as_bf16x8(fv[h][r]), acc[s][r]);
+                    acc[s][r] = mfma16x16x32(as_bf16x8(q.x[h][s]), as_bf16x8(q.f[h][r]), acc[s][r]);
+    };
+    // up to two 16-rank operands the next step's loads are in flight while one
+    // is multiplied (beyond, the registers hold one step)
+    constexpr int step = 64 * kWgWaves;
+    const int first = k0 + 64 * wave;
+    if constexpr (R <= 2 && VEC) {
+        Step q[2];
+        if (first < k1) load(q[0], first);
+        for (int k = first; k < k1; k += 2 * step) {
+            if (k + step < k1) load(q[1], k + step);
+            multiply(q[0]);
+            if (k + step >= k1) break;
+            if (k + 2 * step < k1) load(q[0], k + 2 * step);
+            multiply(q[1]);
+        }
+    } else {
+        for (int k = first; k < k1; k += step) {
+            Step q;
+            load(q, k);
+            multiply(q);
+        }
     }
     for (int w = 0; w < kWgWaves; ++w) {
         if (wave == w) {
@@ -330,14 +368,21 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
     }
     const uint16_t* f = factor + static_cast<size_t>(ti.group) * rank * width;
     const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * 32;
+    // every lane's rows first: a row's number read between the rows' loads would
+    // wait for all of them
+    int rows_at[kSubs][4];
+#pragma unroll
+    for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows_at[s][i] = trow[16 * s + 4 * c + i];
     u32x4 op[R ? R : 1][8];
 #pragma unroll
     for (int r = 0; r < R; ++r) factor_operands<VEC>(f, r, rank, col, width, c, op[r]);
-    for (int s = 0; 16 * s < ti.rows; ++s) {
-        int row[4];
+    static_for<0, kSubs>([&](auto sub) {
+        constexpr int s = decltype(sub)::value;
+        if (16 * s >= ti.rows) return;
+        const int (&row)[4] = rows_at[s];
         u32x4 bv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) row[i] = trow[16 * s + 4 * c + i];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             bv[i] = load8<VEC>(base + static_cast<size_t>(max(row[i], 0)) * width, col, width,
@@ -370,48 +415,52 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
                 o[d] = pack_bf16(bf16_low(bv[i][d]) + acc[2 * d][i], bf16_high(bv[i][d]) + acc[2 * d + 1][i]);
             store8<VEC>(y + static_cast<size_t>(row[i]) * width, col, width, o);
         }
-    }
+    });
 }
 
-// Sum over a segment's rows of (rank-long column) x (wide row): the segment's
-// tiles go to the four waves in turn, which are summed in wave order. An
-// adapter of one segment (or without rows) is written to `grad` in bf16; the
-// float32 sums of the others' segments go to `sums`, [shared segment][rank]
-// [width]. Grid: (strips, segments, rank pairs).
+// One of the two sums over an adapter's rows of a rank-long column times a wide
+// row: dA (g and x) or dB (scaled u and dy).
+struct OuterSide {
+    const uint16_t* x;        // the wide rows
+    const uint16_t* by_rank;  // the rank-long values
+    uint16_t* grad;           // [count][rank][width]
+    float* sums;              // [shared segment][rank][width]
+    int width, strips;
+    bool vec;
+};
+
+// A segment of an adapter's tiles: its tiles go to the four waves in turn, which
+// are summed in wave order. An adapter of one segment (or without rows) is
+// written to `grad` in bf16; the float32 sums of the others' segments go to
+// `sums`.
 template <int R, bool VEC>
-__global__ __launch_bounds__(kWgThreads) void outer_kernel(
-    const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ tile_rows, const uint16_t* __restrict__ by_rank, int rows, int width,
-    int rank, int r16, int count, int seg_tiles, float* __restrict__ sums,
-    uint16_t* __restrict__ grad) {
-    __shared__ float sum[16 * R * kStrip];
+__device__ __forceinline__ void outer_segment(const OuterSide& p, const Found& at, int strip, int r0,
+                                              int r16, int rank, int seg_tiles, const int* seg_rows,
+                                              float* sum) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, c = lane >> 4;
-    const int r0 = blockIdx.z * R;  // this workgroup's 16-rank operands: r0 .. r0 + R - 1
-    const Found at = find_entry(offsets, count, rows, seg_tiles * kTileRows, true, blockIdx.y);
-    if (at.group < 0) return;
-    const int col = blockIdx.x * kStrip + 8 * j;
+    const int width = p.width, col = strip * kStrip + 8 * j;
     const int group_tiles = (at.end - at.first + kTileRows - 1) / kTileRows;
+    const int n = min(group_tiles - at.index * seg_tiles, seg_tiles);
     const int t0 = at.tiles + at.index * seg_tiles;
-    const int t1 = at.tiles + min(group_tiles, (at.index + 1) * seg_tiles);
-    // This wave's 32-row halves of tiles t0 + wave, t0 + wave + 4, ...; the next
-    // half's rows are loaded while one is multiplied.
+    // This wave's 32-row halves of the segment's tiles wave, wave + 4, ...; the
+    // next half's rows are loaded while one is multiplied.
     struct Half {
         u32x4 patch[8], a[R][2];
     };
     auto load = [&](Half& q, int step) {
-        const int t = t0 + wave + kWgWaves * (step >> 1), h = step & 1;
-        const int32_t* trow = tile_rows + t * kTileRows + 32 * h + 8 * c;
+        const int t = wave + kWgWaves * (step >> 1), h = step & 1;
+        const int* trow = seg_rows + t * kTileRows + 32 * h + 8 * c;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            q.patch[i] = load8<VEC>(x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
+            q.patch[i] = load8<VEC>(p.x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
                                     trow[i] >= 0);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int part = 0; part < 2; ++part)
                 q.a[r][part] = *reinterpret_cast<const u32x4*>(
-                    by_rank + (((static_cast<size_t>(t) * r16 + r0 + r) * 2 + part) * 16 + j) * kTileRows +
+                    p.by_rank + (((static_cast<size_t>(t0 + t) * r16 + r0 + r) * 2 + part) * 16 + j) * kTileRows +
                     32 * h + 8 * c);
     };
     floatx4 acc[R][8] = {};
@@ -426,7 +475,7 @@ __global__ __launch_bounds__(kWgThreads) void outer_kernel(
             }
         });
     };
-    const int steps = t1 - t0 > wave ? 2 * ((t1 - t0 - wave + kWgWaves - 1) / kWgWaves) : 0;
+    const int steps = n > wave ? 2 * ((n - wave + kWgWaves - 1) / kWgWaves) : 0;
     Half q[2];
     if (steps) load(q[0], 0);
     for (int step = 0; step < steps; step += 2) {
@@ -443,48 +492,75 @@ __global__ __launch_bounds__(kWgThreads) void outer_kernel(
                 for (int i = 0; i < 4; ++i) {
                     float* o = sum + (16 * r + 4 * c + i) * kStrip + 8 * j;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) o[q] = w ? o[q] + acc[r][q][i] : acc[r][q][i];
+                    for (int e = 0; e < 8; ++e) o[e] = w ? o[e] + acc[r][e][i] : acc[r][e][i];
                 }
         }
         __syncthreads();
     }
     for (int i = tid; i < 16 * R * kStrip; i += kWgThreads) {
-        const int r = 16 * r0 + i / kStrip, k = blockIdx.x * kStrip + i % kStrip;
+        const int r = 16 * r0 + i / kStrip, k = strip * kStrip + i % kStrip;
         if (r >= rank || k >= width) continue;
         if (group_tiles > seg_tiles)
-            sums[(static_cast<size_t>(at.shared + at.index) * rank + r) * width + k] = sum[i];
+            p.sums[(static_cast<size_t>(at.shared + at.index) * rank + r) * width + k] = sum[i];
         else
-            grad[(static_cast<size_t>(at.group) * rank + r) * width + k] = round_bf16(sum[i]);
+            p.grad[(static_cast<size_t>(at.group) * rank + r) * width + k] = round_bf16(sum[i]);
     }
 }
 
-// The segments' sums of an adapter of several, ascending, rounded to bf16.
-// Grid: (column chunks, ranks, adapters).
+// Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces.
+// Grid: (strips of side a then of side b, segments, rank pairs).
+template <int R, bool VEC>
+__global__ __launch_bounds__(kWgThreads) void outer_kernel(
+    OuterSide a, OuterSide b, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ tile_rows, int rows, int rank, int r16, int count, int seg_tiles) {
+    __shared__ float sum[16 * R * kStrip];
+    __shared__ int seg_rows[kMaxSegTiles * kTileRows];
+    const Found at = find_entry(offsets, count, rows, seg_tiles * kTileRows, true, blockIdx.y);
+    if (at.group < 0) return;
+    const int t0 = at.tiles + at.index * seg_tiles;
+    const int n = min((at.end - at.first + kTileRows - 1) / kTileRows - at.index * seg_tiles, seg_tiles);
+    for (int i = threadIdx.x; i < n * kTileRows; i += kWgThreads)
+        seg_rows[i] = tile_rows[static_cast<size_t>(t0) * kTileRows + i];
+    __syncthreads();
+    const bool second = static_cast<int>(blockIdx.x) >= a.strips;
+    const OuterSide& p = second ? b : a;
+    const int strip = second ? blockIdx.x - a.strips : blockIdx.x, r0 = blockIdx.z * R;
+    if (VEC || p.vec)
+        outer_segment<R, true>(p, at, strip, r0, r16, rank, seg_tiles, seg_rows, sum);
+    else
+        outer_segment<R, false>(p, at, strip, r0, r16, rank, seg_tiles, seg_rows, sum);
+}
+
+// The segments' sums of the adapters of several, ascending, rounded to bf16, of
+// both sides. Grid: (column chunks of side a then of side b, ranks, adapters).
 __global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
-    const float* __restrict__ sums, const int32_t* __restrict__ offsets, int rows, int width,
-    int rank, int seg_tiles, uint16_t* __restrict__ grad) {
-    const int a = blockIdx.z, r = blockIdx.y;
-    const int k = blockIdx.x * kWgThreads + threadIdx.x;
+    OuterSide a, OuterSide b, int chunks_a, const int32_t* __restrict__ offsets, int rows, int rank,
+    int seg_tiles) {
+    const int n_ad = blockIdx.z, r = blockIdx.y;
+    const bool second = static_cast<int>(blockIdx.x) >= chunks_a;
+    const OuterSide& p = second ? b : a;
+    const int k = (second ? blockIdx.x - chunks_a : blockIdx.x) * kWgThreads + threadIdx.x;
     const int lane = threadIdx.x & 63, per = seg_tiles * kTileRows;
     int before = 0, mine = 0;  // shared segments of the adapters before, and this one's segments
-    for (int g0 = 0; g0 <= a; g0 += 64) {
+    for (int g0 = 0; g0 <= n_ad; g0 += 64) {
         const int g = g0 + lane;
         int n = 0;
-        if (g <= a) {
+        if (g <= n_ad) {
             const int first = min(max(offsets[g], 0), rows);
             n = (min(max(offsets[g + 1], first), rows) - first + per - 1) / per;
         }
-        int s = g < a && n > 1 ? n : 0;
+        int s = g < n_ad && n > 1 ? n : 0;
 #pragma unroll
         for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
         before += s;
-        mine = __shfl(n, a & 63);
+        mine = __shfl(n, n_ad & 63);
     }
-    if (mine <= 1 || k >= width) return;
+    if (mine <= 1 || k >= p.width) return;
     float v = 0.f;
+#pragma unroll 4
     for (int q = 0; q < mine; ++q)
-        v += sums[(static_cast<size_t>(before + q) * rank + r) * width + k];
-    grad[(static_cast<size_t>(a) * rank + r) * width + k] = round_bf16(v);
+        v += p.sums[(static_cast<size_t>(before + q) * rank + r) * p.width + k];
+    p.grad[(static_cast<size_t>(n_ad) * rank + r) * p.width + k] = round_bf16(v);
 }
 
 // ---- plans and launches ---------------------------------------------------------
@@ -493,14 +569,13 @@ __global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
 // read again by rows that share one).
 constexpr int kDirectRows = 64;
 constexpr int kTargetGroups = 1024;  // workgroups that fill the compute units a few times
-constexpr int kSegTiles = 16;        // tiles of one segment of the outer sums: 1024 rows
 
 struct Plan {
     int r16, tiles;             // 16-rank operands; tiles at most
     int splits, split_cols;     // column splits of the inner products
     int segments;               // segments of the outer sums, at most
     int shared;                 // those of adapters with several, at most
-    size_t offsets, order, counts, partial, info, tile_rows, by_row, by_rank, u_rank, sums, bytes;
+    size_t offsets, order, counts, partial, info, tile_rows, by_row, by_rank, u_rank, sums_a, sums_b, bytes;
 };
 
 int inner_splits(int tiles, int width) {
@@ -522,7 +597,7 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     const int width = backward ? out : in;
     p.split_cols = split_columns(width, inner_splits(p.tiles, width));
     p.splits = (width + p.split_cols - 1) / p.split_cols;
-    const int per = kSegTiles * kTileRows;
+    const int per = kMaxSegTiles * kTileRows;
     p.segments = count + rows / per;             // sum of max(1, ceil(n / per)), at most
     p.shared = rows > per ? 2 * (rows / per) : 0;  // n > per: ceil(n / per) <= 2 floor(n / per)
     size_t at = 0;
@@ -542,7 +617,8 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     if (backward) {
         p.by_rank = take(tiles * kTileRows * ranks * 2 * 2);
         p.u_rank = take(tiles * kTileRows * ranks * 2 * 2);
-        p.sums = take(static_cast<size_t>(p.shared) * rank * (in > out ? in : out) * 4);
+        p.sums_a = take(static_cast<size_t>(p.shared) * rank * in * 4);
+        p.sums_b = take(static_cast<size_t>(p.shared) * rank * out * 4);
     }
     p.bytes = at;
     return p;
@@ -578,26 +654,17 @@ hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int r
 }
 
 template <int R>
-hipError_t launch_outer_r(const Plan& p, const uint16_t* x, const uint16_t* by_rank, int rows,
-                          int width, int rank, int count, uint16_t* grad, bool vec, void* ws,
-                          hipStream_t st) {
-    float* sums = at<float>(ws, p.sums);
+hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b, int rows, int rank,
+                          int count, void* ws, hipStream_t st) {
+    const int32_t* offsets = at<int32_t>(ws, p.offsets);
     const hipError_t e = launch_kernel(
-        vec ? outer_kernel<R, true> : outer_kernel<R, false>,
-        dim3((width + kStrip - 1) / kStrip, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, x,
-        at<int32_t>(ws, p.offsets), at<int32_t>(ws, p.tile_rows), by_rank, rows, width, rank, p.r16,
-        count, kSegTiles, sums, grad);
+        a.vec && b.vec ? outer_kernel<R, true> : outer_kernel<R, false>,
+        dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b, offsets,
+        at<int32_t>(ws, p.tile_rows), rows, rank, p.r16, count, kMaxSegTiles);
     if (e != hipSuccess || !p.shared) return e;
-    return launch_kernel(outer_sum_kernel, dim3((width + kWgThreads - 1) / kWgThreads, rank, count),
-                         dim3(kWgThreads), st, sums, at<int32_t>(ws, p.offsets), rows, width, rank,
-                         kSegTiles, grad);
-}
-
-hipError_t launch_outer(const Plan& p, const uint16_t* x, const uint16_t* by_rank, int rows,
-                        int width, int rank, int count, uint16_t* grad, bool vec, void* ws,
-                        hipStream_t st) {
-    return p.r16 == 1 ? launch_outer_r<1>(p, x, by_rank, rows, width, rank, count, grad, vec, ws, st)
-                      : launch_outer_r<2>(p, x, by_rank, rows, width, rank, count, grad, vec, ws, st);
+    const int ca = (a.width + kWgThreads - 1) / kWgThreads, cb = (b.width + kWgThreads - 1) / kWgThreads;
+    return launch_kernel(outer_sum_kernel, dim3(ca + cb, rank, count), dim3(kWgThreads), st, a, b, ca,
+                         offsets, rows, rank, kMaxSegTiles);
 }
 
 int direct_splits(int width) { return (width + kDirectCols - 1) / kDirectCols; }
@@ -662,11 +729,13 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                            at<uint16_t>(ws, p.by_row), at<uint16_t>(ws, p.by_rank), nullptr, u,
                            at<uint16_t>(ws, p.u_rank))))
         return e;
-    if ((e = launch_outer(p, dy, at<uint16_t>(ws, p.u_rank), rows, f.out, f.rank, f.count, db,
-                          vec_out, ws, st)))
-        return e;
-    if ((e = launch_outer(p, x, at<uint16_t>(ws, p.by_rank), rows, f.in, f.rank, f.count, da, vec_in,
-                          ws, st)))
+    auto strips = [](int width) { return (width + kStrip - 1) / kStrip; };
+    const OuterSide side_b{dy, at<uint16_t>(ws, p.u_rank), db, at<float>(ws, p.sums_b), f.out,
+                           strips(f.out), vec_out};
+    const OuterSide side_a{x, at<uint16_t>(ws, p.by_rank), da, at<float>(ws, p.sums_a), f.in,
+                           strips(f.in), vec_in};
+    if ((e = p.r16 == 1 ? launch_outer_r<1>(p, side_b, side_a, rows, f.rank, f.count, ws, st)
+                        : launch_outer_r<2>(p, side_b, side_a, rows, f.rank, f.count, ws, st)))
         return e;
     if (rows == 0) return hipSuccess;
     return launch_expand(p, f.a, f.in, f.rank, f.count, base, dx, vec_in, ws, st);

@@ -11,6 +11,7 @@ using trellis::aligned;
 using trellis::status_of;
 
 static_assert(trellis::kMaxGroups == TRELLIS_MAX_GROUPS, "the header's limit");
+static_assert(trellis::kMaxSlots == TRELLIS_MAX_SLOTS, "the header's limit");
 static_assert(trellis::kMaxRank == TRELLIS_MAX_RANK, "the header's limit");
 
 namespace {

@@ -10,6 +10,7 @@
 namespace trellis {
 
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxSlots = 1 << 21;
 constexpr int kMaxKeys = kMaxGroups + 1;  // one more for the slots outside every group
 constexpr int kMaxRank = 128;             // of an adapter
 constexpr int kTileRows = 64;             // rows of an adapter's tile: four 16-row operands
@@ -129,13 +130,29 @@ __device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets,
     return {-1, 0, 0, 0, 0, 0};
 }
 
+// 16 bytes at a 4-byte boundary (what a global access of any width needs).
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
 // 8 values of a row from column `col` on, zeros past `width` and where !live.
-// VEC: rows are multiples of 8 values and 16-byte aligned.
+// VEC: rows are multiples of 8 values and 16-byte aligned. Otherwise a row
+// starts at any 2-byte boundary: at a 4-byte one the values are read as they
+// are, else from the five 4-byte words that hold them (whose outer halves are
+// not used); at the row's end one by one.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ row, int col, int width, bool live) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if constexpr (VEC) {
         if (live && col < width) v = *reinterpret_cast<const u32x4*>(row + col);
+    } else if (live && col + 8 <= width) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row + col);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p & ~static_cast<uintptr_t>(3));
+        v = *reinterpret_cast<const u32x4_a4*>(w);
+        if (p & 2) {
+            const uint32_t last = w[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                v[d] = __builtin_amdgcn_alignbit(d < 3 ? v[d < 3 ? d + 1 : 3] : last, v[d], 16);
+        }
     } else {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {

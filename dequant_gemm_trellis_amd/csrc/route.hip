@@ -14,13 +14,15 @@
 namespace trellis {
 namespace {
 
-// One workgroup sorts up to kSingleSlots slots in one launch; more slots are
+// One workgroup sorts up to kMaxChunkSlots slots in one launch; more slots are
 // cut into chunks: a launch counts each chunk's ids, a second one places them.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kSingleSlots = 8192;
-constexpr int kChunkSlots = 2048;   // slots per workgroup, at least
-constexpr int kMaxChunks = 256;     // every workgroup of the second launch reads all chunks' counts
+constexpr int kMaxSteps = 8;          // 64-slot steps of a wave: their ids stay in registers
+constexpr int kMaxChunkSlots = kMaxSteps * kSortThreads;
+constexpr int kOneChunk = 8192;       // slots that one workgroup sorts alone
+constexpr int kChunkSlots = 2048;     // slots per workgroup of several, at least
+constexpr int kMaxChunks = kMaxSlots / kMaxChunkSlots;  // each reads all chunks' counts
 
 // Lanes of the wave whose key equals this lane's, among the lanes with `live`.
 __device__ __forceinline__ uint64_t same_key(int key, bool live, int bits) {
@@ -62,26 +64,42 @@ __device__ __forceinline__ int slot_key(const int32_t* ids, int i, int groups) {
     return static_cast<uint32_t>(id) < static_cast<uint32_t>(groups) ? id : groups;
 }
 
-// Ids per chunk: counts[chunk][keys].
+// The keys of a wave's steps of a chunk [s0, s1) (`keys` past its end): each wave
+// takes a contiguous part. One memory round trip for all of them.
+__device__ __forceinline__ void load_keys(const int32_t* __restrict__ ids, int s0, int s1, int groups,
+                                          int keys, int& first, int& steps, int (&key)[kMaxSteps]) {
+    steps = (s1 - s0 + kSortThreads - 1) / kSortThreads;
+    first = s0 + static_cast<int>(threadIdx.x >> 6) * steps * kWave + (threadIdx.x & 63);
+#pragma unroll
+    for (int s = 0; s < kMaxSteps; ++s) {
+        const int i = first + s * kWave;
+        key[s] = s < steps && i < s1 ? slot_key(ids, i, groups) : keys;
+    }
+}
+
+// Ids per chunk: counts[chunk][keys]. Equal keys of a wave's step are added by
+// one lane (runs of one key would queue up at one counter otherwise).
 __global__ __launch_bounds__(kSortThreads) void route_count_kernel(
     const int32_t* __restrict__ ids, int slots, int groups, int keys, int chunk,
     int32_t* __restrict__ counts) {
     __shared__ int hist[kMaxKeys];
+    const int s0 = blockIdx.x * chunk, s1 = min(slots, s0 + chunk);
+    const int lane = threadIdx.x & 63, bits = 32 - __clz(keys);
+    int first, steps, key[kMaxSteps];
+    load_keys(ids, s0, s1, groups, keys, first, steps, key);
     for (int g = threadIdx.x; g < keys; g += kSortThreads) hist[g] = 0;
     __syncthreads();
-    const int s0 = blockIdx.x * chunk, s1 = min(slots, s0 + chunk);
-    for (int i = s0 + threadIdx.x; i < s1; i += kSortThreads) {
-        const int key = slot_key(ids, i, groups);
-        if (key < keys) atomicAdd(&hist[key], 1);
+#pragma unroll
+    for (int s = 0; s < kMaxSteps; ++s) {
+        if (s >= steps) break;
+        const bool live = key[s] < keys;
+        const uint64_t same = same_key(key[s], live, bits);
+        if (live && (same >> lane) == 1) atomicAdd(&hist[key[s]], __popcll(same));
     }
     __syncthreads();
     for (int g = threadIdx.x; g < keys; g += kSortThreads)
         counts[static_cast<size_t>(blockIdx.x) * keys + g] = hist[g];
 }
-
-// The ids of a wave's first kKeptSteps steps stay in registers between counting
-// and placing: one memory round trip for all of them instead of two per step.
-constexpr int kKeptSteps = kSingleSlots / kSortThreads;
 
 // Places of one chunk's slots. keys = groups, or groups + 1 where the slots
 // outside every group are kept as one more group behind the others (then
@@ -91,37 +109,37 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
     const int32_t* __restrict__ ids, int slots, int groups, int keys, int chunk,
     const int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ order, int32_t* __restrict__ position) {
-    // counts of each wave's part, then the next place of each (wave, key)
+    // counts of each wave's part, then the first place of each (wave, key)
     __shared__ int next[kSortWaves * kMaxKeys];
     __shared__ int part[kSortWaves + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int chunks = gridDim.x;
     const int s0 = blockIdx.x * chunk, s1 = min(slots, s0 + chunk);
-    // each wave takes a contiguous part of the chunk, in steps of 64 slots
-    const int steps = (s1 - s0 + kSortThreads - 1) / kSortThreads;
-    const int w0 = s0 + wave * steps * kWave, w1 = min(s1, w0 + steps * kWave);
-    int kept[kKeptSteps];
-#pragma unroll
-    for (int s = 0; s < kKeptSteps; ++s) {
-        const int i = w0 + s * kWave + lane;
-        kept[s] = i < w1 ? slot_key(ids, i, groups) : keys;
-    }
+    const int bits = 32 - __clz(keys);
+    int first, steps, key[kMaxSteps], local[kMaxSteps];
+    load_keys(ids, s0, s1, groups, keys, first, steps, key);
     for (int g = tid; g < kSortWaves * keys; g += kSortThreads) next[g] = 0;
     __syncthreads();
+    // place of each slot among its wave's slots of the same key
 #pragma unroll
-    for (int s = 0; s < kKeptSteps; ++s)
-        if (kept[s] < keys) atomicAdd(&next[wave * keys + kept[s]], 1);
-    for (int i = w0 + kKeptSteps * kWave + lane; i < w1; i += kWave) {
-        const int key = slot_key(ids, i, groups);
-        if (key < keys) atomicAdd(&next[wave * keys + key], 1);
+    for (int s = 0; s < kMaxSteps; ++s) {
+        if (s >= steps) break;
+        const bool live = key[s] < keys;
+        const uint64_t same = same_key(key[s], live, bits);
+        int* n = next + wave * keys + key[s];
+        local[s] = live ? *n + __popcll(same & ((1ull << lane) - 1)) : 0;
+        wave_lds_sync();  // every lane has read its key's count
+        if (live && (same >> lane) == 1) *n = local[s] + 1;  // the last lane of its key
+        wave_lds_sync();
     }
     __syncthreads();
     // Per key: slots of all chunks, of earlier chunks, and of earlier waves.
-    int base = 0;  // first place of the keys before this round
+    int base = 0;  // first place of the keys of this round
     for (int g0 = 0; g0 < keys; g0 += kSortThreads) {
         const int g = g0 + tid;
         int mine = 0, earlier = 0, all = 0;
         if (g < keys) {
+#pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
                 const int n = next[w * keys + g];
                 next[w * keys + g] = mine;
@@ -139,32 +157,24 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
             }
         }
         int total;
-        const int first = base + scan_workgroup(all, part, &total);
+        const int place = base + scan_workgroup(all, part, &total);
         if (g < keys) {
-            for (int w = 0; w < kSortWaves; ++w) next[w * keys + g] += first + earlier;
-            if (blockIdx.x == 0) offsets[g] = first;
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) next[w * keys + g] += place + earlier;
+            if (blockIdx.x == 0) offsets[g] = place;
         }
         base += total;
         __syncthreads();  // `part` is written again, and `next` is read by all waves
     }
     if (blockIdx.x == 0 && tid == 0) offsets[keys] = base;
-    const int bits = 32 - __clz(keys);
-    auto place_step = [&](int i, int key) {
-        const bool live = key < keys;
-        const uint64_t same = same_key(key, live, bits);
-        int place = -1;
-        if (live) place = next[wave * keys + key] + __popcll(same & ((1ull << lane) - 1));
-        wave_lds_sync();  // every lane has read its key's next place
-        if (live && (same >> lane) == 1) next[wave * keys + key] = place + 1;  // the last of its key
-        wave_lds_sync();
-        if (i < w1 && position) position[i] = place;
-        if (live) order[place] = i;
-    };
 #pragma unroll
-    for (int s = 0; s < kKeptSteps; ++s)
-        if (w0 + s * kWave < w1) place_step(w0 + s * kWave + lane, kept[s]);
-    for (int i0 = w0 + kKeptSteps * kWave; i0 < w1; i0 += kWave)
-        place_step(i0 + lane, i0 + lane < w1 ? slot_key(ids, i0 + lane, groups) : keys);
+    for (int s = 0; s < kMaxSteps; ++s) {
+        const int i = first + s * kWave;
+        if (s >= steps || i >= s1) break;
+        const int place = key[s] < keys ? next[wave * keys + key[s]] + local[s] : -1;
+        if (position) position[i] = place;
+        if (place >= 0) order[place] = i;
+    }
     for (int p = max(base, s0) + tid; p < s1; p += kSortThreads) order[p] = -1;
 }
 
@@ -287,6 +297,8 @@ __global__ __launch_bounds__(kMoveThreads) void combine_backward_kernel(
     }
 }
 
+// Slots per workgroup, a multiple of kSortThreads between kChunkSlots and
+// kMaxChunkSlots.
 int chunk_slots(int slots) {
     const int even = (slots + kMaxChunks - 1) / kMaxChunks;
     return even > kChunkSlots ? (even + kSortThreads - 1) / kSortThreads * kSortThreads
@@ -301,7 +313,7 @@ dim3 move_grid(int width, int tokens, bool vec) {
 }  // namespace
 
 size_t route_workspace_bytes(int slots, int keys) {
-    if (slots <= kSingleSlots) return 0;
+    if (slots <= kOneChunk) return 0;
     const int chunk = chunk_slots(slots);
     return static_cast<size_t>((slots + chunk - 1) / chunk) * keys * sizeof(int32_t);
 }
@@ -309,9 +321,9 @@ size_t route_workspace_bytes(int slots, int keys) {
 hipError_t launch_route(const int32_t* ids, int slots, int groups, bool tail, int32_t* offsets,
                         int32_t* order, int32_t* position, int32_t* counts, hipStream_t st) {
     const int keys = groups + (tail ? 1 : 0);
-    if (slots <= kSingleSlots)
+    if (slots <= kOneChunk)
         return launch_kernel(route_place_kernel, dim3(1), dim3(kSortThreads), st, ids, slots,
-                             groups, keys, kSingleSlots, nullptr, offsets, order, position);
+                             groups, keys, kOneChunk, nullptr, offsets, order, position);
     const int chunk = chunk_slots(slots), chunks = (slots + chunk - 1) / chunk;
     const hipError_t e = launch_kernel(route_count_kernel, dim3(chunks), dim3(kSortThreads), st, ids,
                                        slots, groups, keys, chunk, counts);

@@ -31,7 +31,7 @@ extern "C" {
 #define TRELLIS_MAX_GROUPS 1024
 
 /* Largest number of slots (tokens x top_k) or rows of one call. */
-#define TRELLIS_MAX_SLOTS (1 << 24)
+#define TRELLIS_MAX_SLOTS (1 << 21)
 
 /*
  * Sort slots by group. ids: int32 [tokens][top_k]; slot i = token * top_k +

@@ -40,7 +40,7 @@ def test_route_validation(T):
         return call(T, "trellis_route", ROUTE, ROUTE_ARGS, **kw)
 
     for kw in (dict(tokens=-1), dict(top_k=0), dict(groups=0), dict(groups=1025),
-               dict(tokens=1 << 24, top_k=2), dict(tokens=2 ** 31 - 1, top_k=2 ** 31 - 1)):
+               dict(tokens=1 << 20, top_k=3), dict(tokens=2 ** 31 - 1, top_k=2 ** 31 - 1)):
         assert route(**kw) == T.ERR_GEOMETRY, kw
     for arg in ("ids", "offsets", "order", "position"):
         assert route(**{arg: 0}) == T.ERR_NULL, arg
@@ -57,8 +57,8 @@ def test_route_workspace_bytes(T):
     none = C.c_size_t(-1).value
     assert f(4096, 2, 128) == 0                      # one workgroup sorts these
     assert f(4097, 2, 128) == 5 * 128 * 4            # five chunks of 2048 slots
-    assert f(1 << 24, 1, 1024) == 256 * 1024 * 4     # never more than 256 chunks
-    for bad in ((-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 1025), (1 << 24, 2, 1)):
+    assert f(1 << 21, 1, 1024) == 256 * 1024 * 4     # never more than 256 chunks
+    for bad in ((-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 1025), (1 << 20, 3, 1)):
         assert f(*bad) == none, bad
 
 
@@ -80,7 +80,7 @@ def test_moves_validation(T, name):
         return call(T, name, order, args, **kw)
 
     for kw in (dict(tokens=-1), dict(top_k=0), dict(width=0), dict(width=(1 << 19) + 1),
-               dict(tokens=1 << 23, top_k=3)):
+               dict(tokens=1 << 20, top_k=3)):
         assert move(**kw) == T.ERR_GEOMETRY, kw
     for arg in order:
         if arg[0] == "#":
@@ -220,7 +220,7 @@ def test_experts_validation(T, axis):
                 T.Geometry(axis, 256, 12, 3, 0, 256, 0), T.Geometry(axis, 256, 12, 3, 300, 300, 0)):
         assert experts(bad) == T.ERR_GEOMETRY
         assert T.raw().trellis_experts_workspace_bytes(C.byref(bad), 10, 4) == C.c_size_t(-1).value
-    for kw in (dict(rows=-1), dict(rows=(1 << 24) + 1), dict(experts=0), dict(experts=1025)):
+    for kw in (dict(rows=-1), dict(rows=(1 << 21) + 1), dict(experts=0), dict(experts=1025)):
         assert experts(**kw) == T.ERR_GEOMETRY, kw
     for arg in ("x", "offsets", "codes", "scales", "lut", "y"):
         assert experts(**{arg: 0}) == T.ERR_NULL, arg
