@@ -368,21 +368,19 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
     }
     const uint16_t* f = factor + static_cast<size_t>(ti.group) * rank * width;
     const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * 32;
-    // every lane's rows first: a row's number read between the rows' loads would
-    // wait for all of them
-    int rows_at[kSubs][4];
-#pragma unroll
-    for (int s = 0; s < kSubs; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rows_at[s][i] = trow[16 * s + 4 * c + i];
+    // a row's number read from memory between the rows' loads would wait for
+    // all of them: each lane holds one and passes it on
+    const int my_row = trow[lane];
     u32x4 op[R ? R : 1][8];
 #pragma unroll
     for (int r = 0; r < R; ++r) factor_operands<VEC>(f, r, rank, col, width, c, op[r]);
     static_for<0, kSubs>([&](auto sub) {
         constexpr int s = decltype(sub)::value;
         if (16 * s >= ti.rows) return;
-        const int (&row)[4] = rows_at[s];
+        int row[4];
         u32x4 bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = __shfl(my_row, 16 * s + 4 * c + i);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             bv[i] = load8<VEC>(base + static_cast<size_t>(max(row[i], 0)) * width, col, width,
