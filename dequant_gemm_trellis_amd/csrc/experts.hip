@@ -59,6 +59,15 @@ __device__ __forceinline__ int count_tiles(const int32_t* __restrict__ offsets, 
     return __builtin_amdgcn_readfirstlane(n);
 }
 
+// A load from a uniform address plus an offset per lane. The offset is opaque, or
+// the compiler adds it to a loop's invariant base and keeps 64-bit addresses in
+// vector registers.
+template <typename T>
+__device__ __forceinline__ T load_at(const void* uniform, uint32_t lane_bytes) {
+    asm volatile("" : "+v"(lane_bytes));
+    return *reinterpret_cast<const T*>(static_cast<const char*>(uniform) + lane_bytes);
+}
+
 // Where the units of a launch are: `units` of them, this workgroup's (or
 // wave's) every `step`-th from `first` on below `end`. Each XCD takes a
 // contiguous range, so that strips of one tile share its rows in one L2.
@@ -85,9 +94,12 @@ struct ExArgs {
     uint16_t* y;
 };
 
-// x of a tile in operand order: [tile][block][S][MT] operands of 64 lanes x 16
-// bytes; rows past the tile's last are zeros. Grid: (tiles, blocks).
-template <int MT>
+// x of a tile in operand order, [tile][step][MT] operands of 64 lanes x 16 bytes;
+// rows past the tile's last are zeros. A wave's load of an operand is then 1 KB
+// in a row; taken from the rows it is 16 pieces of 64 bytes (axis 0; measured
+// 343 us against 230 with this order for 16384 rows of 1536 -> 2048 at k = 4)
+// or 64 of 16 bytes (axis 1). Grid: (tiles, 256 contracted values).
+template <int MT, int AXIS, bool VEC>
 __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restrict__ x,
                                                        const int32_t* __restrict__ offsets,
                                                        int experts, int rows, int in,
@@ -96,18 +108,32 @@ __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restric
     if (at.group < 0) return;
     const int row0 = at.first + at.index * 16 * MT;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
-    const size_t base = (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * 8 * MT;
-    // S fastest within a wave: the eight reads of a lane come from one line
-    for (int o = threadIdx.x >> 6; o < MT; o += 4) {
-        const int row = row0 + 16 * o + j;
-        const uint16_t* p = x + static_cast<size_t>(row) * in + 256 * blockIdx.y + 64 * c;
-        u32x4 v[8] = {};
-        if (row < at.end) {
+    const int steps = (in + 31) / 32, s0 = 8 * blockIdx.y, n = min(8, steps - s0);
+    u32x4* o = out + (static_cast<size_t>(blockIdx.x) * steps + s0) * MT * 64 + lane;
+    // the reads of a lane (axis 1) or of a lane group (axis 0) come from one line
+    for (int m = threadIdx.x >> 6; m < MT; m += 4) {
+        const int row = row0 + 16 * m + j;
+        const uint16_t* p = x + static_cast<size_t>(min(row, at.end - 1)) * in;
+        u32x4 v[8];
 #pragma unroll
-            for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const u32x4*>(p + 8 * s);
+        for (int s = 0; s < 8; ++s) {
+            const int step = min(s0 + s, steps - 1);
+            // axis 1: step s of a block is weights 64 c + 8 s; axis 0: 32 rows in
+            // a row, the last step's the last 32
+            const int first = AXIS == 1 ? 8 * s + 256 * static_cast<int>(blockIdx.y) + 64 * c
+                                        : min(32 * step, in - 32) + 8 * c;
+            v[s] = load8<VEC>(p, first, in, row < at.end);
+            if (AXIS == 0) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {  // values already counted
+                    if (first + 2 * d < 32 * step) v[s][d] &= 0xFFFF0000u;
+                    if (first + 2 * d + 1 < 32 * step) v[s][d] &= 0x0000FFFFu;
+                }
+            }
         }
 #pragma unroll
-        for (int s = 0; s < 8; ++s) out[(base + s * MT + o) * 64 + lane] = v[s];
+        for (int s = 0; s < 8; ++s)
+            if (s < n) o[(s * MT + m) * 64] = v[s];
     }
 }
 
@@ -127,7 +153,6 @@ __global__ __launch_bounds__(kExThreads) void experts1_kernel(ExArgs p) {
         const int t = u / strips, n0 = (u - t * strips) * 16 * G;
         const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
         const int row0 = at.first + at.index * 16 * MT;
-        const int live = __builtin_amdgcn_readfirstlane(min(MT, (at.end - row0 + 15) / 16));
         const uint32_t* codes = p.codes + at.group * p.words;
         const float* scales = p.scales + static_cast<size_t>(at.group) * p.out;
         int rowc[G];
@@ -144,19 +169,25 @@ __global__ __launch_bounds__(kExThreads) void experts1_kernel(ExArgs p) {
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 load_run64<K>(codes + block_word<K>(p.lay, rowc[g], b), 3 - c, w[g]);
-            static_for<0, 8>([&](auto sc_) {
-                constexpr int S = decltype(sc_)::value;
-                u32x4 a[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) a[m] = xo[(static_cast<size_t>(8 * b + S) * MT + m) * 64];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const u32x4 f = pack_fragment(gather_tab<K, S, pair, rep>(w[g], tab), sc[g]);
+            // fragment i is step i / G of group i % G; its values are read one
+            // fragment ahead
+            u32x4 a[MT];
+            Gathered<pair> v[2];
+            v[0] = gather_tab<K, 0, pair, rep>(w[0], tab);
+            static_for<0, 8 * G>([&](auto ic) {
+                constexpr int i = decltype(ic)::value, S = i / G, g = i % G, n = i + 1;
+                if constexpr (g == 0) {
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        if (m < live)
-                            acc[g][m] = mfma16x16x32(as_bf16x8(a[m]), as_bf16x8(f), acc[g][m]);
+                        a[m] = xo[(static_cast<size_t>(8 * b + S) * MT + m) * 64];
                 }
+                __builtin_amdgcn_s_setprio(2);
+                if constexpr (n < 8 * G) v[n & 1] = gather_tab<K, n / G, pair, rep>(w[n % G], tab);
+                __builtin_amdgcn_s_setprio(0);
+                const u32x4 f = pack_fragment(v[i & 1], sc[g]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    acc[g][m] = mfma16x16x32(as_bf16x8(a[m]), as_bf16x8(f), acc[g][m]);
             });
         }
 #pragma unroll
@@ -174,176 +205,257 @@ __global__ __launch_bounds__(kExThreads) void experts1_kernel(ExArgs p) {
     }
 }
 
-// Sum of the waves' [16][128] parts in wave order (parts of wave groups that
-// own other columns are kept apart by the caller's columns).
-__device__ __forceinline__ void add_part(float* sum, int col, int c, const floatx4& v, bool first) {
+// ---- few rows per expert: a workgroup's waves share a strip's contraction ---------
+
+// Partial sums of up to four waves, [part][16][128]; the columns of a row are
+// swizzled by its lane group, so that the 64 lanes of a store hit all banks.
+constexpr int kParts = 4;
+constexpr int kPartFloats = 16 * kStripCols;
+__device__ __forceinline__ int part_at(int row, int col) {
+    return row * kStripCols + (col ^ (16 * (row >> 2)));
+}
+
+// The sums of a tile's strip from the waves' parts, in a fixed order: wave q
+// adds wave q + 4's part to its own, then the four meet, part 0 first. WAYS
+// waves (1, 2, 4 or 8) share each column; way `q` of them is this wave's, its
+// values given by each(f): f(row, column, value). Every wave of the workgroup
+// calls it; a strip of columns [col0, col0 + 128) of rows [row0, end).
+template <int WAYS, typename F>
+__device__ __forceinline__ void sum_strip(float* parts, int q, F&& each, uint16_t* __restrict__ y,
+                                          int row0, int end, int col0, int out) {
+    __syncthreads();  // the parts of the strip before are read
+    if (WAYS > kParts) {
+        if (q >= kParts)
+            each([&](int row, int col, float v) { parts[(q - kParts) * kPartFloats + part_at(row, col)] = v; });
+        __syncthreads();
+        if (q < kParts)
+            each([&](int row, int col, float v) { parts[q * kPartFloats + part_at(row, col)] += v; });
+    } else {
+        each([&](int row, int col, float v) { parts[q * kPartFloats + part_at(row, col)] = v; });
+    }
+    __syncthreads();
+    constexpr int n = WAYS < kParts ? WAYS : kParts;
+    const int row = threadIdx.x / (kStripCols / 4), c4 = 4 * (threadIdx.x % (kStripCols / 4));
+    if (row0 + row >= end) return;
+    floatx4 v = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float* o = sum + (4 * c + i) * kStripCols + col;
-        *o = first ? v[i] : *o + v[i];
+    for (int k = 0; k < n; ++k) v += *reinterpret_cast<const floatx4*>(parts + k * kPartFloats + part_at(row, c4));
+    uint16_t* o = y + static_cast<size_t>(row0 + row) * out + col0 + c4;
+    const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+    if (out % 4 == 0) {
+        if (col0 + c4 < out) *reinterpret_cast<uint2*>(o) = uint2{lo, hi};
+    } else {
+        if (col0 + c4 < out) o[0] = static_cast<uint16_t>(lo);
+        if (col0 + c4 + 1 < out) o[1] = static_cast<uint16_t>(lo >> 16);
+        if (col0 + c4 + 2 < out) o[2] = static_cast<uint16_t>(hi);
+        if (col0 + c4 + 3 < out) o[3] = static_cast<uint16_t>(hi >> 16);
+    }
+}
+static_assert(kExThreads == 16 * kStripCols / 4, "a thread sums four columns of a row");
+
+// A strip of a tile of 16 rows.
+struct Unit {
+    int group, row0, end, col0;
+};
+__device__ __forceinline__ Unit unit_at(const ExArgs& p, int u, int strips) {
+    const int t = u / strips;
+    const Found at = find_entry(p.offsets, p.experts, p.rows, 16, false, t);
+    return {at.group, at.first + 16 * at.index, at.end, (u - t * strips) * kStripCols};
+}
+
+// A wave's work over its strips: pieces (a block or a 32-row step) from `first`
+// on, every `stride`-th below `pieces` of every strip of `r`. load(work, unit,
+// piece) of the next piece is in flight while multiply(work) runs;
+// finish(unit) follows a strip's last piece.
+template <typename Work, typename Load, typename Between, typename Multiply, typename Finish>
+__device__ __forceinline__ void run_units(const ExArgs& p, const Range& r, int strips, int first,
+                                          int stride, int pieces, Load&& load, Between&& between,
+                                          Multiply&& multiply, Finish&& finish) {
+    int u = r.first, piece = first;
+    Unit unit = {};
+    Work q[2];
+    if (u < r.end) {
+        unit = unit_at(p, u, strips);
+        if (piece < pieces) load(q[0], unit, piece);
+    }
+    between();
+    auto one = [&](Work& now, Work& next) {
+        int nu = u, np = piece + stride;
+        Unit nunit = unit;
+        if (np >= pieces) {
+            np = first;
+            nu = u + r.step;
+            if (nu < r.end) nunit = unit_at(p, nu, strips);
+        }
+        if (nu < r.end && np < pieces) load(next, nunit, np);
+        if (piece < pieces) multiply(now);
+        if (nu != u) finish(unit);
+        u = nu;
+        piece = np;
+        unit = nunit;
+    };
+    while (u < r.end) {
+        one(q[0], q[1]);
+        if (u < r.end) one(q[1], q[0]);
     }
 }
 
-// Axis 1, tiles of 16 rows: a workgroup takes 128 output columns of a tile; its
-// waves are G ways along the contraction (8 blocks at a time) and 8 / G along
-// the columns, G 16-column groups each.
+// Axis 1: the waves are G ways along the contraction (a block each at a time)
+// and 8 / G along the columns, G 16-column groups each.
 template <int K, int G>
 __global__ __launch_bounds__(kExThreads) void experts1_few_kernel(ExArgs p) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
-    __shared__ float sum[16 * kStripCols];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(16))) float parts[kParts * kPartFloats];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
-    const int kw = wave % G, nw = wave / G;
-    stage_table<K>(tab, p.lut);
+    const int kw = wave % G, first = (wave / G) * 16 * G;  // this wave's way and its columns
     const int nb = p.in / kT, strips = (p.out + kStripCols - 1) / kStripCols;
     const int tiles = count_tiles(p.offsets, p.experts, p.rows, 16);
-    const Range r = xcd_range(tiles * strips, 1, 0);
-    for (int u = r.first; u < r.end; u += r.step) {
-        const int t = u / strips, n0 = (u - t * strips) * kStripCols + nw * 16 * G;
-        const Found at = find_entry(p.offsets, p.experts, p.rows, 16, false, t);
-        const int row0 = at.first + at.index * 16;
-        const uint32_t* codes = p.codes + at.group * p.words;
-        const float* scales = p.scales + static_cast<size_t>(at.group) * p.out;
-        int rowc[G];
+    struct Work {
+        uint32_t w[G][2 * K + 1];
         float sc[G];
+        u32x4 a[8];
+    };
+    floatx4 acc[G] = {};
+    run_units<Work>(
+        p, xcd_range(tiles * strips, 1, 0), strips, kw, G, nb,
+        [&](Work& q, const Unit& un, int b) {
+            const uint32_t* codes = p.codes + un.group * p.words;
+            const float* scales = p.scales + static_cast<size_t>(un.group) * p.out;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            rowc[g] = min(n0 + 16 * g + j, p.out - 1);
-            sc[g] = scales[rowc[g]];
-        }
-        const uint16_t* xr = p.x + static_cast<size_t>(min(row0 + j, at.end - 1)) * p.in + 64 * c;
-        floatx4 acc[G] = {};
-        for (int b = kw; b < nb; b += G) {
-            uint32_t w[G][2 * K + 1];
-            u32x4 a[8];
+            for (int g = 0; g < G; ++g) {
+                const int row = min(un.col0 + first + 16 * g + j, p.out - 1);
+                load_run64<K>(codes + block_word<K>(p.lay, row, b), 3 - c, q.w[g]);
+                q.sc[g] = scales[row];
+            }
+            const uint16_t* x = p.x + static_cast<size_t>(min(un.row0 + j, un.end - 1)) * p.in +
+                                static_cast<size_t>(b) * kT + 64 * c;
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                load_run64<K>(codes + block_word<K>(p.lay, rowc[g], b), 3 - c, w[g]);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                a[s] = *reinterpret_cast<const u32x4*>(xr + static_cast<size_t>(b) * kT + 8 * s);
+            for (int s = 0; s < 8; ++s) q.a[s] = *reinterpret_cast<const u32x4*>(x + 8 * s);
+        },
+        [&] { stage_table<K>(tab, p.lut); },
+        [&](const Work& q) {
             static_for<0, 8>([&](auto sc_) {
                 constexpr int S = decltype(sc_)::value;
 #pragma unroll
                 for (int g = 0; g < G; ++g)
                     acc[g] = mfma16x16x32(
-                        as_bf16x8(a[S]),
-                        as_bf16x8(pack_fragment(gather_tab<K, S, pair, rep>(w[g], tab), sc[g])),
+                        as_bf16x8(q.a[S]),
+                        as_bf16x8(pack_fragment(gather_tab<K, S, pair, rep>(q.w[g], tab), q.sc[g])),
                         acc[g]);
             });
-        }
-        for (int q = 0; q < G; ++q) {
-            if (kw == q) {
+        },
+        [&](const Unit& un) {
+            sum_strip<G>(parts, kw, [&](auto&& f) {
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    add_part(sum, nw * 16 * G + 16 * g + j, c, acc[g], q == 0);
-            }
-            __syncthreads();
-        }
-        const int first = (u - t * strips) * kStripCols;
-        for (int i = tid; i < 16 * kStripCols; i += kExThreads) {
-            const int row = row0 + i / kStripCols, n = first + i % kStripCols;
-            if (row < at.end && n < p.out)
-                p.y[static_cast<size_t>(row) * p.out + n] = round_bf16(sum[i]);
-        }
-        __syncthreads();  // `sum` is written again by the next unit
-    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f(4 * c + i, first + 16 * g + j, acc[g][i]);
+            }, p.y, un.row0, un.end, un.col0, p.out);
+#pragma unroll
+            for (int g = 0; g < G; ++g) acc[g] = floatx4{};
+        });
 }
 
 // ---- axis 0 ---------------------------------------------------------------------
 
-// One 32-row step of a wave's strip: the two words that hold the windows of a
-// lane's 8 columns in each of its 8 stored rows, and the rows' scales.
-struct Patch {
+// Words of one 32-row step of a wave's strip, CL adjacent columns per lane: the
+// two that hold a lane's windows in each of its 8 stored rows.
+struct Words {
     uint32_t a[8], b[8];
-    float sc[8];
 };
 
 struct Strip0 {
-    const uint32_t* codes;  // the strip's block in stored row 0
+    const uint32_t* codes;   // the strip's block in stored row 0
     const float* scales;
     uint64_t row_words;
-    int w0, w1, sh, in, c;
+    uint32_t at_a, at_b;     // bytes from a step's first row to the words of the lane's first row
+    int sh;                  // where the windows start in the first word
 };
 
-template <int K>
+template <int K, int CL>
 __device__ __forceinline__ Strip0 strip0(const ExArgs& p, int expert, int col0, int j, int c) {
     constexpr int wpb = Bits<K>::wpb;
-    const int t0 = (col0 % kT) + 8 * j;  // first weight of this lane's 8 columns
-    const int lo = (kT - 8 - t0) * K;    // bit of weight t0 + 7
-    Strip0 s;
-    s.codes = p.codes + expert * p.words + block_word<K>(p.lay, 0, col0 / kT);
-    s.scales = p.scales + static_cast<size_t>(expert) * p.in;
-    s.row_words = p.lay.row_words;
-    s.w0 = lo >> 5;
-    s.sh = lo & 31;
-    s.w1 = s.w0 + 1 == wpb ? 0 : s.w0 + 1;  // tail-biting wrap
-    s.in = p.in;
-    s.c = c;
-    return s;
+    const int t0 = (col0 % kT) + CL * j;  // first weight of this lane's columns
+    const int lo = (kT - CL - t0) * K;    // bit of its last weight
+    const int w0 = lo >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1;  // tail-biting wrap
+    const uint32_t row = static_cast<uint32_t>(8 * c * p.lay.row_words);
+    return {p.codes + expert * p.words + block_word<K>(p.lay, 0, col0 / kT),
+            p.scales + static_cast<size_t>(expert) * p.in, p.lay.row_words, 4 * (row + w0),
+            4 * (row + w1), lo & 31};
 }
 
-__device__ __forceinline__ void load_patch(Patch& q, const Strip0& s, int step) {
+typedef floatx4 floatx4_a4 __attribute__((aligned(4)));
+
+// Loads of 32 whole rows from row0 on: a uniform row plus an offset per lane.
+__device__ __forceinline__ void load_words(Words& q, const Strip0& s, int row0) {
+    const uint32_t* row = s.codes + static_cast<uint64_t>(row0) * s.row_words;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int row = min(32 * step + 8 * s.c + i, s.in - 1);  // past the end: x is zero there
-        const uint32_t* w = s.codes + row * s.row_words;
-        q.a[i] = w[s.w0];
-        q.b[i] = w[s.w1];
-        q.sc[i] = s.scales[row];
+        q.a[i] = load_at<uint32_t>(row + i * s.row_words, s.at_a);
+        q.b[i] = load_at<uint32_t>(row + i * s.row_words, s.at_b);
     }
 }
 
-// The eight operands of a patch, column by column (k = 2: by pairs), each
-// multiplied with the tile's x operands.
-template <int K, int MT>
-__device__ __forceinline__ void mul_patch(const Patch& q, const Strip0& s, const float* tab,
-                                          const u32x4 (&x)[MT], int live, floatx4 (&acc)[8][MT]) {
-    uint32_t g[8][2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        g[i][0] = __builtin_amdgcn_alignbit(q.b[i], q.a[i], s.sh);
-        g[i][1] = q.b[i] >> s.sh;
-    }
-    auto mul = [&](auto ec, const u32x4& f) {
-        constexpr int e = decltype(ec)::value;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            if (MT == 1 || m < live)
-                acc[e][m] = mfma16x16x32(as_bf16x8(x[m]), as_bf16x8(f), acc[e][m]);
+// A step's operands come in pieces: a column, or for k = 2 a pair of columns.
+// Their codebook values are read a piece ahead of their use.
+template <int K, int CL>
+struct Pieces {
+    static constexpr bool pair = ExTable<K>::pair;
+    static constexpr int cols = pair ? 2 : 1, n = CL / cols;
+    static constexpr int words = (CL - 1) * K + kL <= 32 ? 1 : 2;  // of a row's windows
+    struct Values {
+        float v[8][cols];
     };
-    if constexpr (ExTable<K>::pair) {
-        static_for<0, 4>([&](auto pc) {
-            constexpr int P = decltype(pc)::value, O = (6 - 2 * P) * K;
-            floatx2 v[8];
+    uint32_t g[8][words];
+
+    __device__ __forceinline__ void set(const Words& q, int sh) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lds_pair(tab, field_offset<O, 14, 3>(g[i]));
-            u32x4 f0, f1;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                f0[d] = pack_bf16(v[2 * d].x * q.sc[2 * d], v[2 * d + 1].x * q.sc[2 * d + 1]);
-                f1[d] = pack_bf16(v[2 * d].y * q.sc[2 * d], v[2 * d + 1].y * q.sc[2 * d + 1]);
-            }
-            mul(std::integral_constant<int, 2 * P>{}, f0);
-            mul(std::integral_constant<int, 2 * P + 1>{}, f1);
-        });
-    } else {
+        for (int i = 0; i < 8; ++i) {
+            g[i][0] = __builtin_amdgcn_alignbit(q.b[i], q.a[i], sh);
+            if constexpr (words == 2) g[i][1] = q.b[i] >> sh;
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void gather(Values& o, const float* tab) const {
         const uint32_t copy = rep_lane_offset();
-        static_for<0, 8>([&](auto ec) {
-            constexpr int e = decltype(ec)::value, o = (7 - e) * K;
-            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = lds_lut(tab, field_offset<o, kL, 5>(g[i]) | copy);
-            u32x4 f;
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (pair) {
+                const floatx2 v = lds_pair(tab, field_offset<(CL - 2 - 2 * P) * K, 14, 3>(g[i]));
+                o.v[i][0] = v.x;
+                o.v[i][1] = v.y;
+            } else {
+                o.v[i][0] = lds_lut(tab, field_offset<(CL - 1 - P) * K, kL, 5>(g[i]) | copy);
+            }
+        }
+    }
+    // Column C of a piece, scaled by the rows' scales.
+    template <int C>
+    static __device__ __forceinline__ u32x4 pack(const Values& o, const float (&sc)[8]) {
+        u32x4 f;
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-                f[d] = pack_bf16(v[2 * d] * q.sc[2 * d], v[2 * d + 1] * q.sc[2 * d + 1]);
-            mul(ec, f);
+        for (int d = 0; d < 4; ++d)
+            f[d] = pack_bf16(o.v[2 * d][C] * sc[2 * d], o.v[2 * d + 1][C] * sc[2 * d + 1]);
+        return f;
+    }
+    // Every column's operand to mul(column, operand).
+    template <typename F>
+    __device__ __forceinline__ void each(const float (&sc)[8], const float* tab, F&& mul) const {
+        Values v[2];
+        gather<0>(v[0], tab);
+        static_for<0, n>([&](auto pc) {
+            constexpr int P = decltype(pc)::value;
+            if constexpr (P + 1 < n) gather<P + 1>(v[(P + 1) & 1], tab);
+            static_for<0, cols>([&](auto cc) {
+                constexpr int C = decltype(cc)::value;
+                mul(std::integral_constant<int, cols * P + C>{}, pack<C>(v[P & 1], sc));
+            });
         });
     }
-}
+};
 
 // x operand of 16 rows from row0 on (rows past `end` read the last), step `step`.
 template <bool VEC>
@@ -352,36 +464,65 @@ __device__ __forceinline__ u32x4 x_operand(const ExArgs& p, int row0, int end, i
     return load8<VEC>(p.x + static_cast<size_t>(row) * p.in, 32 * step + 8 * c, p.in, true);
 }
 
-template <int K, int MT, bool VEC>
+// Tiles of MT x 16 rows: a wave takes 64 columns of a tile, 4 per lane. A last
+// step of fewer than 32 rows takes the last 32 stored rows again, with zeros in
+// the x operands for those already counted (operands_kernel); in >= 32.
+template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
+    constexpr int CL = 4;
+    using Ps = Pieces<K, CL>;
     __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
     stage_table<K>(tab, p.lut);
-    const int steps = (p.in + 31) / 32, strips = p.out / kStripCols;
+    const int steps = (p.in + 31) / 32, strips = p.out / (16 * CL);
     const int tiles = count_tiles(p.offsets, p.experts, p.rows, 16 * MT);
     const Range r = xcd_range(tiles * strips, kExWaves, wave);
     for (int u = r.first; u < r.end; u += r.step) {
-        const int t = u / strips, col0 = (u - t * strips) * kStripCols;
+        const int t = u / strips, col0 = (u - t * strips) * 16 * CL;
         const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
         const int row0 = at.first + at.index * 16 * MT;
-        const int live = __builtin_amdgcn_readfirstlane(min(MT, (at.end - row0 + 15) / 16));
-        const Strip0 s = strip0<K>(p, at.group, col0, j, c);
-        floatx4 acc[8][MT] = {};
-        Patch q[2];
-        load_patch(q[0], s, 0);
-        auto one = [&](Patch& now, Patch& next, int step) {
-            u32x4 x[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-                x[m] = x_operand<VEC>(p, min(row0 + 16 * m, at.end - 1), at.end, step, j, c);
-            if (step + 1 < steps) load_patch(next, s, step + 1);
-            mul_patch<K, MT>(now, s, tab, x, live, acc);
+        const Strip0 s = strip0<K, CL>(p, at.group, col0, j, c);
+        auto first_row = [&](int step) { return min(32 * step, p.in - 32); };
+        const u32x4* xo = reinterpret_cast<const u32x4*>(p.x) + static_cast<size_t>(t) * steps * MT * kWave;
+        auto load_x = [&](int step, int m) {
+            return load_at<u32x4>(xo + (static_cast<size_t>(min(step, steps - 1)) * MT + m) * kWave, 16 * lane);
         };
-        for (int step = 0; step < steps; step += 2) {
-            one(q[0], q[1], step);
-            if (step + 1 < steps) one(q[1], q[0], step + 1);
+        auto load_sc = [&](float (&q)[8], int step) {
+            const float* at_row = s.scales + first_row(step);
+            const floatx4 lo = load_at<floatx4_a4>(at_row, 32 * c), hi = load_at<floatx4_a4>(at_row + 4, 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q[i] = lo[i];
+                q[4 + i] = hi[i];
+            }
+        };
+        Words q;
+        float sc[8], next_sc[8];
+        u32x4 x[MT];
+        load_sc(sc, 0);
+        load_words(q, s, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x[m] = load_x(0, m);
+        floatx4 acc[CL][MT] = {};
+        for (int step = 0; step < steps; ++step) {
+            Ps ps;
+            ps.set(q, s.sh);
+            // the scales first: they are moved at the step's end, and a move
+            // waits for everything loaded before
+            load_sc(next_sc, step + 1);
+            load_words(q, s, first_row(step + 1));
+            ps.each(sc, tab, [&](auto ec, const u32x4& f) {
+                constexpr int e = decltype(ec)::value;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    acc[e][m] = mfma16x16x32(as_bf16x8(x[m]), as_bf16x8(f), acc[e][m]);
+                    if constexpr (e == CL - 1) x[m] = load_x(step + 1, m);
+                }
+            });
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = next_sc[i];
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -389,52 +530,76 @@ __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
             for (int i = 0; i < 4; ++i) {
                 const int row = row0 + 16 * m + 4 * c + i;
                 if (row >= at.end) continue;
-                u32x4 o;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) o[d] = pack_bf16(acc[2 * d][m][i], acc[2 * d + 1][m][i]);
-                *reinterpret_cast<u32x4*>(p.y + static_cast<size_t>(row) * p.out + col0 + 8 * j) = o;
+                *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(row) * p.out + col0 + CL * j) =
+                    uint2{pack_bf16(acc[0][m][i], acc[1][m][i]), pack_bf16(acc[2][m][i], acc[3][m][i])};
             }
     }
 }
 
 template <int K, bool VEC>
 __global__ __launch_bounds__(kExThreads) void experts0_few_kernel(ExArgs p) {
+    constexpr int CL = 8;
     __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
-    __shared__ float sum[16 * kStripCols];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(16))) float parts[kParts * kPartFloats];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
-    stage_table<K>(tab, p.lut);
     const int steps = (p.in + 31) / 32, strips = p.out / kStripCols;
     const int tiles = count_tiles(p.offsets, p.experts, p.rows, 16);
-    const Range r = xcd_range(tiles * strips, 1, 0);
-    for (int u = r.first; u < r.end; u += r.step) {
-        const int t = u / strips, col0 = (u - t * strips) * kStripCols;
-        const Found at = find_entry(p.offsets, p.experts, p.rows, 16, false, t);
-        const int row0 = at.first + at.index * 16;
-        const Strip0 s = strip0<K>(p, at.group, col0, j, c);
-        floatx4 acc[8][1] = {};
-        for (int step = wave; step < steps; step += kExWaves) {
-            Patch q;
-            load_patch(q, s, step);
-            const u32x4 x[1] = {x_operand<VEC>(p, row0, at.end, step, j, c)};
-            mul_patch<K, 1>(q, s, tab, x, 1, acc);
-        }
-        for (int w = 0; w < kExWaves; ++w) {
-            if (wave == w) {
+    struct Work {
+        Words q;
+        float sc[8];
+        u32x4 x;
+        int sh;
+    };
+    floatx4 acc[CL] = {};
+    run_units<Work>(
+        p, xcd_range(tiles * strips, 1, 0), strips, wave, kExWaves, steps,
+        [&](Work& q, const Unit& un, int step) {
+            const Strip0 s = strip0<K, CL>(p, un.group, un.col0, j, c);
+            q.x = x_operand<VEC>(p, un.row0, un.end, step, j, c);
+            q.sh = s.sh;
+            if (32 * step + 32 <= p.in) {
+                load_words(q.q, s, 32 * step);
+                const floatx4 lo = load_at<floatx4_a4>(s.scales + 32 * step, 32 * c);
+                const floatx4 hi = load_at<floatx4_a4>(s.scales + 32 * step + 4, 32 * c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) add_part(sum, 8 * j + e, c, acc[e][0], w == 0);
+                for (int i = 0; i < 4; ++i) {
+                    q.sc[i] = lo[i];
+                    q.sc[4 + i] = hi[i];
+                }
+                return;
             }
-            __syncthreads();
-        }
-        for (int i = tid; i < 16 * kStripCols / 2; i += kExThreads) {
-            const int row = row0 + i / (kStripCols / 2), at2 = 2 * (i % (kStripCols / 2));
-            if (row < at.end)
-                *reinterpret_cast<uint32_t*>(p.y + static_cast<size_t>(row) * p.out + col0 + at2) =
-                    pack_bf16(sum[2 * i], sum[2 * i + 1]);
-        }
-        __syncthreads();
-    }
+            // the last rows, one by one; past the end x is zero
+            const uint32_t row = static_cast<uint32_t>(32 * c * s.row_words);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = min(32 * step + 8 * c + i, p.in - 1);
+                const uint32_t* w = s.codes + static_cast<uint64_t>(r) * s.row_words;
+                q.q.a[i] = w[(s.at_a - row) / 4];
+                q.q.b[i] = w[(s.at_b - row) / 4];
+                q.sc[i] = s.scales[r];
+            }
+        },
+        [&] { stage_table<K>(tab, p.lut); },
+        [&](const Work& q) {
+            Pieces<K, CL> ps;
+            ps.set(q.q, q.sh);
+            ps.each(q.sc, tab, [&](auto ec, const u32x4& f) {
+                constexpr int e = decltype(ec)::value;
+                acc[e] = mfma16x16x32(as_bf16x8(q.x), as_bf16x8(f), acc[e]);
+            });
+        },
+        [&](const Unit& un) {
+            sum_strip<kExWaves>(parts, wave, [&](auto&& f) {
+#pragma unroll
+                for (int e = 0; e < CL; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f(4 * c + i, CL * j + e, acc[e][i]);
+            }, p.y, un.row0, un.end, un.col0, p.out);
+#pragma unroll
+            for (int e = 0; e < CL; ++e) acc[e] = floatx4{};
+        });
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -443,57 +608,56 @@ __global__ __launch_bounds__(kExThreads) void experts0_few_kernel(ExArgs p) {
 // decode-bound and a workgroup shares one tile; beyond, taller tiles decode
 // each weight for more rows.
 enum class Tile { few, some, many };
-Tile tile_for(int rows, int experts) {
+Tile tile_for(int axis, int in, int rows, int experts) {
     const int mean = (rows + experts - 1) / experts;
-    return mean <= 16 ? Tile::few : mean <= 64 ? Tile::some : Tile::many;
+    if (mean <= 16 || (axis == 0 && in < 32)) return Tile::few;
+    return mean <= 64 ? Tile::some : Tile::many;
 }
 
 int tiles_at_most(int rows, int experts, int per) {
     return rows / per + (experts < rows ? experts : rows);
 }
 
-// Rows per tile on axis 1 and axis 0.
-constexpr int kSome1 = 4, kMany1 = 8, kSome0 = 2, kMany0 = 4;
+// 16-row operands of a tile.
+constexpr int kSome = 4, kMany = 8;
 
+// x in operand order into the workspace, then the products.
 template <int K, int MT>
-hipError_t launch1(const ExpertWeights& w, ExArgs p, void* ws, hipStream_t st) {
-    const int tiles = tiles_at_most(p.rows, p.experts, 16 * MT);
+hipError_t launch_wide(const ExpertWeights& w, ExArgs p, void* ws, hipStream_t st) {
+    const dim3 grid(tiles_at_most(p.rows, p.experts, 16 * MT), (w.in + 255) / 256);
     u32x4* operands = static_cast<u32x4*>(ws);
-    const hipError_t e = launch_kernel(operands_kernel<MT>, dim3(tiles, w.in / kT), dim3(256), st, p.x,
-                                       p.offsets, p.experts, p.rows, p.in, operands);
+    auto order = w.axis == 1      ? operands_kernel<MT, 1, true>
+                 : w.in % 8 == 0 ? operands_kernel<MT, 0, true>
+                                 : operands_kernel<MT, 0, false>;
+    const hipError_t e = launch_kernel(order, grid, dim3(256), st, p.x, p.offsets, p.experts, p.rows,
+                                       p.in, operands);
     if (e != hipSuccess) return e;
     p.x = static_cast<const uint16_t*>(ws);
-    return launch_kernel(experts1_kernel<K, MT, 4>, dim3(cu_count()), dim3(kExThreads), st, p);
+    return launch_kernel(w.axis == 1 ? experts1_kernel<K, MT, 4> : experts0_kernel<K, MT>,
+                         dim3(cu_count()), dim3(kExThreads), st, p);
 }
 
 template <int K>
 hipError_t launch_k(const ExpertWeights& w, const ExArgs& p, void* ws, hipStream_t st) {
-    const Tile tile = tile_for(p.rows, p.experts);
-    const dim3 grid(cu_count()), block(kExThreads);
-    if (w.axis == 1) {
-        if (tile == Tile::some) return launch1<K, kSome1>(w, p, ws, st);
-        if (tile == Tile::many) return launch1<K, kMany1>(w, p, ws, st);
-        const int nb = w.in / kT;
-        auto kernel = nb >= 8   ? experts1_few_kernel<K, 8>
-                      : nb >= 4 ? experts1_few_kernel<K, 4>
-                      : nb >= 2 ? experts1_few_kernel<K, 2>
-                                : experts1_few_kernel<K, 1>;
-        return launch_kernel(kernel, grid, block, st, p);
-    }
-    const bool vec = w.in % 8 == 0;
-    auto kernel = tile == Tile::few    ? (vec ? experts0_few_kernel<K, true> : experts0_few_kernel<K, false>)
-                  : tile == Tile::some ? (vec ? experts0_kernel<K, kSome0, true> : experts0_kernel<K, kSome0, false>)
-                                       : (vec ? experts0_kernel<K, kMany0, true> : experts0_kernel<K, kMany0, false>);
-    return launch_kernel(kernel, grid, block, st, p);
+    const Tile tile = tile_for(w.axis, w.in, p.rows, p.experts);
+    if (tile == Tile::some) return launch_wide<K, kSome>(w, p, ws, st);
+    if (tile == Tile::many) return launch_wide<K, kMany>(w, p, ws, st);
+    const int nb = w.in / kT;
+    auto kernel = w.axis == 1 ? (nb >= 4   ? experts1_few_kernel<K, 4>
+                                 : nb >= 2 ? experts1_few_kernel<K, 2>
+                                           : experts1_few_kernel<K, 1>)
+                              : (w.in % 8 == 0 ? experts0_few_kernel<K, true> : experts0_few_kernel<K, false>);
+    return launch_kernel(kernel, dim3(cu_count()), dim3(kExThreads), st, p);
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int axis, int in, int rows, int experts) {
-    const Tile tile = tile_for(rows, experts);
-    if (axis != 1 || tile == Tile::few) return 0;
-    const int per = 16 * (tile == Tile::some ? kSome1 : kMany1);
-    return static_cast<size_t>(tiles_at_most(rows, experts, per)) * per * in * sizeof(uint16_t);
+    const Tile tile = tile_for(axis, in, rows, experts);
+    if (tile == Tile::few) return 0;
+    const int per = 16 * (tile == Tile::some ? kSome : kMany);
+    const size_t values = static_cast<size_t>((in + 31) / 32) * 32;
+    return static_cast<size_t>(tiles_at_most(rows, experts, per)) * per * values * sizeof(uint16_t);
 }
 
 hipError_t launch_experts(const uint16_t* x, int rows, const int32_t* offsets,

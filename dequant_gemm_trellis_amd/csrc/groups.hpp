@@ -120,12 +120,14 @@ __device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets,
         const uint64_t past = __ballot(before + inc > t);
         if (past) {
             const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
-            return {g0 + l, t - before - __shfl(inc - n, l), __shfl(first, l), __shfl(end, l),
-                    tiles + __shfl(tinc - nt, l), shared + __shfl(sinc - ns, l)};
+            // the same in every lane: as scalars, so that addresses stay scalar
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            return {g0 + l, t - before - of(inc - n), of(first), of(end), tiles + of(tinc - nt),
+                    shared + of(sinc - ns)};
         }
-        before += __shfl(inc, 63);
-        tiles += __shfl(tinc, 63);
-        shared += __shfl(sinc, 63);
+        before += __builtin_amdgcn_readlane(inc, 63);
+        tiles += __builtin_amdgcn_readlane(tinc, 63);
+        shared += __builtin_amdgcn_readlane(sinc, 63);
     }
     return {-1, 0, 0, 0, 0, 0};
 }
