@@ -178,7 +178,7 @@ size_t trellis_experts_workspace_bytes(const trellis_geometry* g, int32_t rows, 
     trellis::Dims d;
     if (trellis::check_geometry(g, &d) || check_groups(experts) || check_slots(rows, 1))
         return static_cast<size_t>(-1);
-    return rows ? trellis::experts_workspace_bytes(g->axis, g->in_features, rows, experts) : 0;
+    return rows ? trellis::experts_workspace_bytes(g->axis, g->in_features, g->out_features, rows, experts) : 0;
 }
 
 int trellis_experts(const uint16_t* x, int32_t rows, const int32_t* offsets, int32_t experts,

@@ -75,10 +75,11 @@ struct Range {
     int first, end, step;
 };
 __device__ __forceinline__ Range xcd_range(int units, int per_group, int index) {
-    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
-    const int groups = (gridDim.x - xcd + kXcds - 1) / kXcds;
-    const int u0 = static_cast<int>(static_cast<int64_t>(units) * xcd / kXcds);
-    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (xcd + 1) / kXcds);
+    const int dies = min(kXcds, static_cast<int>(gridDim.x));
+    const int xcd = blockIdx.x % dies, slot = blockIdx.x / dies;
+    const int groups = (gridDim.x - xcd + dies - 1) / dies;
+    const int u0 = static_cast<int>(static_cast<int64_t>(units) * xcd / dies);
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (xcd + 1) / dies);
     return {u0 + slot * per_group + index, u1, groups * per_group};
 }
 
@@ -96,9 +97,9 @@ struct ExArgs {
 
 // x of a tile in operand order, [tile][step][MT] operands of 64 lanes x 16 bytes;
 // rows past the tile's last are zeros. A wave's load of an operand is then 1 KB
-// in a row; taken from the rows it is 16 pieces of 64 bytes (axis 0; measured
-// 343 us against 230 with this order for 16384 rows of 1536 -> 2048 at k = 4)
-// or 64 of 16 bytes (axis 1). Grid: (tiles, 256 contracted values).
+// in a row; taken from the rows it is 16 pieces of 64 bytes on axis 0 (16384 rows
+// of 1536 -> 2048, k = 4: 343 us, against 214 with this order and 27 for making
+// it) or 64 of 16 bytes on axis 1. Grid: (tiles, 256 contracted values).
 template <int MT, int AXIS, bool VEC>
 __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restrict__ x,
                                                        const int32_t* __restrict__ offsets,
@@ -114,16 +115,18 @@ __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restric
     for (int m = threadIdx.x >> 6; m < MT; m += 4) {
         const int row = row0 + 16 * m + j;
         const uint16_t* p = x + static_cast<size_t>(min(row, at.end - 1)) * in;
-        u32x4 v[8];
+        u32x4 v[8] = {};
+        if constexpr (AXIS == 1) {  // step s of a block is weights 64 c + 8 s
+            if (row < at.end) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const int step = min(s0 + s, steps - 1);
-            // axis 1: step s of a block is weights 64 c + 8 s; axis 0: 32 rows in
-            // a row, the last step's the last 32
-            const int first = AXIS == 1 ? 8 * s + 256 * static_cast<int>(blockIdx.y) + 64 * c
-                                        : min(32 * step, in - 32) + 8 * c;
-            v[s] = load8<VEC>(p, first, in, row < at.end);
-            if (AXIS == 0) {
+                for (int s = 0; s < 8; ++s)
+                    v[s] = *reinterpret_cast<const u32x4*>(p + 256 * blockIdx.y + 64 * c + 8 * s);
+            }
+        } else {  // 32 rows in a row, the last step's the last 32
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int step = min(s0 + s, steps - 1), first = min(32 * step, in - 32) + 8 * c;
+                v[s] = load8<VEC>(p, first, in, row < at.end);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {  // values already counted
                     if (first + 2 * d < 32 * step) v[s][d] &= 0xFFFF0000u;
@@ -133,24 +136,27 @@ __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restric
         }
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-            if (s < n) o[(s * MT + m) * 64] = v[s];
+            if (AXIS == 1 || s < n) o[(s * MT + m) * 64] = v[s];
     }
 }
 
-// Axis 1, tiles of MT x 16 rows: a wave takes 16 G output columns of a tile.
-template <int K, int MT, int G>
+constexpr int kWideCols = 64;  // columns of a wave's strip in a tile of several operands
+
+// Axis 1, tiles of MT x 16 rows: a wave takes four 16-column groups of a tile.
+template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void experts1_kernel(ExArgs p) {
+    constexpr int G = kWideCols / 16;
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
     stage_table<K>(tab, p.lut);
-    const int nb = p.in / kT, strips = (p.out + 16 * G - 1) / (16 * G);
+    const int nb = p.in / kT, strips = (p.out + kWideCols - 1) / kWideCols;
     const int tiles = count_tiles(p.offsets, p.experts, p.rows, 16 * MT);
     const Range r = xcd_range(tiles * strips, kExWaves, wave);
     for (int u = r.first; u < r.end; u += r.step) {
-        const int t = u / strips, n0 = (u - t * strips) * 16 * G;
+        const int t = u / strips, n0 = (u - t * strips) * kWideCols;
         const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
         const int row0 = at.first + at.index * 16 * MT;
         const uint32_t* codes = p.codes + at.group * p.words;
@@ -337,14 +343,17 @@ __global__ __launch_bounds__(kExThreads) void experts1_few_kernel(ExArgs p) {
         },
         [&] { stage_table<K>(tab, p.lut); },
         [&](const Work& q) {
-            static_for<0, 8>([&](auto sc_) {
-                constexpr int S = decltype(sc_)::value;
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    acc[g] = mfma16x16x32(
-                        as_bf16x8(q.a[S]),
-                        as_bf16x8(pack_fragment(gather_tab<K, S, pair, rep>(q.w[g], tab), q.sc[g])),
-                        acc[g]);
+            // fragment i is step i / G of group i % G; its values are read one
+            // fragment ahead
+            Gathered<pair> v[2];
+            v[0] = gather_tab<K, 0, pair, rep>(q.w[0], tab);
+            static_for<0, 8 * G>([&](auto ic) {
+                constexpr int i = decltype(ic)::value, S = i / G, g = i % G, n = i + 1;
+                __builtin_amdgcn_s_setprio(2);
+                if constexpr (n < 8 * G) v[n & 1] = gather_tab<K, n / G, pair, rep>(q.w[n % G], tab);
+                __builtin_amdgcn_s_setprio(0);
+                acc[g] = mfma16x16x32(as_bf16x8(q.a[S]), as_bf16x8(pack_fragment(v[i & 1], q.sc[g])),
+                                      acc[g]);
             });
         },
         [&](const Unit& un) {
@@ -476,11 +485,11 @@ __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j = lane & 15, c = lane >> 4;
     stage_table<K>(tab, p.lut);
-    const int steps = (p.in + 31) / 32, strips = p.out / (16 * CL);
+    const int steps = (p.in + 31) / 32, strips = p.out / kWideCols;
     const int tiles = count_tiles(p.offsets, p.experts, p.rows, 16 * MT);
     const Range r = xcd_range(tiles * strips, kExWaves, wave);
     for (int u = r.first; u < r.end; u += r.step) {
-        const int t = u / strips, col0 = (u - t * strips) * 16 * CL;
+        const int t = u / strips, col0 = (u - t * strips) * kWideCols;
         const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
         const int row0 = at.first + at.index * 16 * MT;
         const Strip0 s = strip0<K, CL>(p, at.group, col0, j, c);
@@ -604,22 +613,43 @@ __global__ __launch_bounds__(kExThreads) void experts0_few_kernel(ExArgs p) {
 
 // ---- launches ---------------------------------------------------------------------
 
-// Rows of a tile by the average of an expert's: up to 16 the products are
-// decode-bound and a workgroup shares one tile; beyond, taller tiles decode
-// each weight for more rows.
-enum class Tile { few, some, many };
-Tile tile_for(int axis, int in, int rows, int experts) {
-    const int mean = (rows + experts - 1) / experts;
-    if (mean <= 16 || (axis == 0 && in < 32)) return Tile::few;
-    return mean <= 64 ? Tile::some : Tile::many;
+// The tiles of a call: strips of 16 rows shared by a workgroup's waves, or tiles
+// of 2, 4 or 8 operands of which every wave takes strips of its own.
+enum class Tile { few, two, four, eight };
+constexpr int kOperands[] = {1, 2, 4, 8};
+
+// The tile with the least estimated time. The host does not know how the rows
+// fall: it takes rows / (rows of a tile) tiles plus 0.6 of an expert's last, at
+// least one per expert. All units of a launch of about one size, the time goes
+// by the rounds that the compute units (few) or their eight waves take, times a
+// round's. Measured for 64 experts of 2048 -> 1536 (axis 1; axis 0 alike per
+// contracted value, its few-row strips a third slower) at k = 3, 512 to 8192
+// rows, us: a round of few-row strips 16, of two operands 68, of four 75, of
+// eight 100; at 512 rows 54 / 68 / 71 / 93, at 1024 83 / 71 / 77 / 97, at 2048
+// 129 / 132 / 82 / 106, at 4096 218 / 146 / 150 / 110, at 8192 377 / 261 / 167 /
+// 200 (two operands at 4096 rows took fewer rounds than estimated).
+Tile tile_for(int axis, int in, int out, int rows, int experts) {
+    if (axis == 0 && in < 32) return Tile::few;  // a tile's step is 32 whole rows
+    const int64_t used = experts < rows ? experts : rows;
+    const int64_t cus = cu_count();
+    auto cost = [&](int t, int64_t round) {
+        const int64_t per = 16 * kOperands[t];
+        int64_t tiles = rows / per + used * 6 / 10;
+        tiles = tiles > used ? tiles : used;
+        const int cols = t ? kWideCols : kStripCols;
+        const int64_t units = tiles * ((out + cols - 1) / cols), slots = t ? cus * kExWaves : cus;
+        return (units + slots - 1) / slots * round;
+    };
+    const int64_t round[] = {axis == 1 ? 16 : 21, 68, 75, 100};
+    int best = 0;
+    for (int t = 1; t < 4; ++t)
+        if (cost(t, round[t]) < cost(best, round[best])) best = t;
+    return static_cast<Tile>(best);
 }
 
 int tiles_at_most(int rows, int experts, int per) {
     return rows / per + (experts < rows ? experts : rows);
 }
-
-// 16-row operands of a tile.
-constexpr int kSome = 4, kMany = 8;
 
 // x in operand order into the workspace, then the products.
 template <int K, int MT>
@@ -633,15 +663,18 @@ hipError_t launch_wide(const ExpertWeights& w, ExArgs p, void* ws, hipStream_t s
                                        p.in, operands);
     if (e != hipSuccess) return e;
     p.x = static_cast<const uint16_t*>(ws);
-    return launch_kernel(w.axis == 1 ? experts1_kernel<K, MT, 4> : experts0_kernel<K, MT>,
+    return launch_kernel(w.axis == 1 ? experts1_kernel<K, MT> : experts0_kernel<K, MT>,
                          dim3(cu_count()), dim3(kExThreads), st, p);
 }
 
 template <int K>
 hipError_t launch_k(const ExpertWeights& w, const ExArgs& p, void* ws, hipStream_t st) {
-    const Tile tile = tile_for(w.axis, w.in, p.rows, p.experts);
-    if (tile == Tile::some) return launch_wide<K, kSome>(w, p, ws, st);
-    if (tile == Tile::many) return launch_wide<K, kMany>(w, p, ws, st);
+    switch (tile_for(w.axis, w.in, w.out, p.rows, p.experts)) {
+    case Tile::two: return launch_wide<K, 2>(w, p, ws, st);
+    case Tile::four: return launch_wide<K, 4>(w, p, ws, st);
+    case Tile::eight: return launch_wide<K, 8>(w, p, ws, st);
+    case Tile::few: break;
+    }
     const int nb = w.in / kT;
     auto kernel = w.axis == 1 ? (nb >= 4   ? experts1_few_kernel<K, 4>
                                  : nb >= 2 ? experts1_few_kernel<K, 2>
@@ -652,10 +685,10 @@ hipError_t launch_k(const ExpertWeights& w, const ExArgs& p, void* ws, hipStream
 
 }  // namespace
 
-size_t experts_workspace_bytes(int axis, int in, int rows, int experts) {
-    const Tile tile = tile_for(axis, in, rows, experts);
+size_t experts_workspace_bytes(int axis, int in, int out, int rows, int experts) {
+    const Tile tile = tile_for(axis, in, out, rows, experts);
     if (tile == Tile::few) return 0;
-    const int per = 16 * (tile == Tile::some ? kSome : kMany);
+    const int per = 16 * kOperands[static_cast<int>(tile)];
     const size_t values = static_cast<size_t>((in + 31) / 32) * 32;
     return static_cast<size_t>(tiles_at_most(rows, experts, per)) * per * values * sizeof(uint16_t);
 }

@@ -64,7 +64,7 @@ struct ExpertWeights {
     size_t words;
     int axis, k, in, out, experts;
 };
-size_t experts_workspace_bytes(int axis, int in, int rows, int experts);
+size_t experts_workspace_bytes(int axis, int in, int out, int rows, int experts);
 hipError_t launch_experts(const uint16_t* x, int rows, const int32_t* offsets,
                           const ExpertWeights& w, uint16_t* y, void* ws, hipStream_t st);
 
