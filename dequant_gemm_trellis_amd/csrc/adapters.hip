@@ -10,7 +10,7 @@
 // or writes the wide rows once and does little with them, so the memory bounds
 // them all.
 //
-// Few rows (kDirectRows): two launches that follow each row's own adapter.
+// Few rows: one or two launches that follow each row's own adapter.
 // Many rows: the rows are sorted by adapter and cut into tiles of 64 rows of
 // one adapter, which share the factor's values in bf16 matrix instructions.
 // There a rank-long float32 value w (u or g) enters as two bf16 parts, hi =
@@ -113,21 +113,23 @@ __global__ __launch_bounds__(kWgThreads) void direct_inner_kernel(
     }
 }
 
-// y[m] = base[m] + s u[m] B over 512 columns: wave w sums u[m][r] from the
-// splits for its ranks r = w, w + 4, ... (lanes over splits, then a fixed tree),
-// multiplies, and the four waves' sums meet in LDS in wave order. The first
-// workgroup of a row writes u. Grid: (column chunks, rows).
+// y[m] = base[m] + s u[m] B over 512 columns: u[m] summed from the splits by 16
+// lanes per rank (then a fixed tree), while the first rows of B are on their
+// way; wave w multiplies ranks w, w + 4, ..., and the four waves' sums meet in
+// LDS in wave order. The first workgroup of a row writes u. Grid: (column
+// chunks, rows).
 template <bool VEC>
 __global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
     const float* __restrict__ partial, int splits, const int32_t* __restrict__ ids,
     const uint16_t* __restrict__ factor, const float* __restrict__ scales, int width, int rank,
     int count, const uint16_t* base, uint16_t* y, float* __restrict__ u) {
+    __shared__ float us[kMaxRank];
     __shared__ float sums[kWgWaves][8][kWave];
     const int m = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rows = gridDim.y;
     const int a = ids[m];
     const bool has = static_cast<uint32_t>(a) < static_cast<uint32_t>(count);
     const int col = blockIdx.x * kDirectCols + 8 * lane;
-    const uint16_t* brow = base + static_cast<size_t>(m) * width;
+    const uint16_t* brow = (base ? base : y) + static_cast<size_t>(m) * width;
     uint16_t* yrow = y + static_cast<size_t>(m) * width;
     if (!has) {
         if (u && blockIdx.x == 0)
@@ -140,34 +142,40 @@ __global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
     const uint16_t* f = factor + static_cast<size_t>(a) * rank * width;
     u32x4 b = {0u, 0u, 0u, 0u};
     if (wave == 0) b = load8<VEC>(brow, col, width, base != nullptr);
-    float acc[8] = {};
-    // kRanks of a wave's ranks at a time: their loads are in flight together
-    constexpr int kRanks = 4;
-    for (int r0 = wave; r0 < rank; r0 += kRanks * kWgWaves) {
-        u32x4 w[kRanks];
-        float s[kRanks];
+    constexpr int kEarly = 4;
+    u32x4 early[kEarly];
 #pragma unroll
-        for (int i = 0; i < kRanks; ++i) {
-            const int r = r0 + i * kWgWaves;
-            w[i] = load8<VEC>(f + static_cast<size_t>(min(r, rank - 1)) * width, col, width, r < rank);
-            s[i] = 0.f;
-            for (int k = lane; r < rank && k < splits; k += kWave)
-                s[i] += partial[(static_cast<size_t>(k) * rows + m) * rank + r];
-        }
+    for (int i = 0; i < kEarly; ++i) {
+        const int r = wave + i * kWgWaves;
+        early[i] = load8<VEC>(f + static_cast<size_t>(min(r, rank - 1)) * width, col, width, r < rank);
+    }
+    for (int i = threadIdx.x; i < 16 * rank; i += kWgThreads) {
+        const int r = i / 16;
+        float s = 0.f;
+        for (int k = i % 16; k < splits; k += 16) s += partial[(static_cast<size_t>(k) * rows + m) * rank + r];
 #pragma unroll
-        for (int i = 0; i < kRanks; ++i) {
-            const int r = r0 + i * kWgWaves;
-#pragma unroll
-            for (int d = 32; d; d >>= 1) s[i] += __shfl_xor(s[i], d);
-            if (u && blockIdx.x == 0 && lane == 0 && r < rank) u[static_cast<size_t>(m) * rank + r] = s[i];
-            const float us = s[i] * scale;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                acc[2 * d] = r < rank ? fmaf(us, bf16_low(w[i][d]), acc[2 * d]) : acc[2 * d];
-                acc[2 * d + 1] = r < rank ? fmaf(us, bf16_high(w[i][d]), acc[2 * d + 1]) : acc[2 * d + 1];
-            }
+        for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d);
+        if (i % 16 == 0) {
+            us[r] = s * scale;
+            if (u && blockIdx.x == 0) u[static_cast<size_t>(m) * rank + r] = s;
         }
     }
+    __syncthreads();
+    float acc[8] = {};
+    auto add = [&](int r, const u32x4& w) {
+        const float ur = us[r];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            acc[2 * d] = fmaf(ur, bf16_low(w[d]), acc[2 * d]);
+            acc[2 * d + 1] = fmaf(ur, bf16_high(w[d]), acc[2 * d + 1]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+        if (wave + i * kWgWaves < rank) add(wave + i * kWgWaves, early[i]);
+#pragma unroll 4
+    for (int r = wave + kEarly * kWgWaves; r < rank; r += kWgWaves)
+        add(r, load8<VEC>(f + static_cast<size_t>(r) * width, col, width, true));
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[wave][e][lane] = acc[e];
     __syncthreads();
@@ -180,6 +188,100 @@ __global__ __launch_bounds__(kWgThreads) void direct_expand_kernel(
     for (int d = 0; d < 4; ++d)
         o[d] = pack_bf16(bf16_low(b[d]) + acc[2 * d], bf16_high(b[d]) + acc[2 * d + 1]);
     store8<VEC>(yrow, col, width, o);
+}
+
+// Both products in one launch: every workgroup computes the whole of its row's u
+// (its 16 waves take a rank each at a time; the factor comes from the L2 for all
+// but the row's first workgroup), then 1024 columns: 128 lanes of 8 columns, the
+// ranks in eight parts that meet in LDS in order. The second factor's first
+// ranks are on their way during the first product. Grid: (column chunks, rows).
+constexpr int kOneThreads = 1024;
+constexpr int kOneCols = 1024;
+constexpr int kOneParts = kOneThreads / (kOneCols / 8);
+
+template <bool VEC_IN, bool VEC_OUT>
+__global__ __launch_bounds__(kOneThreads) void direct_kernel(
+    const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint16_t* __restrict__ a,
+    const uint16_t* __restrict__ b, const float* __restrict__ scales, int in, int out, int rank,
+    int count, const uint16_t* base, uint16_t* y, float* __restrict__ u) {
+    __shared__ float us[kMaxRank];
+    __shared__ float sums[kOneParts][8][kOneCols / 8];
+    const int m = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int id = ids[m];
+    const bool has = static_cast<uint32_t>(id) < static_cast<uint32_t>(count);
+    const int lc = tid % (kOneCols / 8), part = tid / (kOneCols / 8);
+    const int col = blockIdx.x * kOneCols + 8 * lc;
+    const uint16_t* brow = (base ? base : y) + static_cast<size_t>(m) * out;
+    uint16_t* yrow = y + static_cast<size_t>(m) * out;
+    if (!has) {
+        if (u && blockIdx.x == 0)
+            for (int r = tid; r < rank; r += kOneThreads) u[static_cast<size_t>(m) * rank + r] = 0.f;
+        if (base != y && part == 0)
+            store8<VEC_OUT>(yrow, col, out, load8<VEC_OUT>(brow, col, out, base != nullptr));
+        return;
+    }
+    const float scale = scales[id];
+    const uint16_t* fb = b + static_cast<size_t>(id) * rank * out;
+    constexpr int kEarly = 2;
+    u32x4 early[kEarly], bv = {0u, 0u, 0u, 0u};
+    if (part == 0) bv = load8<VEC_OUT>(brow, col, out, base != nullptr);
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i) {
+        const int r = part + i * kOneParts;
+        early[i] = load8<VEC_OUT>(fb + static_cast<size_t>(min(r, rank - 1)) * out, col, out, r < rank);
+    }
+    const uint16_t* xr = x + static_cast<size_t>(m) * in;
+    for (int r = wave; r < rank; r += kOneThreads / kWave) {
+        const uint16_t* fa = a + (static_cast<size_t>(id) * rank + r) * in;
+        float s = 0.f;
+#pragma unroll 8
+        for (int k = 8 * lane; k < in; k += 8 * kWave) {
+            const u32x4 xv = load8<VEC_IN>(xr, k, in, true), w = load8<VEC_IN>(fa, k, in, true);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                s = fmaf(bf16_low(xv[d]), bf16_low(w[d]), s);
+                s = fmaf(bf16_high(xv[d]), bf16_high(w[d]), s);
+            }
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+        if (lane == 0) {
+            us[r] = s * scale;
+            if (u && blockIdx.x == 0) u[static_cast<size_t>(m) * rank + r] = s;
+        }
+    }
+    __syncthreads();
+    float acc[8] = {};
+    auto add = [&](int r, const u32x4& w) {
+        const float ur = us[r];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            acc[2 * d] = fmaf(ur, bf16_low(w[d]), acc[2 * d]);
+            acc[2 * d + 1] = fmaf(ur, bf16_high(w[d]), acc[2 * d + 1]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+        if (part + i * kOneParts < rank) add(part + i * kOneParts, early[i]);
+#pragma unroll 4
+    for (int r = part + kEarly * kOneParts; r < rank; r += kOneParts)
+        add(r, load8<VEC_OUT>(fb + static_cast<size_t>(r) * out, col, out, true));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[part][e][lc] = acc[e];
+    __syncthreads();
+    if (part) return;
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        acc[e] = sums[0][e][lc];
+#pragma unroll
+        for (int q = 1; q < kOneParts; ++q) acc[e] += sums[q][e][lc];
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        o[d] = pack_bf16(bf16_low(bv[d]) + acc[2 * d], bf16_high(bv[d]) + acc[2 * d + 1]);
+    store8<VEC_OUT>(yrow, col, out, o);
 }
 
 // ---- many rows ----------------------------------------------------------------
@@ -362,7 +464,7 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
         if (base == y) return;
         for (int i = c; i < ti.rows; i += 4) {
             const size_t at = static_cast<size_t>(trow[i]) * width;
-            store8<VEC>(y + at, col, width, load8<VEC>(base + at, col, width, base != nullptr));
+            store8<VEC>(y + at, col, width, load8<VEC>((base ? base : y) + at, col, width, base != nullptr));
         }
         return;
     }
@@ -383,7 +485,7 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
         for (int i = 0; i < 4; ++i) row[i] = __shfl(my_row, 16 * s + 4 * c + i);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            bv[i] = load8<VEC>(base + static_cast<size_t>(max(row[i], 0)) * width, col, width,
+            bv[i] = load8<VEC>((base ? base : y) + static_cast<size_t>(max(row[i], 0)) * width, col, width,
                                base && row[i] >= 0);
         const uint16_t* a_at = rows_op + static_cast<size_t>(16 * s + j) * r16 * 32 + 8 * c;
         floatx4 acc[8] = {};
@@ -563,9 +665,16 @@ __global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
 
 // ---- plans and launches ---------------------------------------------------------
 
-// Rows up to which each row follows its own adapter (two launches, the factors
-// read again by rows that share one).
-constexpr int kDirectRows = 64;
+// Up to kDirectRanks ranks over all rows each row follows its own adapter: two
+// launches, the factors read again by rows that share one. 5120 -> 17408, 32
+// adapters, us (direct / tiles): rank 8, 300 rows 22 / 25; rank 16, 32 rows 11 /
+// 20, 200 rows 22 / 24, 300 rows 30 / 26; rank 32, 100 rows 25 / 32; rank 64, 32
+// rows 26 / 31, 64 rows 38 / 37, 100 rows 46 / 41.
+constexpr int kDirectRanks = 4096;
+constexpr int kDirectRows = 512;
+bool direct_rows(int rows, int rank) {
+    return rows <= kDirectRows && rows * rank <= kDirectRanks;
+}
 constexpr int kTargetGroups = 1024;  // workgroups that fill the compute units a few times
 
 struct Plan {
@@ -665,12 +774,21 @@ hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b,
                          offsets, rows, rank, kMaxSegTiles);
 }
 
+// Few rows whose first factor is small enough for every workgroup of a row to
+// read: one launch. 5120 -> 17408 at rank 16: 1 row 6.5 us against 8.5 in two
+// launches, 8 rows 9.0 / 8.8 (and one launch less for the host to issue), 32
+// rows 17.3 / 12.0; 17408 -> 5120, 1 row 12.4 / 8.2.
+bool direct_in_one(int rows, int in, int rank) {
+    return rows <= 8 && static_cast<int64_t>(in) * rank <= 1 << 17;
+}
+
 int direct_splits(int width) { return (width + kDirectCols - 1) / kDirectCols; }
 
 }  // namespace
 
 size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, bool backward) {
-    if (!backward && rows <= kDirectRows)
+    if (!backward && direct_rows(rows, rank) && direct_in_one(rows, in, rank)) return 0;
+    if (!backward && direct_rows(rows, rank))
         return static_cast<size_t>(direct_splits(in)) * rows * rank * sizeof(float);
     return make_plan(rows, in, out, rank, count, backward).bytes;
 }
@@ -680,7 +798,13 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
                            bool vec_out, void* ws, hipStream_t st) {
     hipError_t e;
     if (rows == 0) return hipSuccess;
-    if (rows <= kDirectRows) {
+    if (direct_rows(rows, f.rank) && direct_in_one(rows, f.in, f.rank)) {
+        auto kernel = vec_in ? (vec_out ? direct_kernel<true, true> : direct_kernel<true, false>)
+                             : (vec_out ? direct_kernel<false, true> : direct_kernel<false, false>);
+        return launch_kernel(kernel, dim3((f.out + kOneCols - 1) / kOneCols, rows), dim3(kOneThreads),
+                             st, x, ids, f.a, f.b, f.scales, f.in, f.out, f.rank, f.count, base, y, u);
+    }
+    if (direct_rows(rows, f.rank)) {
         const int splits = direct_splits(f.in);
         e = launch_kernel(vec_in ? direct_inner_kernel<true> : direct_inner_kernel<false>,
                           dim3(splits, rows), dim3(kWgThreads), st, x, ids, f.a, f.in, f.rank,

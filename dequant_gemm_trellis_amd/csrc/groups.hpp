@@ -135,31 +135,36 @@ __device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets,
 // 16 bytes at a 4-byte boundary (what a global access of any width needs).
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
-// 8 values of a row from column `col` on, zeros past `width` and where !live.
-// VEC: rows are multiples of 8 values and 16-byte aligned. Otherwise a row
-// starts at any 2-byte boundary: at a 4-byte one the values are read as they
-// are, else from the five 4-byte words that hold them (whose outer halves are
-// not used); at the row's end one by one.
+// 8 values of a row from column `col` on, zeros past `width` and where !live
+// (`row` is a row that can be read in any case). VEC: rows are multiples of 8
+// values and 16-byte aligned. Otherwise a row starts at any 2-byte boundary, and
+// the values come from the five (at a 4-byte boundary four) 4-byte words that
+// hold them, whose outer halves are not used; without a branch, so that many
+// such loads are in flight together. At the row's end they come one by one.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load8(const uint16_t* __restrict__ row, int col, int width, bool live) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if constexpr (VEC) {
         if (live && col < width) v = *reinterpret_cast<const u32x4*>(row + col);
-    } else if (live && col + 8 <= width) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(row + col);
+        return v;
+    }
+    const bool whole = col + 8 <= width;
+    if (width >= 8) {  // uniform
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row + (whole ? col : 0));
         const uint32_t* w = reinterpret_cast<const uint32_t*>(p & ~static_cast<uintptr_t>(3));
-        v = *reinterpret_cast<const u32x4_a4*>(w);
-        if (p & 2) {
-            const uint32_t last = w[4];
+        const uint32_t odd = (p >> 1) & 1;
+        const u32x4 q = *reinterpret_cast<const u32x4_a4*>(w);
+        const uint32_t last = w[3 + odd];
+        const bool take = live && whole;
 #pragma unroll
-            for (int d = 0; d < 4; ++d)
-                v[d] = __builtin_amdgcn_alignbit(d < 3 ? v[d < 3 ? d + 1 : 3] : last, v[d], 16);
-        }
-    } else {
+        for (int d = 0; d < 4; ++d)
+            v[d] = take ? __builtin_amdgcn_alignbit(d < 3 ? q[d < 3 ? d + 1 : 3] : last, q[d], 16 * odd) : 0u;
+    }
+    if (live && !whole && col < width) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-            const uint32_t lo = live && col + 2 * d < width ? row[col + 2 * d] : 0u;
-            const uint32_t hi = live && col + 2 * d + 1 < width ? row[col + 2 * d + 1] : 0u;
+            const uint32_t lo = col + 2 * d < width ? row[col + 2 * d] : 0u;
+            const uint32_t hi = col + 2 * d + 1 < width ? row[col + 2 * d + 1] : 0u;
             v[d] = lo | (hi << 16);
         }
     }

@@ -143,7 +143,7 @@ typedef struct trellis_adapter_set {
  * (trellis_prefill or trellis_gemv of x), or null for zeros; y: bf16
  * [rows][out], which may be `base` itself (rows without an adapter are then
  * not touched); u: float32 [rows][rank], kept for the backward pass, or null.
- * u and the sum are float32; up to 64 rows every product is a float32 one,
+ * u and the sum are float32; for few rows every product is a float32 one,
  * beyond that u enters the second product as two bf16 parts (an error of at
  * most 2^-16 of it). workspace: 16-byte aligned, at least
  * trellis_adapters_workspace_bytes(f, rows, 0) bytes.
