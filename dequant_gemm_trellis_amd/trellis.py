@@ -358,7 +358,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _apart(outputs: dict, inputs: dict) -> None:
-    """Refuse an output that shares memory with an input or another output."""
+    """Refuse an output that shares memory with an input or another output (new
+    outputs, given as None, do not)."""
     outs = [(name, t.data_ptr(), t.nbytes) for name, t in outputs.items() if t is not None]
     ins = [(name, t.data_ptr(), t.nbytes) for name, t in inputs.items() if t is not None]
     for i, (a, a0, an) in enumerate(outs):
@@ -554,7 +555,9 @@ def adapters(x, ids, a, b, scales, base=None, y=None, u=None, keep_inner=False, 
         _want("base", base, torch.bfloat16, (rows, f.out_features), dev)
     nbytes = adapters_workspace_bytes(f, rows, False)
     with _on(stream, dev):
-        given = {"y": y, "u": u, "workspace": workspace}
+        given = None
+        if y is not None or u is not None or workspace is not None:
+            given = {"y": y, "u": u, "workspace": workspace}
         if y is None:
             y = x.new_empty((rows, f.out_features))
         else:
@@ -564,9 +567,10 @@ def adapters(x, ids, a, b, scales, base=None, y=None, u=None, keep_inner=False, 
         elif keep_inner:
             u = x.new_empty((rows, f.rank), dtype=torch.float32)
         ws, ws_bytes, keep = _workspace("trellis_adapters", nbytes, workspace, x)
-        same = base is not None and base.data_ptr() == y.data_ptr()
-        _apart(given, {"x": x, "ids": ids, "a": a, "b": b, "scales": scales,
-                       "base": None if same else base})
+        if given is not None:
+            same = base is not None and base.data_ptr() == y.data_ptr()
+            _apart(given, {"x": x, "ids": ids, "a": a, "b": b, "scales": scales,
+                           "base": None if same else base})
         _check("trellis_adapters", _lib.trellis_adapters(
             x.data_ptr(), ids.data_ptr(), rows, C.byref(f), _ptr(base), y.data_ptr(), _ptr(u), ws,
             ws_bytes, _handle(dev)))

@@ -339,6 +339,30 @@ def test_another_stream(gpu_lib):
         assert same(got, ref)
 
 
+def test_offsets_past_32_bits(gpu_lib):
+    """More than 2^31 outputs: the last rows equal those of a short call (exact
+    integers, so both sums give the same bits)."""
+    say("adapters past 2^31 values")
+    T, rows, tail = gpu_lib, 131072, 300
+    p = Problem(16, tail, 64, 17408, 8, 2, "one")
+    d = p.cuda()
+    assert rows * 17408 > 2 ** 31
+
+    def long(t):
+        return torch.cat([t.new_zeros((rows - tail, t.shape[1])), t])
+
+    ids = torch.cat([torch.zeros(rows - tail, dtype=torch.int32, device="cuda"), d["ids"]])
+    y, u = T.adapters(long(d["x"]), ids, d["a"], d["b"], d["scales"], base=long(d["base_y"]),
+                      keep_inner=True)
+    want, want_u = p.forward()
+    assert same(y[-tail:], want) and not y[:-tail].any()
+    del y
+    dx, da, db = T.adapters_backward(long(d["dy"]), long(d["x"]), u, ids, d["a"], d["b"],
+                                     d["scales"], base=long(d["base_x"]))
+    for got, ref in zip((dx[-tail:], da, db), p.backward(want_u)):
+        assert same(got, ref)
+
+
 @pytest.mark.parametrize("M", [1, 20])
 def test_beside_the_projection(gpu_lib, M):
     """As it is used: the coded projection of all rows, each row's adapter added

@@ -147,6 +147,21 @@ def test_not_finite_rows_stay_alone(gpu_lib, axis, i, o):
         assert torch.equal(y[fine], want[fine]) and bool(y[bad[:2]].isnan().all())
 
 
+@pytest.mark.parametrize("axis,i,o", [(0, 33, 2048), (1, 256, 2049)])
+def test_offsets_past_32_bits(gpu_lib, axis, i, o):
+    """More than 2^31 outputs, the last rows another expert's."""
+    say(f"experts past 2^31 values, axis {axis}")
+    rows, tail = 1050000, 200
+    p = Problem(10, axis, i, o, 3, [50, tail])
+    x, _, codes, scales, lut = p.cuda()
+    assert rows * o > 2 ** 31
+    x = torch.cat([x.new_zeros((rows - tail, i)), x[50:]])
+    offsets = torch.tensor([0, rows - tail, rows], dtype=torch.int32, device="cuda")
+    y = gpu_lib.experts(x, offsets, codes, scales, lut, p.shape)
+    assert torch.equal(y[-tail:].cpu(), p.want()[50:].to(torch.bfloat16))
+    assert not y[:-tail].any()
+
+
 def test_gradient_is_the_other_axis(gpu_lib):
     """<experts(x), d> = <x, experts with the axis flipped (d)>, exactly for
     integers whose outputs stay below 2^8."""

@@ -278,3 +278,19 @@ def test_wild_positions_select_no_row(gpu_lib):
     assert out.sum(1).tolist() == [16, 0, 0, 16, 16, 0]
     z = T.combine(torch.ones((6, 16), dtype=torch.bfloat16, device="cuda"), None, r)
     assert z[:, 0].tolist() == [1, 1, 1]
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    """More than 2^31 values in the sorted rows: the last rows are the tokens'."""
+    say("dispatch and combine past 2^31 values")
+    T, tokens, top_k, width = gpu_lib, 66000, 8, 4096
+    ids = torch.zeros((tokens, top_k), dtype=torch.int32, device="cuda")
+    x = torch.arange(tokens, device="cuda").remainder(251).to(torch.bfloat16)[:, None].repeat(1, width)
+    r = T.route(ids, 2)
+    assert tokens * top_k * width > 2 ** 31
+    out = T.dispatch(x, r)
+    assert torch.equal(out[-top_k - 3:], x[[-2] * 3 + [-1] * top_k])
+    assert torch.equal(T.combine(out, None, r)[-5:], (x[-5:].float() * top_k).to(torch.bfloat16))
+    dy, dw = T.combine_backward(x, out, torch.full((tokens, top_k), 2.0, device="cuda"), r)
+    assert torch.equal(dy[-9:], (2 * x[[-2] + [-1] * 8].float()).to(torch.bfloat16))
+    assert torch.equal(dw[-1], (x[-1].double() @ x[-1].double()).float().repeat(top_k))
