@@ -10,7 +10,8 @@
 // or writes the wide rows once and does little with them, so the memory bounds
 // them all.
 //
-// Few rows: one or two launches that follow each row's own adapter.
+// Few rows: one or two launches (the gradient: three) that follow each row's own
+// adapter, all in float32.
 // Many rows: the rows are sorted by adapter and cut into tiles of 64 rows of
 // one adapter, which share the factor's values in bf16 matrix instructions.
 // There a rank-long float32 value w (u or g) enters as two bf16 parts, hi =
@@ -282,6 +283,116 @@ __global__ __launch_bounds__(kOneThreads) void direct_kernel(
     for (int d = 0; d < 4; ++d)
         o[d] = pack_bf16(bf16_low(bv[d]) + acc[2 * d], bf16_high(bv[d]) + acc[2 * d + 1]);
     store8<VEC_OUT>(yrow, col, out, o);
+}
+
+// The gradients of an adapter's factors over few rows: a workgroup takes 512
+// columns and 16 ranks of one adapter, finds its rows (ascending), and its eight
+// waves take them in turn: 16 ranks x 8 columns of float32 sums per lane. Wave q
+// adds wave q + 4's sums to its own, then the four meet in order. `inner` are
+// the float32 rank-long values without the scale. Grid: (column chunks of side a
+// then of side b, adapters, 16 ranks each).
+constexpr int kFewThreads = 512;
+constexpr int kFewRows = kFewThreads;  // rows of a call, at most: a thread finds one
+constexpr int kFewRanks = 16;
+
+struct FewSide {
+    const uint16_t* x;   // the wide rows
+    const float* inner;  // [rows][rank]
+    uint16_t* grad;
+    int width, chunks;
+    bool vec;
+};
+
+template <bool VEC>
+__device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int wave,
+                                         const int* __restrict__ list,
+                                         const float (*__restrict__ coef)[kFewRanks],
+                                         float (&acc)[kFewRanks][8]) {
+#pragma unroll 4
+    for (int i = wave; i < n; i += kFewThreads / kWave) {
+        const u32x4 v = load8<VEC>(p.x + static_cast<size_t>(list[i]) * p.width, col, p.width, true);
+        float e[8];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            e[2 * d] = bf16_low(v[d]);
+            e[2 * d + 1] = bf16_high(v[d]);
+        }
+#pragma unroll
+        for (int r = 0; r < kFewRanks; ++r)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[r][q] = fmaf(coef[i][r], e[q], acc[r][q]);
+    }
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(kFewThreads) void direct_outer_kernel(
+    FewSide a, FewSide b, const int32_t* __restrict__ ids, const float* __restrict__ scales, int rows,
+    int rank) {
+    constexpr int waves = kFewThreads / kWave;
+    union Shared {
+        float coef[kFewRows][kFewRanks];
+        float part[waves / 2][kFewRanks][8][kWave];
+    };
+    __shared__ Shared sh;
+    __shared__ int list[kFewRows], found[waves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int id = blockIdx.y, r0 = blockIdx.z * kFewRanks;
+    const bool second = static_cast<int>(blockIdx.x) >= a.chunks;
+    const FewSide& p = second ? b : a;
+    const int chunk = second ? blockIdx.x - a.chunks : blockIdx.x;
+    const int col = chunk * kDirectCols + 8 * lane;
+    const bool mine = tid < rows && ids[tid] == id;
+    const uint64_t votes = __ballot(mine);
+    if (lane == 0) found[wave] = __popcll(votes);
+    __syncthreads();
+    int before = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < waves; ++w) {
+        if (w < wave) before += found[w];
+        n += found[w];
+    }
+    if (mine) list[before + __popcll(votes & ((1ull << lane) - 1))] = tid;
+    __syncthreads();
+    const float scale = scales[id];
+    for (int i = tid; i < n * kFewRanks; i += kFewThreads) {
+        const int r = r0 + i % kFewRanks;
+        sh.coef[i / kFewRanks][i % kFewRanks] =
+            r < rank ? p.inner[static_cast<size_t>(list[i / kFewRanks]) * rank + r] * scale : 0.f;
+    }
+    __syncthreads();
+    float acc[kFewRanks][8] = {};
+    if (VEC || p.vec)
+        add_rows<true>(p, col, n, wave, list, sh.coef, acc);
+    else
+        add_rows<false>(p, col, n, wave, list, sh.coef, acc);
+    __syncthreads();  // the parts take the coefficients' place
+    auto each = [&](auto&& f) {
+#pragma unroll
+        for (int r = 0; r < kFewRanks; ++r)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f(sh.part[wave % (waves / 2)][r][q][lane], acc[r][q]);
+    };
+    if (wave >= waves / 2) each([](float& o, float v) { o = v; });
+    __syncthreads();
+    if (wave < waves / 2) each([](float& o, float v) { o += v; });
+    __syncthreads();
+    for (int r = wave; r < kFewRanks && r0 + r < rank; r += waves) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            v[q] = sh.part[0][r][q][lane];
+#pragma unroll
+            for (int w = 1; w < waves / 2; ++w) v[q] += sh.part[w][r][q][lane];
+        }
+        u32x4 o;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = pack_bf16(v[2 * d], v[2 * d + 1]);
+        uint16_t* row = p.grad + (static_cast<size_t>(id) * rank + r0 + r) * p.width;
+        if (VEC || p.vec)
+            store8<true>(row, col, p.width, o);
+        else
+            store8<false>(row, col, p.width, o);
+    }
 }
 
 // ---- many rows ----------------------------------------------------------------
@@ -774,6 +885,17 @@ hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b,
                          offsets, rows, rank, kMaxSegTiles);
 }
 
+// The gradient of few rows in three launches. 5120 -> 17408, 4 adapters, us (this /
+// sorted tiles): rank 16, 1 row 15 / 26, 32 rows 18 / 27, 100 rows 23 / 30, 200
+// rows 32 / 33, 300 rows 41 / 34; rank 64, 32 rows 41 / 53; rank 8, 200 rows 26 /
+// 33.
+constexpr int kBackwardRows = 256;
+constexpr int kBackwardRanks = 3200;
+static_assert(kBackwardRows <= kFewRows, "a thread finds a row");
+bool direct_backward(int rows, int rank) {
+    return rows > 0 && rows <= kBackwardRows && rows * rank <= kBackwardRanks;
+}
+
 // Few rows whose first factor is small enough for every workgroup of a row to
 // read: one launch. 5120 -> 17408 at rank 16: 1 row 6.5 us against 8.5 in two
 // launches, 8 rows 9.0 / 8.8 (and one launch less for the host to issue), 32
@@ -786,10 +908,17 @@ int direct_splits(int width) { return (width + kDirectCols - 1) / kDirectCols; }
 
 }  // namespace
 
+// The few-row gradient's workspace: the splits' inner products, then their sums.
+size_t direct_partial_floats(int rows, int out, int rank) {
+    return (static_cast<size_t>(direct_splits(out)) * rows * rank + 3) / 4 * 4;
+}
+
 size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, bool backward) {
     if (!backward && direct_rows(rows, rank) && direct_in_one(rows, in, rank)) return 0;
     if (!backward && direct_rows(rows, rank))
         return static_cast<size_t>(direct_splits(in)) * rows * rank * sizeof(float);
+    if (backward && direct_backward(rows, rank))
+        return (direct_partial_floats(rows, out, rank) + static_cast<size_t>(rows) * rank) * sizeof(float);
     return make_plan(rows, in, out, rank, count, backward).bytes;
 }
 
@@ -836,6 +965,25 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                                     const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                                     bool vec_in, bool vec_out, void* ws, hipStream_t st) {
     hipError_t e;
+    if (direct_backward(rows, f.rank)) {
+        float* partial = static_cast<float*>(ws);
+        float* inner = partial + direct_partial_floats(rows, f.out, f.rank);
+        const int splits = direct_splits(f.out);
+        e = launch_kernel(vec_out ? direct_inner_kernel<true> : direct_inner_kernel<false>,
+                          dim3(splits, rows), dim3(kWgThreads), st, dy, ids, f.b, f.out, f.rank,
+                          f.count, partial);
+        if (e != hipSuccess) return e;
+        e = launch_kernel(vec_in ? direct_expand_kernel<true> : direct_expand_kernel<false>,
+                          dim3(direct_splits(f.in), rows), dim3(kWgThreads), st, partial, splits, ids,
+                          f.a, f.scales, f.in, f.rank, f.count, base, dx, inner);
+        if (e != hipSuccess) return e;
+        const FewSide side_b{dy, u, db, f.out, direct_splits(f.out), vec_out};
+        const FewSide side_a{x, inner, da, f.in, direct_splits(f.in), vec_in};
+        return launch_kernel(vec_in && vec_out ? direct_outer_kernel<true> : direct_outer_kernel<false>,
+                             dim3(side_b.chunks + side_a.chunks, f.count,
+                                  (f.rank + kFewRanks - 1) / kFewRanks),
+                             dim3(kFewThreads), st, side_b, side_a, ids, f.scales, rows, f.rank);
+    }
     const Plan p = make_plan(rows, f.in, f.out, f.rank, f.count, true);
     if ((e = launch_route(ids, rows, f.count, true, at<int32_t>(ws, p.offsets),
                           at<int32_t>(ws, p.order), nullptr, at<int32_t>(ws, p.counts), st)))

@@ -168,8 +168,8 @@ int trellis_adapters_backward(const uint16_t* dy, const uint16_t* x, const float
     if ((st = check_workspace(workspace, workspace_bytes,
                               trellis_adapters_workspace_bytes(f, rows, 1))))
         return st;
-    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && aligned(dx, 16);
-    const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, nullptr);
+    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && all16(dx, da, nullptr);
+    const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, db);
     return status_of(trellis::launch_adapters_backward(dy, x, u, ids, factors(f), rows, base, dx, da,
                                                        db, vec_in, vec_out, workspace, stream));
 }

@@ -162,8 +162,9 @@ int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
  * base: bf16 [rows][in], the shared projection's own gradient (the product of
  * dy with the same codes on the other axis), or null for zeros; dx may be
  * `base` itself. da and db have the factors' layout and are written whole:
- * zeros for adapters without rows (also for rows = 0). Sums run in float32; g
- * and u enter the second products as two bf16 parts. workspace: 16-byte
+ * zeros for adapters without rows (also for rows = 0). Sums run in float32;
+ * beyond few rows g and u enter the second products as two bf16 parts.
+ * workspace: 16-byte
  * aligned, at least trellis_adapters_workspace_bytes(f, rows, 1) bytes.
  */
 int trellis_adapters_backward(const uint16_t *dy, const uint16_t *x, const float *u,

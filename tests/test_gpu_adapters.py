@@ -98,6 +98,7 @@ SIZES = [(1, 256, 16, 1, 1), (1, 512, 4111, 16, 8), (2, 300, 520, 13, 3), (31, 1
          (200, 777, 1000, 33, 4), (500, 264, 640, 64, 70), (130, 512, 384, 128, 3),
          (97, 1, 1, 17, 1024), (256, 264, 392, 16, 6), (257, 264, 392, 16, 6),
          (512, 64, 72, 8, 9), (513, 64, 72, 8, 9), (8, 512, 1032, 16, 3), (9, 512, 1032, 16, 3),
+         (200, 520, 1030, 16, 3), (201, 520, 1030, 16, 3), (256, 72, 515, 12, 2), (25, 264, 600, 128, 3),
          (1025, 136, 520, 16, 1), (2500, 256, 192, 32, 2),
          (3000, 64, 133, 8, 5)]
 
