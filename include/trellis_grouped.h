@@ -100,11 +100,12 @@ int trellis_combine_backward(const uint16_t *dout, const uint16_t *y, const floa
  * device; codes: uint32 [experts][...], every expert's in the layout of `g`
  * (g describes one expert); scales: float32 [experts][stored rows]; lut:
  * float32 [4096], shared by the experts; y: bf16 [rows][out], whose rows
- * outside every expert are left as they were. Offsets are taken as ascending
- * and clamped to [0, rows]. rows <= TRELLIS_MAX_SLOTS. x, codes, lut and y
+ * outside every expert are left as they were. Offsets are clamped to [0, rows];
+ * ones that are not ascending leave it open which expert's product a row gets,
+ * if any. rows <= TRELLIS_MAX_SLOTS. x, codes, lut and y
  * need 16-byte alignment. workspace: 16-byte aligned, at least
  * trellis_experts_workspace_bytes(g, rows, experts) bytes (0 for few rows per
- * expert and on axis 0: may be null then).
+ * expert: may be null then).
  */
 int trellis_experts(const uint16_t *x, int32_t rows, const int32_t *offsets, int32_t experts,
                     const uint32_t *codes, const float *scales, const float *lut,
@@ -164,8 +165,8 @@ int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
  * `base` itself. da and db have the factors' layout and are written whole:
  * zeros for adapters without rows (also for rows = 0). Sums run in float32;
  * beyond few rows g and u enter the second products as two bf16 parts.
- * workspace: 16-byte
- * aligned, at least trellis_adapters_workspace_bytes(f, rows, 1) bytes.
+ * workspace: 16-byte aligned, at least
+ * trellis_adapters_workspace_bytes(f, rows, 1) bytes.
  */
 int trellis_adapters_backward(const uint16_t *dy, const uint16_t *x, const float *u,
                               const int32_t *ids, int32_t rows, const trellis_adapter_set *f,

@@ -133,6 +133,22 @@ def test_wild_offsets(gpu_lib, axis, i, o, rows):
     assert bool((y == 3.0).all())
 
 
+@pytest.mark.parametrize("axis,i,o", [(1, 256, 64), (0, 64, 256)])
+@pytest.mark.parametrize("rows", [30, 3000])
+def test_offsets_that_go_back_and_forth(gpu_lib, axis, i, o, rows):
+    """More tiles than ascending offsets can make: within bounds, every row
+    untouched or one expert's (here all experts are alike)."""
+    say(f"experts with offsets back and forth, axis {axis}, {rows} rows")
+    p = Problem(11, axis, i, o, 3, [rows])
+    x, _, codes, scales, lut = p.cuda()
+    y = torch.full((rows, o), 3.0, dtype=torch.bfloat16, device="cuda")
+    cut = torch.tensor([0, rows] * 8 + [0], dtype=torch.int32, device="cuda")
+    gpu_lib.experts(x, cut, codes.repeat(16, 1, 1), scales.repeat(16, 1), lut, p.shape, y=y)
+    want = p.want().to(torch.bfloat16)
+    same = (y.cpu() == want).all(1)
+    assert bool((same | (y.cpu() == 3.0).all(1)).all()) and bool(same.any())
+
+
 @pytest.mark.parametrize("axis,i,o", [(1, 512, 80), (0, 80, 512)])
 def test_not_finite_rows_stay_alone(gpu_lib, axis, i, o):
     say(f"experts with NaN rows, axis {axis}")
