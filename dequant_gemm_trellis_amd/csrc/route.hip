@@ -20,7 +20,9 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kMaxSteps = 8;          // 64-slot steps of a wave: their ids stay in registers
 constexpr int kMaxChunkSlots = kMaxSteps * kSortThreads;
-constexpr int kOneChunk = 8192;       // slots that one workgroup sorts alone
+// Slots that one workgroup sorts alone: 256 slots of 128 groups 4.5 us, 4096 7.8,
+// 8192 11.7, where two launches take 3.4 + 7.1 us (and the host one more launch).
+constexpr int kOneChunk = 8192;
 constexpr int kChunkSlots = 2048;     // slots per workgroup of several, at least
 constexpr int kMaxChunks = kMaxSlots / kMaxChunkSlots;  // each reads all chunks' counts
 
@@ -182,7 +184,10 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
 //
 // All of these move rows at the memory's rate and do next to nothing to them.
 // A thread holds 8 columns (16 bytes; rows of other lengths: one column), and
-// a token's positions are uniform over its workgroup.
+// a token's positions are uniform over its workgroup. Width 2048, 8 slots per
+// token, 128 experts: 8192 tokens out 59 us (302 MB, 5.1 TB/s; a device copy
+// reaches 5.5), the gradient of 4097 tokens' way back 59 us (286 MB, 4.8 TB/s),
+// 32 tokens back 4 us.
 constexpr int kMoveThreads = 256;
 
 template <bool VEC> struct Cols { static constexpr int n = VEC ? 8 : 1; };
