@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kSortThreads) void route_place_kernel(
     }
     __syncthreads();
     // Per key: slots of all chunks, of earlier chunks, and of earlier waves.
-    int base = 0;  // first place of the keys of this round
+    int base = 0;  // first place of these 1024 keys
     for (int g0 = 0; g0 < keys; g0 += kSortThreads) {
         const int g = g0 + tid;
         int mine = 0, earlier = 0, all = 0;

@@ -331,6 +331,9 @@ class Route(NamedTuple):
     position: torch.Tensor  # [tokens, top_k] place of each slot, -1 if dropped
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
 def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: int) -> None:
     """Refuse a tensor that is not dense, of this type and shape, and on `device`."""
     if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
@@ -345,6 +348,8 @@ def _want(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, device: 
 def _dims(name: str, t: torch.Tensor, n: int) -> torch.Size:
     if t.dim() != n:
         raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    if max(t.shape) > _INT32_MAX:  # the C ABI's sizes would wrap around
+        raise ValueError(f"{name}: a dimension of {tuple(t.shape)} is larger than {_INT32_MAX}")
     return t.shape
 
 
@@ -406,6 +411,8 @@ def route(ids, groups: int, workspace=None, stream=None) -> Route:
     dev = _device(ids)
     _want("ids", ids, torch.int32, (tokens, top_k), dev)
     fn = "trellis_route"
+    if not 0 < groups <= _INT32_MAX:
+        raise TrellisError(fn, ERR_GEOMETRY)
     nbytes = _lib.trellis_route_workspace_bytes(tokens, top_k, groups)
     with _on(stream, dev):
         ws, ws_bytes, keep = _workspace(fn, nbytes, workspace, ids)

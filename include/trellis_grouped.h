@@ -146,7 +146,9 @@ typedef struct trellis_adapter_set {
  * not touched); u: float32 [rows][rank], kept for the backward pass, or null.
  * u and the sum are float32; for few rows every product is a float32 one,
  * beyond that u enters the second product as two bf16 parts (an error of at
- * most 2^-16 of it). workspace: 16-byte aligned, at least
+ * most 2^-16 of it). Where a value of b that a row meets is infinite, y is not
+ * finite there, but it may be NaN where the formula has an infinity (the parts'
+ * products differ in sign or are 0 times infinity). workspace: 16-byte aligned, at least
  * trellis_adapters_workspace_bytes(f, rows, 0) bytes.
  */
 int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
@@ -164,7 +166,8 @@ int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
  * dy with the same codes on the other axis), or null for zeros; dx may be
  * `base` itself. da and db have the factors' layout and are written whole:
  * zeros for adapters without rows (also for rows = 0). Sums run in float32;
- * beyond few rows g and u enter the second products as two bf16 parts.
+ * beyond few rows g and u enter the second products as two bf16 parts, and an
+ * infinity in a, x or dy may give NaN where the formula has an infinity.
  * workspace: 16-byte aligned, at least
  * trellis_adapters_workspace_bytes(f, rows, 1) bytes.
  */

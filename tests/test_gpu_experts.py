@@ -277,3 +277,43 @@ def test_a_layer_of_experts(gpu_lib, tokens):
             slack_dx[m] += half * back.abs() + (half + 2 * fp32) * wd[m, j] * (c.abs() @ dd[m].abs())
     for got, ref, more in ((z, want, slack), (dx, want_dx, slack_dx), (dw, want_dw, slack_dw)):
         assert bool(((got.double().cpu() - ref).abs() <= 1.01 * (more + half * (ref.abs() + more))).all())
+
+
+@pytest.mark.parametrize("axis,i,o", [(1, 256, 16), (0, 32, 256)])
+@pytest.mark.parametrize("most", [1, 40])
+def test_the_most_experts(gpu_lib, axis, i, o, most):
+    """1024 experts, three of four without rows; up to 40 rows of the others."""
+    say(f"1024 experts axis {axis}, up to {most} rows each")
+    g = np.random.default_rng([11, axis, most])
+    counts = [int(n) if e % 4 == 1 or e == 1023 else 0 for e, n in enumerate(g.integers(1, most + 1, 1024))]
+    p = Problem(11, axis, i, o, 2, counts)
+    assert torch.equal(gpu_lib.experts(*p.cuda(), p.shape).cpu(), p.want().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("groups", [0, 1025, 2 ** 32 + 4])
+def test_route_refuses_numbers_of_groups(gpu_lib, groups):
+    with pytest.raises(gpu_lib.TrellisError):
+        gpu_lib.route(torch.zeros((3, 2), dtype=torch.int32, device="cuda"), groups)
+
+
+def test_two_calls_at_once(gpu_lib):
+    """The same codes and rows on two streams at the same time, each call with a
+    workspace of its own: every call's bits are those of a call alone."""
+    say("experts on two streams at once")
+    p = Problem(12, 1, 512, 300, 3, [200, 0, 90, 170])
+    q = Problem(12, 0, 300, 512, 4, [150, 40, 0, 300])
+    a, b = p.cuda(), q.cuda()
+    want = [v.want().to(torch.bfloat16) for v in (p, q)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(6):
+        for args, shape in ((a, p.shape), (b, q.shape)):
+            for n in range(2):
+                got[n].append(gpu_lib.experts(*args, shape, stream=streams[n]))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for ys in got:
+        for c, y in enumerate(ys):
+            assert torch.equal(y.cpu(), want[c % 2])

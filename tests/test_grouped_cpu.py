@@ -231,3 +231,18 @@ def test_experts_validation(T, axis):
         assert experts(ws=0) == T.ERR_WORKSPACE
         assert experts(ws_bytes=need - 1) == T.ERR_WORKSPACE
     assert experts(rows=0, x=0, y=0) == T.OK  # nothing to do, nothing enqueued
+
+
+def test_sizes_past_32_bits_do_not_wrap_around(T):
+    """A dimension of 2^32 would arrive at the C ABI as zero."""
+    for t in (torch.zeros((1, 1), dtype=torch.int32).expand(2 ** 32, 1),
+              torch.zeros((1, 1), dtype=torch.int32).expand(1, 2 ** 32)):
+        with pytest.raises(ValueError, match="larger than"):
+            T.route(t, 4)
+    x = torch.zeros((1, 1), dtype=torch.bfloat16).expand(2 ** 32, 1)
+    r = T.Route(torch.zeros(5, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                torch.zeros((1, 1), dtype=torch.int32))
+    with pytest.raises(ValueError, match="larger than"):
+        T.dispatch(x, r)
+    with pytest.raises(ValueError, match="larger than"):
+        T.combine(x, None, r)
