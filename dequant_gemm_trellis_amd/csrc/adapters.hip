@@ -291,14 +291,16 @@ __global__ __launch_bounds__(kOneThreads) void direct_kernel(
 }
 
 // The gradients of an adapter's factors over few rows: a workgroup takes 512
-// columns and 16 ranks of one adapter, finds its rows (ascending), and its eight
-// waves take them in turn: 16 ranks x 8 columns of float32 sums per lane. Wave q
-// adds wave q + 4's sums to its own, then the four meet in order. `inner` are
-// the float32 rank-long values without the scale. Grid: (column chunks of side a
-// then of side b, adapters, 16 ranks each).
-constexpr int kFewThreads = 512;
-constexpr int kFewRows = kFewThreads;  // rows of a call, at most: a thread finds one
-constexpr int kFewRanks = 16;
+// columns and 4 ranks of one adapter, finds its rows (ascending), and its waves
+// take them in turn: 4 ranks x 8 columns of float32 sums per lane. Of W waves,
+// wave q adds wave q + W / 2's sums to its own, then the halves meet in order.
+// `inner` are the float32 rank-long values without the scale. Grid: (column
+// chunks of side a then of side b, adapters, 4 ranks each).
+// 5120 -> 17408, 4 adapters, us: 16 ranks a workgroup 7.9 (32 rows at rank 16) and
+// 19.1 (at rank 64), 8 ranks 6.7 and 15.6, 4 ranks 6.3 and 15.9 (two ranks 7.3 and
+// 18.6); with 4 waves instead of 8 5.6 and 10.6. The rows come from the L2 again.
+constexpr int kFewRows = 256;  // rows of a call, at most: a thread finds one
+constexpr int kFewRanks = 4;
 
 struct FewSide {
     const uint16_t* x;   // the wide rows
@@ -308,13 +310,13 @@ struct FewSide {
     bool vec;
 };
 
-template <bool VEC>
+template <int WAVES, bool VEC>
 __device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int wave,
                                          const int* __restrict__ list,
                                          const float (*__restrict__ coef)[kFewRanks],
                                          float (&acc)[kFewRanks][8]) {
 #pragma unroll 4
-    for (int i = wave; i < n; i += kFewThreads / kWave) {
+    for (int i = wave; i < n; i += WAVES) {
         const u32x4 v = load8<VEC>(p.x + static_cast<size_t>(list[i]) * p.width, col, p.width, true);
         float e[8];
 #pragma unroll
@@ -329,11 +331,11 @@ __device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int w
     }
 }
 
-template <bool VEC>
-__global__ __launch_bounds__(kFewThreads) void direct_outer_kernel(
+template <int THREADS, bool VEC>
+__global__ __launch_bounds__(THREADS) void direct_outer_kernel(
     FewSide a, FewSide b, const int32_t* __restrict__ ids, const float* __restrict__ scales, int rows,
     int rank) {
-    constexpr int waves = kFewThreads / kWave;
+    constexpr int waves = THREADS / kWave;
     union Shared {
         float coef[kFewRows][kFewRanks];
         float part[waves / 2][kFewRanks][8][kWave];
@@ -359,7 +361,7 @@ __global__ __launch_bounds__(kFewThreads) void direct_outer_kernel(
     if (mine) list[before + __popcll(votes & ((1ull << lane) - 1))] = tid;
     __syncthreads();
     const float scale = scales[id];
-    for (int i = tid; i < n * kFewRanks; i += kFewThreads) {
+    for (int i = tid; i < n * kFewRanks; i += THREADS) {
         const int r = r0 + i % kFewRanks;
         sh.coef[i / kFewRanks][i % kFewRanks] =
             r < rank ? p.inner[static_cast<size_t>(list[i / kFewRanks]) * rank + r] * scale : 0.f;
@@ -367,9 +369,9 @@ __global__ __launch_bounds__(kFewThreads) void direct_outer_kernel(
     __syncthreads();
     float acc[kFewRanks][8] = {};
     if (VEC || p.vec)
-        add_rows<true>(p, col, n, wave, list, sh.coef, acc);
+        add_rows<waves, true>(p, col, n, wave, list, sh.coef, acc);
     else
-        add_rows<false>(p, col, n, wave, list, sh.coef, acc);
+        add_rows<waves, false>(p, col, n, wave, list, sh.coef, acc);
     __syncthreads();  // the parts take the coefficients' place
     auto each = [&](auto&& f) {
 #pragma unroll
@@ -901,6 +903,15 @@ bool direct_backward(int rows, int rank) {
     return rows > 0 && rows <= kBackwardRows && rows * rank <= kBackwardRanks;
 }
 
+// The few-row outer products with 4 waves a workgroup, where there are two
+// workgroups or more per compute unit; with 8 where there are fewer and the rows
+// of an adapter are shared by more waves. Us (4 waves / 8): 512 workgroups 5.3 / 5.9,
+// 704 5.6 / 6.3 and 8.1 / 8.6, 2816 10.6 / 15.9; 352 7.5 / 7.0, 160 5.2 / 4.9, 88
+// 14.6 / 10.0.
+bool many_groups(const dim3& grid) {
+    return static_cast<int64_t>(grid.x) * grid.y * grid.z >= 2 * cu_count();
+}
+
 // Few rows whose first factor is small enough for every workgroup of a row to
 // read: one launch. 5120 -> 17408 at rank 16: 1 row 6.5 us against 8.5 in two
 // launches, 8 rows 9.0 / 8.8 (and one launch less for the host to issue), 32
@@ -984,10 +995,13 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
         if (e != hipSuccess) return e;
         const FewSide side_b{dy, u, db, f.out, direct_splits(f.out), vec_out};
         const FewSide side_a{x, inner, da, f.in, direct_splits(f.in), vec_in};
-        return launch_kernel(vec_in && vec_out ? direct_outer_kernel<true> : direct_outer_kernel<false>,
-                             dim3(side_b.chunks + side_a.chunks, f.count,
-                                  (f.rank + kFewRanks - 1) / kFewRanks),
-                             dim3(kFewThreads), st, side_b, side_a, ids, f.scales, rows, f.rank);
+        const dim3 grid(side_b.chunks + side_a.chunks, f.count, (f.rank + kFewRanks - 1) / kFewRanks);
+        const bool vec = vec_in && vec_out;
+        if (many_groups(grid))
+            return launch_kernel(vec ? direct_outer_kernel<256, true> : direct_outer_kernel<256, false>,
+                                 grid, dim3(256), st, side_b, side_a, ids, f.scales, rows, f.rank);
+        return launch_kernel(vec ? direct_outer_kernel<512, true> : direct_outer_kernel<512, false>,
+                             grid, dim3(512), st, side_b, side_a, ids, f.scales, rows, f.rank);
     }
     const Plan p = make_plan(rows, f.in, f.out, f.rank, f.count, true);
     if ((e = launch_route(ids, rows, f.count, true, at<int32_t>(ws, p.offsets),
