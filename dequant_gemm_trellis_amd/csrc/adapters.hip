@@ -496,19 +496,89 @@ struct TileInfo {
     int32_t rows;
 };
 
+// And of a segment of the outer sums: up to kSegRows rows of an adapter, which
+// has one at least.
+constexpr int kSegRows = kMaxSegTiles * kTileRows;
+struct SegInfo {
+    int32_t group;  // -1: no segment
+    int32_t tile;   // its first
+    int32_t rows;
+    int32_t slot;   // of its float32 sums where the adapter has several; else -1
+};
+
+// The list of `segments` segments (the last ones may be none) of the adapters
+// 64 b, 64 b + 1, ..., by one wave: a lane per adapter. Searched for by each
+// workgroup of the outer sums it would cost 16 steps of a wave's sums for 1024
+// adapters.
+__device__ __forceinline__ void list_segments(const int32_t* __restrict__ offsets, int count, int rows,
+                                              int b, int segments, SegInfo* __restrict__ segs) {
+    const int lane = threadIdx.x & 63;
+    auto group = [&](int g, int& n, int& tiles, int& shared) {
+        int size = 0;
+        n = tiles = shared = 0;
+        if (g < count) {
+            const int first = min(max(offsets[g], 0), rows);
+            size = min(max(offsets[g + 1], first), rows) - first;
+            n = max(1, (size + kSegRows - 1) / kSegRows);
+            tiles = (size + kTileRows - 1) / kTileRows;
+            shared = n > 1 ? n : 0;
+        }
+        return size;
+    };
+    int before = 0, tiles = 0, shared = 0;
+    for (int c = 0; c < b; ++c) {
+        int n, t, s;
+        group(64 * c + lane, n, t, s);
+        before += n;
+        tiles += t;
+        shared += s;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        before += __shfl_xor(before, d);
+        tiles += __shfl_xor(tiles, d);
+        shared += __shfl_xor(shared, d);
+    }
+    int n, t, s;
+    const int g = 64 * b + lane, size = group(g, n, t, s);
+    int end = n, tend = t, send = s;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int e = __shfl_up(end, d), te = __shfl_up(tend, d), se = __shfl_up(send, d);
+        if (lane >= d) {
+            end += e;
+            tend += te;
+            send += se;
+        }
+    }
+    for (int i = 0; i < n; ++i) {
+        const int at = before + end - n + i;
+        if (at < segments)
+            segs[at] = {g, tiles + tend - t + i * kMaxSegTiles, min(size - i * kSegRows, kSegRows),
+                        s ? shared + send - s + i : -1};
+    }
+    if (64 * b + 64 >= count)
+        for (int i = before + __shfl(end, 63) + lane; i < segments; i += 64) segs[i] = {-1, 0, 0, -1};
+}
+
 // A tile's row numbers and group, its inner products summed from the splits
 // (ascending), and their operand forms; a thread per row and rank.
 //   by_row [tile][64][R][hi 16 | lo 16]    (expand; scaled)
 //   by_rank[tile][R][hi | lo][16][64]      (outer; scaled)
 //   u_rank                                 the same of the forward pass's u
-// Rows past the tile's last and ranks past the last are zeros there.
+// Rows past the tile's last and ranks past the last are zeros there. The first
+// workgroups list the segments of the outer sums as well.
 // Grid: (tiles, 4 r16): 256 of the tile's 64 x 16 r16 values each.
 __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const float* __restrict__ partial, int splits, int tiles, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ order, const float* __restrict__ scales, int rows, int rank, int r16,
     int count, TileInfo* __restrict__ info, int32_t* __restrict__ tile_rows,
     uint16_t* __restrict__ by_row, uint16_t* __restrict__ by_rank, float* __restrict__ u_out,
-    const float* __restrict__ u_in, uint16_t* __restrict__ u_rank) {
+    const float* __restrict__ u_in, uint16_t* __restrict__ u_rank, SegInfo* __restrict__ segs,
+    int segments) {
+    if (segs && blockIdx.y == 0 && threadIdx.x < kWave)
+        for (int b = blockIdx.x; 64 * b < count; b += gridDim.x)
+            list_segments(offsets, count, rows, b, segments, segs);
     const int t = blockIdx.x, ranks = 16 * r16;
     const int i = blockIdx.y * kWgThreads + threadIdx.x;
     const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
@@ -647,20 +717,17 @@ struct OuterSide {
     bool vec;
 };
 
-// A segment of an adapter's tiles: its tiles go to the four waves in turn, which
-// are summed in wave order. An adapter of one segment (or without rows) is
+// A segment of an adapter's tiles: its tiles go to the four waves in turn, and the
+// sums of the waves that had any are added in wave order. An adapter of one segment (or without rows) is
 // written to `grad` in bf16; the float32 sums of the others' segments go to
 // `sums`.
 template <int R, bool VEC>
-__device__ __forceinline__ void outer_segment(const OuterSide& p, const Found& at, int strip, int r0,
-                                              int r16, int rank, int seg_tiles, const int* seg_rows,
-                                              float* sum) {
+__device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo& seg, int strip, int r0,
+                                              int r16, int rank, const int* seg_rows, float* sum) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, c = lane >> 4;
     const int width = p.width, col = strip * kStrip + 8 * j;
-    const int group_tiles = (at.end - at.first + kTileRows - 1) / kTileRows;
-    const int n = min(group_tiles - at.index * seg_tiles, seg_tiles);
-    const int t0 = at.tiles + at.index * seg_tiles;
+    const int n = (seg.rows + kTileRows - 1) / kTileRows, t0 = seg.tile;
     // This wave's 32-row halves of the segment's tiles wave, wave + 4, ...; the
     // next half's rows are loaded while one is multiplied.
     struct Half {
@@ -702,7 +769,8 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const Found& a
         if (step + 2 < steps) load(q[0], step + 2);
         multiply(q[1]);
     }
-    for (int w = 0; w < kWgWaves; ++w) {
+    const int ways = min(n, kWgWaves);  // none: an adapter without rows
+    for (int w = 0; w < ways; ++w) {
         if (wave == w) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -715,50 +783,67 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const Found& a
         }
         __syncthreads();
     }
-    for (int i = tid; i < 16 * R * kStrip; i += kWgThreads) {
-        const int r = 16 * r0 + i / kStrip, k = strip * kStrip + i % kStrip;
+    // 8 columns per thread at a time
+    for (int i = tid; i < 16 * R * kStrip / 8; i += kWgThreads) {
+        const int r = 16 * r0 + i / (kStrip / 8), k = strip * kStrip + 8 * (i % (kStrip / 8));
         if (r >= rank || k >= width) continue;
-        if (group_tiles > seg_tiles)
-            p.sums[(static_cast<size_t>(at.shared + at.index) * rank + r) * width + k] = sum[i];
-        else
-            p.grad[(static_cast<size_t>(at.group) * rank + r) * width + k] = round_bf16(sum[i]);
+        floatx4 v[2] = {};
+        if (ways) {
+            v[0] = *reinterpret_cast<const floatx4*>(sum + 8 * i);
+            v[1] = *reinterpret_cast<const floatx4*>(sum + 8 * i + 4);
+        }
+        if (seg.slot >= 0) {
+            float* o = p.sums + (static_cast<size_t>(seg.slot) * rank + r) * width + k;
+            if constexpr (VEC) {
+                *reinterpret_cast<floatx4*>(o) = v[0];
+                *reinterpret_cast<floatx4*>(o + 4) = v[1];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < width) o[e] = v[e / 4][e % 4];
+            }
+        } else {
+            const u32x4 o = {pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
+                             pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3])};
+            store8<VEC>(p.grad + (static_cast<size_t>(seg.group) * rank + r) * width, k, width, o);
+        }
     }
 }
 
-// Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces.
+// Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces. Without
+// a list (no rows) every adapter is one segment of none.
 // Grid: (strips of side a then of side b, segments, rank pairs).
 template <int R, bool VEC>
 __global__ __launch_bounds__(kWgThreads) void outer_kernel(
-    OuterSide a, OuterSide b, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ tile_rows, int rows, int rank, int r16, int count, int seg_tiles) {
-    __shared__ float sum[16 * R * kStrip];
-    __shared__ int seg_rows[kMaxSegTiles * kTileRows];
-    const Found at = find_entry(offsets, count, rows, seg_tiles * kTileRows, true, blockIdx.y);
-    if (at.group < 0) return;
-    const int t0 = at.tiles + at.index * seg_tiles;
-    const int n = min((at.end - at.first + kTileRows - 1) / kTileRows - at.index * seg_tiles, seg_tiles);
-    for (int i = threadIdx.x; i < n * kTileRows; i += kWgThreads)
-        seg_rows[i] = tile_rows[static_cast<size_t>(t0) * kTileRows + i];
+    OuterSide a, OuterSide b, const SegInfo* __restrict__ segs, const int32_t* __restrict__ tile_rows,
+    int rank, int r16) {
+    __shared__ __attribute__((aligned(16))) float sum[16 * R * kStrip];
+    __shared__ int seg_rows[kSegRows];
+    SegInfo seg = {static_cast<int>(blockIdx.y), 0, 0, -1};
+    if (segs) seg = segs[blockIdx.y];
+    if (seg.group < 0) return;
+    const int n = (seg.rows + kTileRows - 1) / kTileRows * kTileRows;
+    for (int i = threadIdx.x; i < n; i += kWgThreads)
+        seg_rows[i] = tile_rows[static_cast<size_t>(seg.tile) * kTileRows + i];
     __syncthreads();
     const bool second = static_cast<int>(blockIdx.x) >= a.strips;
     const OuterSide& p = second ? b : a;
     const int strip = second ? blockIdx.x - a.strips : blockIdx.x, r0 = blockIdx.z * R;
     if (VEC || p.vec)
-        outer_segment<R, true>(p, at, strip, r0, r16, rank, seg_tiles, seg_rows, sum);
+        outer_segment<R, true>(p, seg, strip, r0, r16, rank, seg_rows, sum);
     else
-        outer_segment<R, false>(p, at, strip, r0, r16, rank, seg_tiles, seg_rows, sum);
+        outer_segment<R, false>(p, seg, strip, r0, r16, rank, seg_rows, sum);
 }
 
 // The segments' sums of the adapters of several, ascending, rounded to bf16, of
 // both sides. Grid: (column chunks of side a then of side b, ranks, adapters).
 __global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
-    OuterSide a, OuterSide b, int chunks_a, const int32_t* __restrict__ offsets, int rows, int rank,
-    int seg_tiles) {
+    OuterSide a, OuterSide b, int chunks_a, const int32_t* __restrict__ offsets, int rows, int rank) {
     const int n_ad = blockIdx.z, r = blockIdx.y;
     const bool second = static_cast<int>(blockIdx.x) >= chunks_a;
     const OuterSide& p = second ? b : a;
     const int k = (second ? blockIdx.x - chunks_a : blockIdx.x) * kWgThreads + threadIdx.x;
-    const int lane = threadIdx.x & 63, per = seg_tiles * kTileRows;
+    const int lane = threadIdx.x & 63, per = kSegRows;
     int before = 0, mine = 0;  // shared segments of the adapters before, and this one's segments
     for (int g0 = 0; g0 <= n_ad; g0 += 64) {
         const int g = g0 + lane;
@@ -800,7 +885,7 @@ struct Plan {
     int splits, split_cols;     // column splits of the inner products
     int segments;               // segments of the outer sums, at most
     int shared;                 // those of adapters with several, at most
-    size_t offsets, order, counts, partial, info, tile_rows, by_row, by_rank, u_rank, sums_a, sums_b, bytes;
+    size_t offsets, order, counts, partial, info, tile_rows, segs, by_row, by_rank, u_rank, sums_a, sums_b, bytes;
 };
 
 int inner_splits(int tiles, int width) {
@@ -822,9 +907,9 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     const int width = backward ? out : in;
     p.split_cols = split_columns(width, inner_splits(p.tiles, width));
     p.splits = (width + p.split_cols - 1) / p.split_cols;
-    const int per = kMaxSegTiles * kTileRows;
-    p.segments = count + rows / per;             // sum of max(1, ceil(n / per)), at most
-    p.shared = rows > per ? 2 * (rows / per) : 0;  // n > per: ceil(n / per) <= 2 floor(n / per)
+    p.segments = count + rows / kSegRows;  // sum of max(1, ceil(n / kSegRows)), at most
+    // n > kSegRows: ceil(n / kSegRows) <= 2 floor(n / kSegRows)
+    p.shared = rows > kSegRows ? 2 * (rows / kSegRows) : 0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -840,6 +925,7 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     p.tile_rows = take(tiles * kTileRows * 4);
     p.by_row = take(tiles * kTileRows * ranks * 2 * 2);
     if (backward) {
+        p.segs = take(p.segments * sizeof(SegInfo));
         p.by_rank = take(tiles * kTileRows * ranks * 2 * 2);
         p.u_rank = take(tiles * kTileRows * ranks * 2 * 2);
         p.sums_a = take(static_cast<size_t>(p.shared) * rank * in * 4);
@@ -881,15 +967,14 @@ hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int r
 template <int R>
 hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b, int rows, int rank,
                           int count, void* ws, hipStream_t st) {
-    const int32_t* offsets = at<int32_t>(ws, p.offsets);
     const hipError_t e = launch_kernel(
         a.vec && b.vec ? outer_kernel<R, true> : outer_kernel<R, false>,
-        dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b, offsets,
-        at<int32_t>(ws, p.tile_rows), rows, rank, p.r16, count, kMaxSegTiles);
+        dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b,
+        rows ? at<SegInfo>(ws, p.segs) : nullptr, at<int32_t>(ws, p.tile_rows), rank, p.r16);
     if (e != hipSuccess || !p.shared) return e;
     const int ca = (a.width + kWgThreads - 1) / kWgThreads, cb = (b.width + kWgThreads - 1) / kWgThreads;
     return launch_kernel(outer_sum_kernel, dim3(ca + cb, rank, count), dim3(kWgThreads), st, a, b, ca,
-                         offsets, rows, rank, kMaxSegTiles);
+                         at<int32_t>(ws, p.offsets), rows, rank);
 }
 
 // The gradient of few rows in three launches. 5120 -> 17408, 4 adapters, us (this /
@@ -971,7 +1056,7 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
                            at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
-                           at<uint16_t>(ws, p.by_row), nullptr, u, nullptr, nullptr)))
+                           at<uint16_t>(ws, p.by_row), nullptr, u, nullptr, nullptr, nullptr, 0)))
         return e;
     return launch_expand(p, f.b, f.out, f.rank, f.count, base, y, vec_out, ws, st);
 }
@@ -1016,7 +1101,7 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
                            at<uint16_t>(ws, p.by_row), at<uint16_t>(ws, p.by_rank), nullptr, u,
-                           at<uint16_t>(ws, p.u_rank))))
+                           at<uint16_t>(ws, p.u_rank), at<SegInfo>(ws, p.segs), p.segments)))
         return e;
     auto strips = [](int width) { return (width + kStrip - 1) / kStrip; };
     const OuterSide side_b{dy, at<uint16_t>(ws, p.u_rank), db, at<float>(ws, p.sums_b), f.out,
