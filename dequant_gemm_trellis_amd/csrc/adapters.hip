@@ -505,13 +505,26 @@ struct SegInfo {
     int32_t rows;
     int32_t slot;   // of its float32 sums where the adapter has several; else -1
 };
+// And of an adapter of several.
+struct SumInfo {
+    int32_t group;  // -1: no adapter
+    int32_t slot;   // of its first segment
+    int32_t n;      // its segments
+    int32_t unused;
+};
 
-// The list of `segments` segments (the last ones may be none) of the adapters
-// 64 b, 64 b + 1, ..., by one wave: a lane per adapter. Searched for by each
+// Segments of adapters of several are counted in the low bits, the adapters above:
+// 2^20 rows make 2048 of the one and 1024 of the other at most.
+constexpr int kOneSeveral = 1 << 12;
+
+// The lists of `segments` segments and of `several` adapters of several segments
+// (the last ones may be none), those of the adapters 64 b, 64 b + 1, ..., by one
+// wave: a lane per adapter. Searched for by each
 // workgroup of the outer sums it would cost 16 steps of a wave's sums for 1024
 // adapters.
 __device__ __forceinline__ void list_segments(const int32_t* __restrict__ offsets, int count, int rows,
-                                              int b, int segments, SegInfo* __restrict__ segs) {
+                                              int b, int segments, SegInfo* __restrict__ segs, int several,
+                                              SumInfo* __restrict__ sums) {
     const int lane = threadIdx.x & 63;
     auto group = [&](int g, int& n, int& tiles, int& shared) {
         int size = 0;
@@ -521,7 +534,7 @@ __device__ __forceinline__ void list_segments(const int32_t* __restrict__ offset
             size = min(max(offsets[g + 1], first), rows) - first;
             n = max(1, (size + kSegRows - 1) / kSegRows);
             tiles = (size + kTileRows - 1) / kTileRows;
-            shared = n > 1 ? n : 0;
+            shared = n > 1 ? n + kOneSeveral : 0;
         }
         return size;
     };
@@ -551,14 +564,19 @@ __device__ __forceinline__ void list_segments(const int32_t* __restrict__ offset
             send += se;
         }
     }
+    const int slot = (shared + send - s) % kOneSeveral, index = (shared + send - s) / kOneSeveral;
     for (int i = 0; i < n; ++i) {
         const int at = before + end - n + i;
         if (at < segments)
             segs[at] = {g, tiles + tend - t + i * kMaxSegTiles, min(size - i * kSegRows, kSegRows),
-                        s ? shared + send - s + i : -1};
+                        s ? slot + i : -1};
     }
-    if (64 * b + 64 >= count)
+    if (s && index < several) sums[index] = {g, slot, n, 0};
+    if (64 * b + 64 >= count) {
+        const int all = shared + __shfl(send, 63);
         for (int i = before + __shfl(end, 63) + lane; i < segments; i += 64) segs[i] = {-1, 0, 0, -1};
+        for (int i = all / kOneSeveral + lane; i < several; i += 64) sums[i] = {-1, 0, 0, 0};
+    }
 }
 
 // A tile's row numbers and group, its inner products summed from the splits
@@ -575,10 +593,10 @@ __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     int count, TileInfo* __restrict__ info, int32_t* __restrict__ tile_rows,
     uint16_t* __restrict__ by_row, uint16_t* __restrict__ by_rank, float* __restrict__ u_out,
     const float* __restrict__ u_in, uint16_t* __restrict__ u_rank, SegInfo* __restrict__ segs,
-    int segments) {
+    int segments, SumInfo* __restrict__ sums, int several) {
     if (segs && blockIdx.y == 0 && threadIdx.x < kWave)
         for (int b = blockIdx.x; 64 * b < count; b += gridDim.x)
-            list_segments(offsets, count, rows, b, segments, segs);
+            list_segments(offsets, count, rows, b, segments, segs, several, sums);
     const int t = blockIdx.x, ranks = 16 * r16;
     const int i = blockIdx.y * kWgThreads + threadIdx.x;
     const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
@@ -836,34 +854,21 @@ __global__ __launch_bounds__(kWgThreads) void outer_kernel(
 }
 
 // The segments' sums of the adapters of several, ascending, rounded to bf16, of
-// both sides. Grid: (column chunks of side a then of side b, ranks, adapters).
-__global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(
-    OuterSide a, OuterSide b, int chunks_a, const int32_t* __restrict__ offsets, int rows, int rank) {
-    const int n_ad = blockIdx.z, r = blockIdx.y;
+// both sides. Grid: (column chunks of side a then of side b, ranks, adapters of
+// several segments at most).
+__global__ __launch_bounds__(kWgThreads) void outer_sum_kernel(OuterSide a, OuterSide b, int chunks_a,
+                                                               const SumInfo* __restrict__ sums, int rank) {
+    const SumInfo info = sums[blockIdx.z];
+    const int r = blockIdx.y;
     const bool second = static_cast<int>(blockIdx.x) >= chunks_a;
     const OuterSide& p = second ? b : a;
     const int k = (second ? blockIdx.x - chunks_a : blockIdx.x) * kWgThreads + threadIdx.x;
-    const int lane = threadIdx.x & 63, per = kSegRows;
-    int before = 0, mine = 0;  // shared segments of the adapters before, and this one's segments
-    for (int g0 = 0; g0 <= n_ad; g0 += 64) {
-        const int g = g0 + lane;
-        int n = 0;
-        if (g <= n_ad) {
-            const int first = min(max(offsets[g], 0), rows);
-            n = (min(max(offsets[g + 1], first), rows) - first + per - 1) / per;
-        }
-        int s = g < n_ad && n > 1 ? n : 0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-        before += s;
-        mine = __shfl(n, n_ad & 63);
-    }
-    if (mine <= 1 || k >= p.width) return;
+    if (info.group < 0 || k >= p.width) return;
     float v = 0.f;
 #pragma unroll 4
-    for (int q = 0; q < mine; ++q)
-        v += p.sums[(static_cast<size_t>(before + q) * rank + r) * p.width + k];
-    p.grad[(static_cast<size_t>(n_ad) * rank + r) * p.width + k] = round_bf16(v);
+    for (int q = 0; q < info.n; ++q)
+        v += p.sums[(static_cast<size_t>(info.slot + q) * rank + r) * p.width + k];
+    p.grad[(static_cast<size_t>(info.group) * rank + r) * p.width + k] = round_bf16(v);
 }
 
 // ---- plans and launches ---------------------------------------------------------
@@ -884,8 +889,8 @@ struct Plan {
     int r16, tiles;             // 16-rank operands; tiles at most
     int splits, split_cols;     // column splits of the inner products
     int segments;               // segments of the outer sums, at most
-    int shared;                 // those of adapters with several, at most
-    size_t offsets, order, counts, partial, info, tile_rows, segs, by_row, by_rank, u_rank, sums_a, sums_b, bytes;
+    int several, shared;        // adapters with several, and their segments, at most
+    size_t offsets, order, counts, partial, info, tile_rows, segs, sums, by_row, by_rank, u_rank, sums_a, sums_b, bytes;
 };
 
 int inner_splits(int tiles, int width) {
@@ -909,7 +914,8 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     p.splits = (width + p.split_cols - 1) / p.split_cols;
     p.segments = count + rows / kSegRows;  // sum of max(1, ceil(n / kSegRows)), at most
     // n > kSegRows: ceil(n / kSegRows) <= 2 floor(n / kSegRows)
-    p.shared = rows > kSegRows ? 2 * (rows / kSegRows) : 0;
+    p.several = rows > kSegRows ? rows / kSegRows : 0;
+    p.shared = 2 * p.several;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -926,6 +932,7 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     p.by_row = take(tiles * kTileRows * ranks * 2 * 2);
     if (backward) {
         p.segs = take(p.segments * sizeof(SegInfo));
+        p.sums = take(p.several * sizeof(SumInfo));
         p.by_rank = take(tiles * kTileRows * ranks * 2 * 2);
         p.u_rank = take(tiles * kTileRows * ranks * 2 * 2);
         p.sums_a = take(static_cast<size_t>(p.shared) * rank * in * 4);
@@ -971,21 +978,24 @@ hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b,
         a.vec && b.vec ? outer_kernel<R, true> : outer_kernel<R, false>,
         dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b,
         rows ? at<SegInfo>(ws, p.segs) : nullptr, at<int32_t>(ws, p.tile_rows), rank, p.r16);
-    if (e != hipSuccess || !p.shared) return e;
+    if (e != hipSuccess || !p.several) return e;
     const int ca = (a.width + kWgThreads - 1) / kWgThreads, cb = (b.width + kWgThreads - 1) / kWgThreads;
-    return launch_kernel(outer_sum_kernel, dim3(ca + cb, rank, count), dim3(kWgThreads), st, a, b, ca,
-                         at<int32_t>(ws, p.offsets), rows, rank);
+    return launch_kernel(outer_sum_kernel, dim3(ca + cb, rank, p.several), dim3(kWgThreads), st, a, b,
+                         ca, at<SumInfo>(ws, p.sums), rank);
 }
 
-// The gradient of few rows in three launches. 5120 -> 17408, 4 adapters, us (this /
-// sorted tiles): rank 16, 1 row 15 / 26, 32 rows 18 / 27, 100 rows 23 / 30, 200
-// rows 32 / 33, 300 rows 41 / 34; rank 64, 32 rows 41 / 53; rank 8, 200 rows 26 /
-// 33.
+// The gradient of few rows in three launches that follow each row (sorted tiles
+// take six); with more adapters up to more ranks over all rows, as the tiles of
+// each cost more. 5120 -> 17408, us (this / sorted tiles): 4 adapters, rank 16, 1
+// row 13 / 26, 100 rows 21 / 30, 200 rows 29 / 33; rank 32, 100 rows 29 / 36, 200
+// rows 44 / 40; one adapter, 200 rows, rank 16 31 / 32, rank 32 45 / 37; 32
+// adapters, 250 rows, rank 32 78 / 81; 64, 200 rows, rank 64 185 / 238; 110, 256
+// rows, rank 128 543 / 719.
 constexpr int kBackwardRows = 256;
-constexpr int kBackwardRanks = 3200;
+constexpr int kBackwardRanks = 4096, kRanksPerAdapter = 256;
 static_assert(kBackwardRows <= kFewRows, "a thread finds a row");
-bool direct_backward(int rows, int rank) {
-    return rows > 0 && rows <= kBackwardRows && rows * rank <= kBackwardRanks;
+bool direct_backward(int rows, int rank, int count) {
+    return rows > 0 && rows <= kBackwardRows && rows * rank <= kBackwardRanks + kRanksPerAdapter * count;
 }
 
 // The few-row outer products with 4 waves a workgroup, where there are two
@@ -1018,7 +1028,7 @@ size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, 
     if (!backward && direct_rows(rows, rank) && direct_in_one(rows, in, rank)) return 0;
     if (!backward && direct_rows(rows, rank))
         return static_cast<size_t>(direct_splits(in)) * rows * rank * sizeof(float);
-    if (backward && direct_backward(rows, rank))
+    if (backward && direct_backward(rows, rank, count))
         return (direct_partial_floats(rows, out, rank) + static_cast<size_t>(rows) * rank) * sizeof(float);
     return make_plan(rows, in, out, rank, count, backward).bytes;
 }
@@ -1056,7 +1066,7 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
                            at<float>(ws, p.partial), p.splits, p.tiles, at<int32_t>(ws, p.offsets),
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
-                           at<uint16_t>(ws, p.by_row), nullptr, u, nullptr, nullptr, nullptr, 0)))
+                           at<uint16_t>(ws, p.by_row), nullptr, u, nullptr, nullptr, nullptr, 0, nullptr, 0)))
         return e;
     return launch_expand(p, f.b, f.out, f.rank, f.count, base, y, vec_out, ws, st);
 }
@@ -1066,7 +1076,7 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                                     const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                                     bool vec_in, bool vec_out, void* ws, hipStream_t st) {
     hipError_t e;
-    if (direct_backward(rows, f.rank)) {
+    if (direct_backward(rows, f.rank, f.count)) {
         float* partial = static_cast<float*>(ws);
         float* inner = partial + direct_partial_floats(rows, f.out, f.rank);
         const int splits = direct_splits(f.out);
@@ -1101,7 +1111,8 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                            at<int32_t>(ws, p.order), f.scales, rows, f.rank, p.r16, f.count,
                            at<TileInfo>(ws, p.info), at<int32_t>(ws, p.tile_rows),
                            at<uint16_t>(ws, p.by_row), at<uint16_t>(ws, p.by_rank), nullptr, u,
-                           at<uint16_t>(ws, p.u_rank), at<SegInfo>(ws, p.segs), p.segments)))
+                           at<uint16_t>(ws, p.u_rank), at<SegInfo>(ws, p.segs), p.segments, at<SumInfo>(ws, p.sums),
+                           p.several)))
         return e;
     auto strips = [](int width) { return (width + kStrip - 1) / kStrip; };
     const OuterSide side_b{dy, at<uint16_t>(ws, p.u_rank), db, at<float>(ws, p.sums_b), f.out,

@@ -407,3 +407,21 @@ def test_beside_the_projection(gpu_lib, M):
     ref_dx, ref_da, ref_db = p.backward(u.cpu(), base=False)
     both(dx, p.dy, weights, ref_dx)
     assert near(da, ref_da) and near(db, ref_db)
+
+
+def test_long_runs_of_some_of_many_adapters(gpu_lib):
+    """Adapters of several 1024-row segments among many of few rows or none, past
+    the 64 adapters that a wave looks at together."""
+    say("adapters, 2100 rows of one of 130")
+    p = Problem(18, 5000, 40, 72, 8, 130)
+    ids = np.random.default_rng(18).integers(-1, 130, 5000).astype(np.int32)
+    ids[::5][:900] = 3
+    ids[1:4600:2] = 70
+    ids[2::4][:1150] = 129
+    p.ids = torch.from_numpy(ids)
+    d = p.cuda()
+    _, u = p.forward()
+    grads = gpu_lib.adapters_backward(d["dy"], d["x"], u.float().cuda(), d["ids"], d["a"], d["b"],
+                                      d["scales"], base=d["base_x"])
+    for got, want in zip(grads, p.backward(u)):
+        assert same(got, want)
