@@ -199,6 +199,38 @@ def test_gradient_against_differences(gpu_lib):
     assert abs((v2 - v0) - float(inner.sum())) <= 1.01 * (e0 + e2 + BF16 * float(inner.abs().sum()))
 
 
+def test_gradient_is_exactly_the_differences(gpu_lib):
+    """combine is linear in y and in the weights: for sparse small integers, whose
+    outputs and products are exact in bf16, the change of <dout, out> over a step of
+    the weights or of y is the step's product with its gradient, to the last bit."""
+    say("combine gradient against exact differences")
+    T, (tokens, top_k, groups, width) = gpu_lib, (40, 4, 10, 512)
+    g, r, order, position = state(T, 9, tokens, top_k, groups, width)
+
+    def draw(*shape, zeros=0.75):
+        v = g.integers(-2, 3, shape) * (g.random(shape) >= zeros)
+        return torch.from_numpy(v.astype(np.float32))
+
+    y, dout = draw(tokens * top_k, width).to(torch.bfloat16), draw(tokens, width).to(torch.bfloat16)
+    w = draw(tokens, top_k, zeros=0.2)
+    dy, dw = T.combine_backward(dout.cuda(), y.cuda(), w.cuda(), r, dy=torch.zeros_like(y).cuda())
+    dy, dw = dy.double().cpu(), dw.double().cpu()
+
+    def value(yy, ww):
+        out = T.combine(yy.to(torch.bfloat16).cuda(), ww.cuda(), r).double().cpu()
+        assert float(out.abs().max()) <= 128
+        return float((dout.double() * out).sum())
+
+    before = value(y, w)
+    for scale in (1, -1):
+        step = scale * draw(tokens, top_k, zeros=0.2)
+        change = float((dw * step.double()).sum())
+        assert value(y, w + step) - before == change and change != 0
+        step = scale * draw(tokens * top_k, width)
+        change = float((dy * step.double()).sum())
+        assert value(y.float() + step, w) - before == change and change != 0
+
+
 def test_dispatch_gradient_is_the_plain_combine(gpu_lib):
     """<dispatch(x), g> = <x, combine(g)> for exactly summed small integers."""
     say("dispatch and its gradient")
