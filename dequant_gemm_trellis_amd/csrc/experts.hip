@@ -488,8 +488,11 @@ __device__ __forceinline__ u32x4 x_operand(const ExArgs& p, int row0, int end, i
 
 // Tiles of MT x 16 rows: a wave takes 64 columns of a tile, 4 per lane. A last
 // step of fewer than 32 rows takes the last 32 stored rows again, with zeros in
-// the x operands for those already counted (operands_kernel); in >= 32.
-template <int K, int MT>
+// the x operands (operands_kernel) and scales of zero for those already counted:
+// an infinite weight times a zero would be NaN; in >= 32. TAIL: in is no multiple
+// of 32 (an instance of its own: the step's code behind the loop costs whole steps
+// 7% at k = 2 and 128 rows).
+template <int K, int MT, bool TAIL>
 __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
     constexpr int CL = 4;
     using Ps = Pieces<K, CL>;
@@ -528,7 +531,7 @@ __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) x[m] = load_x(0, m);
         floatx4 acc[CL][MT] = {};
-        for (int step = 0; step < steps; ++step) {
+        auto one = [&](int step) {
             Ps ps;
             ps.set(q, s.sh);
             // the scales first: they are moved at the step's end, and a move
@@ -545,6 +548,14 @@ __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
             });
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = next_sc[i];
+        };
+        const int whole = TAIL ? p.in / 32 : steps;
+        for (int step = 0; step < whole; ++step) one(step);
+        if constexpr (TAIL) {  // none for the rows already counted
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p.in - 32 + 8 * c + i < 32 * whole) sc[i] = 0.f;
+            one(whole);
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -592,15 +603,16 @@ __global__ __launch_bounds__(kExThreads) void experts0_few_kernel(ExArgs p) {
                 }
                 return;
             }
-            // the last rows, one by one; past the end x is zero
+            // the last rows, one by one; past the end x is zero, and so is the
+            // scale: an infinite weight times a zero would be NaN
             const uint32_t row = static_cast<uint32_t>(32 * c * s.row_words);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int r = min(32 * step + 8 * c + i, p.in - 1);
+                const int past = 32 * step + 8 * c + i, r = min(past, p.in - 1);
                 const uint32_t* w = s.codes + static_cast<uint64_t>(r) * s.row_words;
                 q.q.a[i] = w[(s.at_a - row) / 4];
                 q.q.b[i] = w[(s.at_b - row) / 4];
-                q.sc[i] = s.scales[r];
+                q.sc[i] = past < p.in ? s.scales[r] : 0.f;
             }
         },
         [&] { stage_table<K>(tab, p.lut); },
@@ -672,7 +684,9 @@ hipError_t launch_wide(const ExpertWeights& w, ExArgs p, void* ws, hipStream_t s
                                        p.in, operands);
     if (e != hipSuccess) return e;
     p.x = static_cast<const uint16_t*>(ws);
-    return launch_kernel(w.axis == 1 ? experts1_kernel<K, MT> : experts0_kernel<K, MT>,
+    return launch_kernel(w.axis == 1      ? experts1_kernel<K, MT>
+                         : w.in % 32 == 0 ? experts0_kernel<K, MT, false>
+                                          : experts0_kernel<K, MT, true>,
                          dim3(cu_count()), dim3(kExThreads), st, p);
 }
 

@@ -261,3 +261,44 @@ def test_a_layer_of_experts(gpu_lib):
             slack_dx[m] += half * back.abs() + (half + 2 * fp32) * bsize
     for got, ref, more in ((z, want, slack), (dx, want_dx, slack_dx), (dw, want_dw, slack_dw)):
         assert bool(((got.double().cpu() - ref).abs() <= 1.01 * (more + half * (ref.abs() + more))).all())
+
+
+@pytest.mark.parametrize("i,rows", [(37, 40), (5, 40), (300, 40), (264, 40), (37, 4003), (300, 4003),
+                                    (264, 4003), (45, 8007)])
+def test_infinite_weights_on_axis_0(gpu_lib, i, rows):
+    """Stored rows whose weights overflow, where the last step of 32 stored rows is
+    not full (i % 32): only what the product counts enters it, so an infinity stays
+    one (or is NaN where its x is 0, by the formula)."""
+    say(f"experts with infinite weights, axis 0, {i} inputs, {rows} rows")
+    p = Problem(30, 0, i, 1280, 3, [rows // 3, rows - rows // 3])
+    p.lut[p.lut == 0] = 1.0
+    # the last stored row, and one that the last 32 stored rows hold beside the last step's
+    bad = sorted({i - 1, max(0, 32 * ((i - 1) // 32) - 1)})
+    p.scales[:, bad] = 3e38
+    p.x[:, bad] = 1.0
+    p.x[::5, bad[0]] = 0.0
+    p.x[1::5] = p.x[1::5].abs()
+    y = gpu_lib.experts(*p.cuda(), p.shape).cpu()
+    parts, sizes, at = [], [], 0
+    for e, n in enumerate(p.counts):
+        w = p.weights(e)
+        assert bool(w[bad].isinf().any())
+        q = p.x[at:at + n].double()
+        finite = q @ torch.where(w.isinf(), 0.0, w)
+        sizes.append(q.abs() @ torch.where(w.isinf(), 0.0, w.abs()))
+        for b in bad:  # infinite terms, added one by one
+            finite += q[:, b, None] * torch.where(w[b].isinf(), w[b], 0.0)[None]
+        parts.append(finite)
+        at += n
+    want, size = torch.cat(parts), torch.cat(sizes)
+    rounded, y = want.to(torch.bfloat16).double(), y.double()
+    assert bool(rounded.isinf().any()) and bool(rounded.isnan().any()) and bool(rounded.isfinite().any())
+    assert torch.equal(y.isnan(), rounded.isnan())
+    assert torch.equal(y[y.isinf()], rounded[rounded.isinf()])
+    assert torch.equal(y.isinf(), rounded.isinf())
+    # A weight of +-1 times the scale stays finite, and a float32 sum that it enters
+    # is off by up to 2^-24 of the magnitudes per addition: two such weights of
+    # opposite signs cancel and leave that error, not the small terms between them.
+    fine = rounded.isfinite()
+    off, fp32 = (y - want)[fine].abs(), (i + 1) * 2.0 ** -24 * size[fine]
+    assert bool((off <= 2.0 ** -8 * (want[fine].abs() + fp32) + fp32).all())
