@@ -14,10 +14,12 @@
 // adapter, all in float32.
 // Many rows: the rows are sorted by adapter and cut into tiles of 64 rows of
 // one adapter, which share the factor's values in bf16 matrix instructions.
-// There a rank-long float32 value w (u or g) enters as two bf16 parts, hi =
-// bf16(w) and lo = bf16(w - hi): 16 bits of mantissa, where one part alone
-// would add as much error as the rounding of the output. The two parts of 16
-// ranks fill the 32 contraction slots of one 16x16x32 instruction.
+// There a rank-long float32 value w (u or g) enters as three bf16 parts whose sum
+// is w: its mantissa's upper, middle and lower 8 bits, so that every product is
+// exact and the sums are float32 as those of few rows. (Two parts, 16 bits of
+// mantissa, take 3-5% less time, but y then differs from float32 products by
+// 8.1e-5 of its norm, with three by 3.2e-5, as other orders of the sums do.) Two
+// parts of 16 ranks fill the 32 contraction slots of one 16x16x32 instruction.
 //
 // A matrix instruction contracts over 8 consecutive values per lane. Where the
 // contraction runs across stored rows (ranks in expand, tokens in outer), a
@@ -78,12 +80,21 @@ __device__ __forceinline__ u32x4 patch_column(const u32x4 (&row)[8]) {
     return r;
 }
 
-__device__ __forceinline__ float part_high(float w) {
-    return static_cast<float>(static_cast<__bf16>(w));
-}
-// The rest of w (none behind an infinity or a NaN, which the high part holds).
-__device__ __forceinline__ float part_low(float w, float high) {
-    return __builtin_isfinite(high) ? w - high : 0.f;
+// The bf16 parts of a float32 value, the high one first: 8 bits of mantissa each,
+// cut off and not rounded, so that none overflows. Infinities and NaN are in the
+// first alone.
+constexpr int kBf16Parts = 3;
+struct Parts3 {
+    uint16_t p[kBf16Parts];
+};
+__device__ __forceinline__ Parts3 split3(float w) {
+    if (!__builtin_isfinite(w)) return {{round_bf16(w), 0, 0}};
+    const uint32_t hi = __float_as_uint(w) & 0xFFFF0000u;
+    const float rest = w - __uint_as_float(hi);
+    const uint32_t mid = __float_as_uint(rest) & 0xFFFF0000u;
+    const uint32_t lo = __float_as_uint(rest - __uint_as_float(mid));
+    return {{static_cast<uint16_t>(hi >> 16), static_cast<uint16_t>(mid >> 16),
+             static_cast<uint16_t>(lo >> 16)}};
 }
 
 // ---- few rows ----------------------------------------------------------------
@@ -581,12 +592,13 @@ __device__ __forceinline__ void list_segments(const int32_t* __restrict__ offset
 
 // A tile's row numbers and group, its inner products summed from the splits
 // (ascending), and their operand forms; a thread per row and rank.
-//   by_row [tile][64][R][hi 16 | lo 16]    (expand; scaled)
-//   by_rank[tile][R][hi | lo][16][64]      (outer; scaled)
-//   u_rank                                 the same of the forward pass's u
+//   by_row [tile][64][R][part][16]    (expand; scaled)
+//   by_rank[tile][R][part][16][64]    (outer; scaled)
+//   u_rank                            the same of the forward pass's u
 // Rows past the tile's last and ranks past the last are zeros there. The first
 // workgroups list the segments of the outer sums as well.
-// Grid: (tiles, 4 r16): 256 of the tile's 64 x 16 r16 values each.
+// Grid: (tiles, 4 r16): 16 rows x 16 ranks of the tile each, so that the rows of
+// a rank are stored side by side.
 __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const float* __restrict__ partial, int splits, int tiles, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ order, const float* __restrict__ scales, int rows, int rank, int r16,
@@ -598,12 +610,12 @@ __global__ __launch_bounds__(kWgThreads) void tile_kernel(
         for (int b = blockIdx.x; 64 * b < count; b += gridDim.x)
             list_segments(offsets, count, rows, b, segments, segs, several, sums);
     const int t = blockIdx.x, ranks = 16 * r16;
-    const int i = blockIdx.y * kWgThreads + threadIdx.x;
-    const int row = i / ranks, r = i % ranks, s = r / 16, rr = r % 16;
+    const int s = blockIdx.y / 4, rr = threadIdx.x % 16;
+    const int row = 16 * (blockIdx.y % 4) + threadIdx.x / 16, r = 16 * s + rr;
     const Found at = find_entry(offsets, count + 1, rows, kTileRows, false, t);
     const int p0 = at.first + at.index * kTileRows;
     const int n = at.group < 0 ? 0 : min(kTileRows, at.end - p0);
-    if (i == 0) info[t] = {at.group, n};
+    if (blockIdx.y == 0 && threadIdx.x == 0) info[t] = {at.group, n};
     if (at.group < 0) return;
     const int orig = row < n ? order[p0 + row] : -1;
     if (r == 0) tile_rows[t * kTileRows + row] = orig;
@@ -616,28 +628,28 @@ __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const float scale = scales[at.group];
     float v = 0.f;
     if (live) {
-        const float* p = partial + static_cast<size_t>(t) * (kTileRows * ranks) + i;
+        const float* p = partial + static_cast<size_t>(t) * (kTileRows * ranks) + row * ranks + r;
         const size_t step = static_cast<size_t>(tiles) * (kTileRows * ranks);
 #pragma unroll 8
         for (int k = 0; k < splits; ++k) v += p[k * step];
         if (u_out) u_out[u_at] = v;
     }
-    const float w = v * scale, hi = part_high(w), lo = part_low(w, hi);
-    uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * 32 + rr;
-    q[0] = round_bf16(hi);
-    q[16] = round_bf16(lo);
+    const Parts3 w = split3(v * scale);
+    uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * (16 * kBf16Parts) + rr;
+#pragma unroll
+    for (int part = 0; part < kBf16Parts; ++part) q[16 * part] = w.p[part];
     if (!by_rank) return;
-    const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * 2 * 16 + rr) * kTileRows + row;
-    by_rank[rank_at] = round_bf16(hi);
-    by_rank[rank_at + 16 * kTileRows] = round_bf16(lo);
-    const float uw = live ? u_in[u_at] * scale : 0.f;
-    const float uh = part_high(uw), ul = part_low(uw, uh);
-    u_rank[rank_at] = round_bf16(uh);
-    u_rank[rank_at + 16 * kTileRows] = round_bf16(ul);
+    const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * kBf16Parts * 16 + rr) * kTileRows + row;
+    const Parts3 uw = split3(live ? u_in[u_at] * scale : 0.f);
+#pragma unroll
+    for (int part = 0; part < kBf16Parts; ++part) {
+        by_rank[rank_at + part * 16 * kTileRows] = w.p[part];
+        u_rank[rank_at + part * 16 * kTileRows] = uw.p[part];
+    }
 }
 
 // The eight operands (column 8 j + q each) of 16 ranks of a factor's strip:
-// lanes c and c + 2 hold the ranks of the hi and of the lo parts alike.
+// lanes c and c + 2 hold the same ranks, which meet two parts.
 template <bool VEC>
 __device__ __forceinline__ void factor_operands(const uint16_t* f, int r, int rank, int col, int width,
                                                 int c, u32x4 (&op)[8]) {
@@ -675,7 +687,7 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
         return;
     }
     const uint16_t* f = factor + static_cast<size_t>(ti.group) * rank * width;
-    const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * 32;
+    const uint16_t* rows_op = by_row + static_cast<size_t>(t) * kTileRows * r16 * (16 * kBf16Parts);
     // a row's number read from memory between the rows' loads would wait for
     // all of them: each lane holds one and passes it on
     const int my_row = trow[lane];
@@ -693,23 +705,27 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
         for (int i = 0; i < 4; ++i)
             bv[i] = load8<VEC>((base ? base : y) + static_cast<size_t>(max(row[i], 0)) * width, col, width,
                                base && row[i] >= 0);
-        const uint16_t* a_at = rows_op + static_cast<size_t>(16 * s + j) * r16 * 32 + 8 * c;
+        const uint16_t* a_at = rows_op + static_cast<size_t>(16 * s + j) * r16 * (16 * kBf16Parts) + 8 * c;
         floatx4 acc[8] = {};
+        // the third part's ranks are lanes 0 and 1's; zeros in the others
+        auto multiply = [&](int r, const u32x4 (&f)[8]) {
+            const uint16_t* at = a_at + 16 * kBf16Parts * r;
+            const u32x4 two = *reinterpret_cast<const u32x4*>(at);
+            u32x4 third = {0u, 0u, 0u, 0u};
+            if (c < 2) third = *reinterpret_cast<const u32x4*>(at + 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                acc[q] = mfma16x16x32(as_bf16x8(two), as_bf16x8(f[q]), acc[q]);
+                acc[q] = mfma16x16x32(as_bf16x8(third), as_bf16x8(f[q]), acc[q]);
+            }
+        };
         if constexpr (R > 0) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(a_at + 32 * r);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    acc[q] = mfma16x16x32(as_bf16x8(a), as_bf16x8(op[r][q]), acc[q]);
-            }
+            for (int r = 0; r < R; ++r) multiply(r, op[r]);
         } else {
             for (int r = 0; r < r16; ++r) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(a_at + 32 * r);
                 factor_operands<VEC>(f, r, rank, col, width, c, op[0]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    acc[q] = mfma16x16x32(as_bf16x8(a), as_bf16x8(op[0][q]), acc[q]);
+                multiply(r, op[0]);
             }
         }
 #pragma unroll
@@ -749,7 +765,7 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     // This wave's 32-row halves of the segment's tiles wave, wave + 4, ...; the
     // next half's rows are loaded while one is multiplied.
     struct Half {
-        u32x4 patch[8], a[R][2];
+        u32x4 patch[8], a[R][kBf16Parts];
     };
     auto load = [&](Half& q, int step) {
         const int t = wave + kWgWaves * (step >> 1), h = step & 1;
@@ -761,9 +777,10 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < kBf16Parts; ++part)
                 q.a[r][part] = *reinterpret_cast<const u32x4*>(
-                    p.by_rank + (((static_cast<size_t>(t0 + t) * r16 + r0 + r) * 2 + part) * 16 + j) * kTileRows +
+                    p.by_rank +
+                    (((static_cast<size_t>(t0 + t) * r16 + r0 + r) * kBf16Parts + part) * 16 + j) * kTileRows +
                     32 * h + 8 * c);
     };
     floatx4 acc[R][8] = {};
@@ -772,10 +789,10 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
             constexpr int e = decltype(qc)::value;
             const u32x4 b = patch_column<e>(q.patch);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                acc[r][e] = mfma16x16x32(as_bf16x8(q.a[r][0]), as_bf16x8(b), acc[r][e]);
-                acc[r][e] = mfma16x16x32(as_bf16x8(q.a[r][1]), as_bf16x8(b), acc[r][e]);
-            }
+            for (int part = 0; part < kBf16Parts; ++part)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r][e] = mfma16x16x32(as_bf16x8(q.a[r][part]), as_bf16x8(b), acc[r][e]);
         });
     };
     const int steps = n > wave ? 2 * ((n - wave + kWgWaves - 1) / kWgWaves) : 0;
@@ -929,12 +946,13 @@ Plan make_plan(int rows, int in, int out, int rank, int count, bool backward) {
     p.partial = take(p.splits * tiles * kTileRows * ranks * 4);
     p.info = take(tiles * sizeof(TileInfo));
     p.tile_rows = take(tiles * kTileRows * 4);
-    p.by_row = take(tiles * kTileRows * ranks * 2 * 2);
+    const size_t parts = tiles * kTileRows * ranks * kBf16Parts * sizeof(uint16_t);
+    p.by_row = take(parts);
     if (backward) {
         p.segs = take(p.segments * sizeof(SegInfo));
         p.sums = take(p.several * sizeof(SumInfo));
-        p.by_rank = take(tiles * kTileRows * ranks * 2 * 2);
-        p.u_rank = take(tiles * kTileRows * ranks * 2 * 2);
+        p.by_rank = take(parts);
+        p.u_rank = take(parts);
         p.sums_a = take(static_cast<size_t>(p.shared) * rank * in * 4);
         p.sums_b = take(static_cast<size_t>(p.shared) * rank * out * 4);
     }

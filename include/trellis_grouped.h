@@ -144,12 +144,11 @@ typedef struct trellis_adapter_set {
  * (trellis_prefill or trellis_gemv of x), or null for zeros; y: bf16
  * [rows][out], which may be `base` itself (rows without an adapter are then
  * not touched); u: float32 [rows][rank], kept for the backward pass, or null.
- * u and the sum are float32; for few rows every product is a float32 one,
- * beyond that u enters the second product as two bf16 parts (an error of at
- * most 2^-16 of it). Where a value of b that a row meets is infinite, y is not
- * finite there, but it may be NaN where the formula has an infinity (the parts'
- * products differ in sign or are 0 times infinity). workspace: 16-byte aligned, at least
- * trellis_adapters_workspace_bytes(f, rows, 0) bytes.
+ * u, the products and the sums are float32; beyond few rows u enters the second
+ * product as three bf16 parts whose sum it is. Where a value of b that a row
+ * meets is infinite, y is not finite there, but it may be NaN where the formula
+ * has an infinity (a part of 0 times infinity). workspace: 16-byte aligned, at
+ * least trellis_adapters_workspace_bytes(f, rows, 0) bytes.
  */
 int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
                      const trellis_adapter_set *f, const uint16_t *base, uint16_t *y, float *u,
@@ -165,9 +164,9 @@ int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
  * base: bf16 [rows][in], the shared projection's own gradient (the product of
  * dy with the same codes on the other axis), or null for zeros; dx may be
  * `base` itself. da and db have the factors' layout and are written whole:
- * zeros for adapters without rows (also for rows = 0). Sums run in float32;
- * beyond few rows g and u enter the second products as two bf16 parts, and an
- * infinity in a, x or dy may give NaN where the formula has an infinity.
+ * zeros for adapters without rows (also for rows = 0). Products and sums are
+ * float32; beyond few rows g and u enter the second products as three bf16 parts,
+ * and an infinity in a, x or dy may give NaN where the formula has an infinity.
  * workspace: 16-byte aligned, at least
  * trellis_adapters_workspace_bytes(f, rows, 1) bytes.
  */

@@ -149,3 +149,45 @@ def test_beside_a_projection_of_many_rows(gpu_lib, M):
     p.base_x = (p.dy.double() @ weights).to(torch.bfloat16)
     for got, ref in zip((dx, da, db), p.backward(want_u)):
         assert same(got, ref)
+
+
+@pytest.mark.parametrize("i,o,rank", [(512, 264, 16), (511, 391, 24), (512, 264, 64)])
+def test_inner_values_keep_their_mantissa(gpu_lib, i, o, rank):
+    """Inner values of up to 20 bits and outputs below 2^24: exact in float32, so
+    equal to the rounded exact value. (With u and g cut to 16 bits, hundreds of
+    these outputs round to another bf16 value.)"""
+    say(f"adapters in tiles, long inner values, {i} -> {o}, rank {rank}")
+    p = tiled(gpu_lib, Problem(46, 600, i, o, rank, 8))
+    g = np.random.default_rng(46)
+
+    def wide(t):
+        v = g.integers(-127, 128, tuple(t.shape)).astype(np.float32)
+        return torch.from_numpy(v).to(torch.bfloat16)
+
+    small = {n: getattr(p, n) for n in ("x", "a", "dy", "b")}
+    most = 2.0 ** 24
+
+    p.x, p.a = wide(p.x), wide(p.a)  # long u, short b: the forward pass and db
+    d = p.cuda()
+    want, want_u = p.forward()
+    assert float(want_u.abs().max()) >= 2 ** 17
+    assert float((want_u.abs().sum(1)).max()) * 2 < most
+    y, u = gpu_lib.adapters(d["x"], d["ids"], d["a"], d["b"], d["scales"], base=d["base_y"],
+                            keep_inner=True)
+    assert torch.equal(u.double().cpu(), want_u) and same(y, want)
+    p.x, p.a = small["x"], small["a"]
+    d = p.cuda()
+    db = gpu_lib.adapters_backward(d["dy"], d["x"], u, d["ids"], d["a"], d["b"], d["scales"])[2]
+    assert max(float(want_u[p.ids == n].abs().sum(0).max()) for n in range(8)) * 2 < most
+    assert same(db, p.backward(want_u)[2])
+
+    p.dy, p.b = wide(p.dy), wide(p.b)  # long g, short a and x: dx and da
+    d = p.cuda()
+    u = torch.zeros((600, rank), device="cuda")
+    dx, da, _ = gpu_lib.adapters_backward(d["dy"], d["x"], u, d["ids"], d["a"], d["b"], d["scales"],
+                                          base=d["base_x"])
+    for n in range(8):
+        v = (float(p.scales[n]) * (p.dy[p.ids == n].double() @ p.b[n].double().T)).abs()
+        assert float(v.max()) >= 2 ** 17 and float(v.sum(0).max()) < most and float(v.sum(1).max()) < most
+    want_dx, want_da, _ = p.backward(u.double().cpu())
+    assert same(dx, want_dx) and same(da, want_da)
