@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kWgThreads) void inner_kernel(
     __shared__ float sum[kTileRows * 16 * R];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, c = lane >> 4;
-    const Found at = find_entry(offsets, count, rows, kTileRows, false, blockIdx.y);
+    const Found at = find_entry(offsets, count, rows, kTileRows, blockIdx.y);
     if (at.group < 0) return;
     const int p0 = at.first + at.index * kTileRows;
     const uint16_t* xr[kSubs];
@@ -612,7 +612,7 @@ __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const int t = blockIdx.x, ranks = 16 * r16;
     const int s = blockIdx.y / 4, rr = threadIdx.x % 16;
     const int row = 16 * (blockIdx.y % 4) + threadIdx.x / 16, r = 16 * s + rr;
-    const Found at = find_entry(offsets, count + 1, rows, kTileRows, false, t);
+    const Found at = find_entry(offsets, count + 1, rows, kTileRows, t);
     const int p0 = at.first + at.index * kTileRows;
     const int n = at.group < 0 ? 0 : min(kTileRows, at.end - p0);
     if (blockIdx.y == 0 && threadIdx.x == 0) info[t] = {at.group, n};
@@ -991,7 +991,7 @@ hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int r
 
 template <int R>
 hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b, int rows, int rank,
-                          int count, void* ws, hipStream_t st) {
+                          void* ws, hipStream_t st) {
     const hipError_t e = launch_kernel(
         a.vec && b.vec ? outer_kernel<R, true> : outer_kernel<R, false>,
         dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b,
@@ -1137,8 +1137,8 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                            strips(f.out), vec_out};
     const OuterSide side_a{x, at<uint16_t>(ws, p.by_rank), da, at<float>(ws, p.sums_a), f.in,
                            strips(f.in), vec_in};
-    if ((e = p.r16 == 1 ? launch_outer_r<1>(p, side_b, side_a, rows, f.rank, f.count, ws, st)
-                        : launch_outer_r<2>(p, side_b, side_a, rows, f.rank, f.count, ws, st)))
+    if ((e = p.r16 == 1 ? launch_outer_r<1>(p, side_b, side_a, rows, f.rank, ws, st)
+                        : launch_outer_r<2>(p, side_b, side_a, rows, f.rank, ws, st)))
         return e;
     if (rows == 0) return hipSuccess;
     return launch_expand(p, f.a, f.in, f.rank, f.count, base, dx, vec_in, ws, st);

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void operands_kernel(const uint16_t* __restric
                                                        const int32_t* __restrict__ offsets,
                                                        int experts, int rows, int in,
                                                        u32x4* __restrict__ out) {
-    const Found at = find_entry(offsets, experts, rows, 16 * MT, false, blockIdx.x);
+    const Found at = find_entry(offsets, experts, rows, 16 * MT, blockIdx.x);
     if (at.group < 0) return;
     const int row0 = at.first + at.index * 16 * MT;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kExThreads) void experts1_kernel(ExArgs p) {
     const Range r = xcd_range(tiles * strips, kExWaves, wave);
     for (int u = r.first; u < r.end; u += r.step) {
         const int t = u / strips, n0 = (u - t * strips) * kWideCols;
-        const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
+        const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, t);
         const int row0 = at.first + at.index * 16 * MT;
         const uint32_t* codes = p.codes + at.group * p.words;
         const float* scales = p.scales + static_cast<size_t>(at.group) * p.out;
@@ -278,7 +278,7 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_at(const ExArgs& p, int u, int strips) {
     const int t = u / strips;
-    const Found at = find_entry(p.offsets, p.experts, p.rows, 16, false, t);
+    const Found at = find_entry(p.offsets, p.experts, p.rows, 16, t);
     return {at.group, at.first + 16 * at.index, at.end, (u - t * strips) * kStripCols};
 }
 
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(kExThreads) void experts0_kernel(ExArgs p) {
     const Range r = xcd_range(tiles * strips, kExWaves, wave);
     for (int u = r.first; u < r.end; u += r.step) {
         const int t = u / strips, col0 = (u - t * strips) * kWideCols;
-        const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, false, t);
+        const Found at = find_entry(p.offsets, p.experts, p.rows, 16 * MT, t);
         const int row0 = at.first + at.index * 16 * MT;
         const Strip0 s = strip0<K, CL>(p, at.group, col0, j, c);
         auto first_row = [&](int step) { return min(32 * step, p.in - 32); };

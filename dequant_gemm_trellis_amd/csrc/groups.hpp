@@ -80,56 +80,43 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
 }
 
-// The place of tile (or segment) t in a list that holds, group by group,
-// ceil(rows of the group / per) entries. Each wave searches for itself, 64
-// groups at a time; with `at_least_one` a group without rows has one entry.
+// The place of tile t in a list that holds, group by group, ceil(rows of the
+// group / per) tiles. Each wave searches for itself, 64 groups at a time.
 struct Found {
-    int group;   // -1: past the end
-    int index;   // entry within its group
-    int first;   // the group's first place, and the place after its last
+    int group;  // -1: past the end
+    int index;  // tile within its group
+    int first;  // the group's first place, and the place after its last
     int end;
-    int tiles;   // tiles of kTileRows rows of the groups before
-    int shared;  // entries of those groups before that have more than one
 };
 
 __device__ __forceinline__ Found find_entry(const int32_t* __restrict__ offsets, int groups, int rows,
-                                            int per, bool at_least_one, int t) {
+                                            int per, int t) {
     const int lane = threadIdx.x & 63;
-    int before = 0, tiles = 0, shared = 0;
+    int before = 0;
     for (int g0 = 0; g0 < groups; g0 += 64) {
         const int g = g0 + lane;
-        int first = 0, end = 0, n = 0, nt = 0;
+        int first = 0, end = 0, n = 0;
         if (g < groups) {
             first = min(max(offsets[g], 0), rows);
             end = min(max(offsets[g + 1], first), rows);
             n = (end - first + per - 1) / per;
-            if (at_least_one && n == 0) n = 1;
-            nt = (end - first + kTileRows - 1) / kTileRows;
         }
-        const int ns = n > 1 ? n : 0;
-        int inc = n, tinc = nt, sinc = ns;
+        int inc = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int a = __shfl_up(inc, d), b = __shfl_up(tinc, d), e = __shfl_up(sinc, d);
-            if (lane >= d) {
-                inc += a;
-                tinc += b;
-                sinc += e;
-            }
+            const int a = __shfl_up(inc, d);
+            if (lane >= d) inc += a;
         }
         const uint64_t past = __ballot(before + inc > t);
         if (past) {
             const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
             // the same in every lane: as scalars, so that addresses stay scalar
             auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-            return {g0 + l, t - before - of(inc - n), of(first), of(end), tiles + of(tinc - nt),
-                    shared + of(sinc - ns)};
+            return {g0 + l, t - before - of(inc - n), of(first), of(end)};
         }
         before += __builtin_amdgcn_readlane(inc, 63);
-        tiles += __builtin_amdgcn_readlane(tinc, 63);
-        shared += __builtin_amdgcn_readlane(sinc, 63);
     }
-    return {-1, 0, 0, 0, 0, 0};
+    return {-1, 0, 0, 0};
 }
 
 // 16 bytes at a 4-byte boundary (what a global access of any width needs).
