@@ -11,8 +11,9 @@
  *     multiple of 8 in arrays aligned to 16 bytes are moved 16 bytes at a time.
  *   - Group indexes, offsets and positions are read on the device and never
  *     trusted as addresses: an index outside its range selects no row.
- *   - Every sum runs in float32 in an order that the sizes and the indexes
- *     fix, so repeated calls give identical bits.
+ *   - Every sum runs in float32 in an order that the sizes, the indexes and the
+ *     current device's number of compute units fix: repeated calls on a device
+ *     give identical bits, devices with other numbers may give others.
  *   - No call reads what an earlier call left in its workspace, and every
  *     call may be captured into a graph and replayed with other indexes of
  *     the same sizes. Calls (and graphs) that share a workspace must not
@@ -112,7 +113,8 @@ int trellis_experts(const uint16_t *x, int32_t rows, const int32_t *offsets, int
                     const trellis_geometry *g, uint16_t *y, void *workspace,
                     size_t workspace_bytes, hipStream_t stream);
 
-/* Workspace bytes of trellis_experts; (size_t)-1 if the sizes are not supported. */
+/* Workspace bytes of trellis_experts on the current device (its number of compute
+ * units decides which tiles a call takes); (size_t)-1 if the sizes are not supported. */
 size_t trellis_experts_workspace_bytes(const trellis_geometry *g, int32_t rows, int32_t experts);
 
 /* Largest rank of an adapter, and number of rows of one adapter call. */
