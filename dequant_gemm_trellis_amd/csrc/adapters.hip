@@ -27,10 +27,11 @@
 // in registers (one byte permute per output word): operand q then holds column
 // 8 j + q, and the eight results give a lane 8 adjacent columns to store.
 //
-// MI355X, 5120 -> 17408: 1 row at rank 16 6.4 us; 4096 rows, 4 adapters, 85 us, 58
-// of them y and base at 4.9 TB/s; their gradient at rank 32, 2 adapters, 138 us:
-// dy read twice at the rate of reads (49 us in the inner product, 48 with x in
-// both outer sums), dx 20, the sort and the tiles' and segments' sums 22.
+// MI355X, 5120 -> 17408: 1 row at rank 16 6.2 us; 4096 rows, 4 adapters, 82 us, 58
+// of them y and base at 4.9 TB/s; their gradient at rank 32, 2 adapters, 142 us:
+// dy read twice (48 us in the inner product, 3.0 TB/s; 51 with x in both outer
+// sums, 3.6 TB/s: the waves, two to a SIMD, wait 42 and 53% of the time for
+// data), dx 21, the sort and the tiles' and segments' sums 22.
 #include "common.hpp"
 #include "groups.hpp"
 #include "launch.hpp"

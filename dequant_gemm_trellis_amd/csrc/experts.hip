@@ -23,8 +23,8 @@
 // 128 x 112 accumulators 289).
 //
 // 64 experts, MI355X: 256 rows of 2048 -> 1536, k = 3: 48 us, 65% of the codebook
-// reads' rate; 16384 rows, k = 2: 174 us (33 of it for the order), 590 TFLOP/s,
-// 45% of a large library product's rate; 1536 -> 2048 on axis 0, k = 4: 231 us,
+// reads' rate; 16384 rows, k = 2: 174 us (34 of it for the order), 580 TFLOP/s,
+// 45% of a large library product's rate; 1536 -> 2048 on axis 0, k = 4: 227 us,
 // 446 TFLOP/s.
 #include "common.hpp"
 #include "groups.hpp"
