@@ -83,20 +83,19 @@ __device__ __forceinline__ u32x4 patch_column(const u32x4 (&row)[8]) {
 }
 
 // The bf16 parts of a float32 value, the high one first: 8 bits of mantissa each,
-// cut off and not rounded, so that none overflows. Infinities and NaN are in the
-// first alone.
+// cut off and not rounded, so that none overflows, an integer's are integers, and
+// all have its sign: their products with an infinity are the infinity that the
+// value's is (a part of 0, of a short mantissa, makes NaN of it). Infinities and
+// NaN are in every part.
 constexpr int kBf16Parts = 3;
 struct Parts3 {
-    uint16_t p[kBf16Parts];
+    float p[kBf16Parts];
 };
 __device__ __forceinline__ Parts3 split3(float w) {
-    if (!__builtin_isfinite(w)) return {{round_bf16(w), 0, 0}};
-    const uint32_t hi = __float_as_uint(w) & 0xFFFF0000u;
-    const float rest = w - __uint_as_float(hi);
-    const uint32_t mid = __float_as_uint(rest) & 0xFFFF0000u;
-    const uint32_t lo = __float_as_uint(rest - __uint_as_float(mid));
-    return {{static_cast<uint16_t>(hi >> 16), static_cast<uint16_t>(mid >> 16),
-             static_cast<uint16_t>(lo >> 16)}};
+    if (!__builtin_isfinite(w)) return {{w, w, w}};
+    auto cut = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); };
+    const float hi = cut(w), rest = w - hi, mid = cut(rest);
+    return {{hi, mid, rest - mid}};
 }
 
 // ---- few rows ----------------------------------------------------------------
@@ -594,7 +593,7 @@ __device__ __forceinline__ void list_segments(const int32_t* __restrict__ offset
 
 // A tile's row numbers and group, its inner products summed from the splits
 // (ascending), and their operand forms; a thread per row and rank.
-//   by_row [tile][64][R][part][16]    (expand; scaled)
+//   by_row [tile][64][R][part][16]    (expand; scaled; half of the last part)
 //   by_rank[tile][R][part][16][64]    (outer; scaled)
 //   u_rank                            the same of the forward pass's u
 // Rows past the tile's last and ranks past the last are zeros there. The first
@@ -639,14 +638,15 @@ __global__ __launch_bounds__(kWgThreads) void tile_kernel(
     const Parts3 w = split3(v * scale);
     uint16_t* q = by_row + ((static_cast<size_t>(t) * kTileRows + row) * r16 + s) * (16 * kBf16Parts) + rr;
 #pragma unroll
-    for (int part = 0; part < kBf16Parts; ++part) q[16 * part] = w.p[part];
+    for (int part = 0; part < kBf16Parts; ++part)
+        q[16 * part] = round_bf16(part == 2 ? 0.5f * w.p[part] : w.p[part]);
     if (!by_rank) return;
     const size_t rank_at = ((static_cast<size_t>(t) * r16 + s) * kBf16Parts * 16 + rr) * kTileRows + row;
     const Parts3 uw = split3(live ? u_in[u_at] * scale : 0.f);
 #pragma unroll
     for (int part = 0; part < kBf16Parts; ++part) {
-        by_rank[rank_at + part * 16 * kTileRows] = w.p[part];
-        u_rank[rank_at + part * 16 * kTileRows] = uw.p[part];
+        by_rank[rank_at + part * 16 * kTileRows] = round_bf16(w.p[part]);
+        u_rank[rank_at + part * 16 * kTileRows] = round_bf16(uw.p[part]);
     }
 }
 
@@ -709,12 +709,16 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
                                base && row[i] >= 0);
         const uint16_t* a_at = rows_op + static_cast<size_t>(16 * s + j) * r16 * (16 * kBf16Parts) + 8 * c;
         floatx4 acc[8] = {};
-        // the third part's ranks are lanes 0 and 1's; zeros in the others
+        // the third part fills its 32 slots as two halves, which the lower 32 lanes
+        // load and pass to the upper ones
         auto multiply = [&](int r, const u32x4 (&f)[8]) {
             const uint16_t* at = a_at + 16 * kBf16Parts * r;
             const u32x4 two = *reinterpret_cast<const u32x4*>(at);
             u32x4 third = {0u, 0u, 0u, 0u};
             if (c < 2) third = *reinterpret_cast<const u32x4*>(at + 32);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                third[d] = __builtin_amdgcn_permlane32_swap(third[d], third[d], false, false)[0];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 acc[q] = mfma16x16x32(as_bf16x8(two), as_bf16x8(f[q]), acc[q]);

@@ -148,9 +148,9 @@ typedef struct trellis_adapter_set {
  * not touched); u: float32 [rows][rank], kept for the backward pass, or null.
  * u, the products and the sums are float32; beyond few rows u enters the second
  * product as three bf16 parts whose sum it is. Where a value of b that a row
- * meets is infinite, y is not finite there, but it may be NaN where the formula
- * has an infinity (a part of 0 times infinity). workspace: 16-byte aligned, at
- * least trellis_adapters_workspace_bytes(f, rows, 0) bytes.
+ * meets is infinite, y is the formula's infinity or, where a part of u is 0 (its
+ * mantissa is short), NaN. workspace: 16-byte aligned, at least
+ * trellis_adapters_workspace_bytes(f, rows, 0) bytes.
  */
 int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
                      const trellis_adapter_set *f, const uint16_t *base, uint16_t *y, float *u,
@@ -168,7 +168,8 @@ int trellis_adapters(const uint16_t *x, const int32_t *ids, int32_t rows,
  * `base` itself. da and db have the factors' layout and are written whole:
  * zeros for adapters without rows (also for rows = 0). Products and sums are
  * float32; beyond few rows g and u enter the second products as three bf16 parts,
- * and an infinity in a, x or dy may give NaN where the formula has an infinity.
+ * and an infinity in a, x or dy gives the formula's infinity or, where it meets a
+ * part of 0, NaN.
  * workspace: 16-byte aligned, at least
  * trellis_adapters_workspace_bytes(f, rows, 1) bytes.
  */

@@ -191,3 +191,68 @@ def test_inner_values_keep_their_mantissa(gpu_lib, i, o, rank):
         assert float(v.max()) >= 2 ** 17 and float(v.sum(0).max()) < most and float(v.sum(1).max()) < most
     want_dx, want_da, _ = p.backward(u.double().cpu())
     assert same(dx, want_dx) and same(da, want_da)
+
+
+@pytest.mark.parametrize("rows", [40, 700])
+@pytest.mark.parametrize("rank", [16, 24, 64])
+def test_infinities_keep_their_sign(gpu_lib, rows, rank):
+    """An infinite value of a factor or of a wide row: the outputs that it enters are
+    the formula's infinities, and no other changes. Over many rows an output is NaN
+    where the second or the third of the parts that its inner value is cut into (the
+    upper 8 bits of what is left, each) is 0: known here of u, not of g."""
+    say(f"adapters with infinities, {rows} rows, rank {rank}")
+    p = Problem(47, rows, 264, 328, rank, 3, "runs", integers=False)
+    many = rows == 700
+    assert sorted_tiles(gpu_lib, p, False) == sorted_tiles(gpu_lib, p, True) == many
+    d = p.cuda()
+    u = gpu_lib.adapters(d["x"], d["ids"], d["a"], d["b"], d["scales"], keep_inner=True)[1].cpu()
+    m = int((p.ids == 1).nonzero()[0])  # a row of adapter 1
+
+    def cut(v):
+        return (v.contiguous().view(torch.int32) & -65536).view(torch.float32)
+
+    def run(which):
+        d = p.cuda()
+        if which == "y":
+            return gpu_lib.adapters(d["x"], d["ids"], d["a"], d["b"], d["scales"], base=d["base_y"])[0].cpu()
+        grads = gpu_lib.adapters_backward(d["dy"], d["x"], u.cuda(), d["ids"], d["a"], d["b"],
+                                          d["scales"], base=d["base_x"])
+        return grads[("dx", "da", "db").index(which)].cpu()
+
+    def check(before, got, hit, inner, sign):
+        """got[hit] are infinities of `sign` times the signs of `inner` (float32: NaN
+        where a part of it is 0; float64: some are infinities), the rest as before."""
+        assert torch.equal(got[~hit], before[~hit])
+        value, want = got[hit].float(), sign * inner.sign().float()
+        assert not value.isfinite().any()
+        fine = ~value.isnan()
+        assert torch.equal(value[fine].sign(), want[fine]) and bool(fine.any())
+        if not many:
+            assert bool(fine.all())
+        elif inner.dtype is torch.float32:
+            rest = inner - cut(inner)
+            assert torch.equal(fine, (rest != 0) & (rest - cut(rest) != 0))
+
+    def set_one(name, at, which, hit, inner):
+        t = getattr(p, name)
+        before, kept = run(which), t[at].clone()
+        for sign in (1, -1):
+            t[at] = sign * float("inf")
+            check(before, run(which), hit, inner, sign)
+        t[at] = kept
+
+    r = rank // 2
+    one = p.ids == 1
+    hit = torch.zeros((rows, 328), dtype=torch.bool)
+    hit[one, 7] = True
+    set_one("b", (1, r, 7), "y", hit, u[one, r])
+    g = p.dy.double() @ p.b[1].double().T
+    hit = torch.zeros((rows, 264), dtype=torch.bool)
+    hit[one, 9] = True
+    set_one("a", (1, r, 9), "dx", hit, g[one, r])
+    hit = torch.zeros((3, rank, 264), dtype=torch.bool)
+    hit[1, :, 11] = True
+    set_one("x", (m, 11), "da", hit, g[m])
+    hit = torch.zeros((3, rank, 328), dtype=torch.bool)
+    hit[1, :, 3] = True
+    set_one("dy", (m, 3), "db", hit, u[m])
