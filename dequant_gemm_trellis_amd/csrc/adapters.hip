@@ -17,10 +17,9 @@
 // There a rank-long float32 value w (u or g) enters as three bf16 parts whose sum
 // is w: its mantissa's upper, middle and lower 8 bits, so that every product is
 // exact and the sums are float32 as those of few rows. (Two parts, 16 bits of
-// mantissa, take up to 7% less time, but then 1.7e-3 to 2.5e-3 of
-// the bf16 results of 4096 rows are not the float64 value rounded; with three
-// 1.0e-4 to 3.0e-4.) Two parts of 16 ranks fill the 32 contraction slots of one
-// 16x16x32 instruction.
+// mantissa, take up to 7% less time, but then 1.7e-3 to 2.5e-3 of the bf16 results
+// of 4096 rows are not the float64 value rounded; with three 1.0e-4 to 3.0e-4.)
+// Two parts of 16 ranks fill the 32 contraction slots of one 16x16x32 instruction.
 //
 // A matrix instruction contracts over 8 consecutive values per lane. Where the
 // contraction runs across stored rows (ranks in expand, tokens in outer), a
