@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtrellis.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["gemv.hip", "axis1.hip", "axis0.hip", "layout.hip", "probe.hip", "route.hip", "adapters.hip", "experts.hip",
-           "api.cpp", "api_grouped.cpp"]
+           "kept.hip", "layer.hip", "api.cpp", "api_grouped.cpp", "api_mlp.cpp"]
 ARCH = "gfx950"
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,

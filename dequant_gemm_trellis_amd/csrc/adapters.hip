@@ -34,6 +34,7 @@
 // data), dx 21, the sort and the tiles' and segments' sums 22.
 #include "common.hpp"
 #include "groups.hpp"
+#include "kept.hpp"
 #include "launch.hpp"
 
 namespace trellis {
@@ -95,6 +96,40 @@ __device__ __forceinline__ Parts3 split3(float w) {
     auto cut = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); };
     const float hi = cut(w), rest = w - hi, mid = cut(rest);
     return {{hi, mid, rest - mid}};
+}
+
+// 8 values of a wide row as loaded, and as bf16: a row of bf16, or (KEPT) one held
+// in 8 bits, whose codes and exponent stay as they are until the values are used.
+struct KeptPiece {
+    u32x2 codes;
+    uint32_t exponent;
+};
+__device__ __forceinline__ u32x4 piece_values(const u32x4& v) { return v; }
+__device__ __forceinline__ u32x4 piece_values(const KeptPiece& v) { return kept_values(v.codes, v.exponent); }
+
+// Where the wide rows of one of the outer products are: `x`, or `kept` if x is null.
+struct WideRows {
+    const uint16_t* x;
+    KeptRows kept;
+};
+
+template <bool KEPT>
+using Piece = std::conditional_t<KEPT, KeptPiece, u32x4>;
+
+template <bool VEC, bool KEPT>
+__device__ __forceinline__ Piece<KEPT> load_piece(const WideRows& p, int row, int col, int width, bool live) {
+    if constexpr (!KEPT) {
+        return load8<VEC>(p.x + static_cast<size_t>(row) * width, col, width, live);
+    } else {
+        KeptPiece v = {{0u, 0u}, 0u};
+        if (live && col < width) {
+            const size_t groups = (width + kKeptGroup - 1) / kKeptGroup;
+            const int8_t* at = p.kept.codes + static_cast<size_t>(row) * width + col;
+            v.codes = VEC ? *reinterpret_cast<const u32x2*>(at) : load_codes(at, width - col);
+            v.exponent = p.kept.exponents[row * groups + col / kKeptGroup];
+        }
+        return v;
+    }
 }
 
 // ---- few rows ----------------------------------------------------------------
@@ -302,7 +337,7 @@ __global__ __launch_bounds__(kOneThreads) void direct_kernel(
 }
 
 // The gradients of an adapter's factors over few rows: a workgroup takes 512
-// columns and 4 ranks of one adapter, finds its rows (ascending), and its waves
+// columns and 4 ranks of one adapter (KEPT: side b's rows are held in 8 bits), finds its rows (ascending), and its waves
 // take them in turn: 4 ranks x 8 columns of float32 sums per lane. Of W waves,
 // wave q adds wave q + W / 2's sums to its own, then the halves meet in order.
 // `inner` are the float32 rank-long values without the scale. Grid: (column
@@ -314,21 +349,21 @@ constexpr int kFewRows = 256;  // rows of a call, at most: a thread finds one
 constexpr int kFewRanks = 4;
 
 struct FewSide {
-    const uint16_t* x;   // the wide rows
+    WideRows x;
     const float* inner;  // [rows][rank]
     uint16_t* grad;
     int width, chunks;
     bool vec;
 };
 
-template <int WAVES, bool VEC>
+template <int WAVES, bool VEC, bool KEPT>
 __device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int wave,
                                          const int* __restrict__ list,
                                          const float (*__restrict__ coef)[kFewRanks],
                                          float (&acc)[kFewRanks][8]) {
 #pragma unroll 4
     for (int i = wave; i < n; i += WAVES) {
-        const u32x4 v = load8<VEC>(p.x + static_cast<size_t>(list[i]) * p.width, col, p.width, true);
+        const u32x4 v = piece_values(load_piece<VEC, KEPT>(p.x, list[i], col, p.width, true));
         float e[8];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -342,7 +377,7 @@ __device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int w
     }
 }
 
-template <int THREADS, bool VEC>
+template <int THREADS, bool VEC, bool KEPT>
 __global__ __launch_bounds__(THREADS) void direct_outer_kernel(
     FewSide a, FewSide b, const int32_t* __restrict__ ids, const float* __restrict__ scales, int rows,
     int rank) {
@@ -379,10 +414,12 @@ __global__ __launch_bounds__(THREADS) void direct_outer_kernel(
     }
     __syncthreads();
     float acc[kFewRanks][8] = {};
-    if (VEC || p.vec)
-        add_rows<waves, true>(p, col, n, wave, list, sh.coef, acc);
+    if (KEPT && second)
+        add_rows<waves, VEC, KEPT>(p, col, n, wave, list, sh.coef, acc);
+    else if (VEC || p.vec)
+        add_rows<waves, true, false>(p, col, n, wave, list, sh.coef, acc);
     else
-        add_rows<waves, false>(p, col, n, wave, list, sh.coef, acc);
+        add_rows<waves, false, false>(p, col, n, wave, list, sh.coef, acc);
     __syncthreads();  // the parts take the coefficients' place
     auto each = [&](auto&& f) {
 #pragma unroll
@@ -748,7 +785,7 @@ __global__ __launch_bounds__(kWgThreads) void expand_kernel(
 // One of the two sums over an adapter's rows of a rank-long column times a wide
 // row: dA (g and x) or dB (scaled u and dy).
 struct OuterSide {
-    const uint16_t* x;        // the wide rows
+    WideRows x;
     const uint16_t* by_rank;  // the rank-long values
     uint16_t* grad;           // [count][rank][width]
     float* sums;              // [shared segment][rank][width]
@@ -760,7 +797,7 @@ struct OuterSide {
 // sums of the waves that had any are added in wave order. An adapter of one segment (or without rows) is
 // written to `grad` in bf16; the float32 sums of the others' segments go to
 // `sums`.
-template <int R, bool VEC>
+template <int R, bool VEC, bool KEPT>
 __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo& seg, int strip, int r0,
                                               int r16, int rank, const int* seg_rows, float* sum) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -770,15 +807,15 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     // This wave's 32-row halves of the segment's tiles wave, wave + 4, ...; the
     // next half's rows are loaded while one is multiplied.
     struct Half {
-        u32x4 patch[8], a[R][kBf16Parts];
+        Piece<KEPT> patch[8];
+        u32x4 a[R][kBf16Parts];
     };
     auto load = [&](Half& q, int step) {
         const int t = wave + kWgWaves * (step >> 1), h = step & 1;
         const int* trow = seg_rows + t * kTileRows + 32 * h + 8 * c;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            q.patch[i] = load8<VEC>(p.x + static_cast<size_t>(max(trow[i], 0)) * width, col, width,
-                                    trow[i] >= 0);
+            q.patch[i] = load_piece<VEC, KEPT>(p.x, max(trow[i], 0), col, width, trow[i] >= 0);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -790,9 +827,12 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     };
     floatx4 acc[R][8] = {};
     auto multiply = [&](const Half& q) {
+        u32x4 patch[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) patch[i] = piece_values(q.patch[i]);
         static_for<0, 8>([&](auto qc) {
             constexpr int e = decltype(qc)::value;
-            const u32x4 b = patch_column<e>(q.patch);
+            const u32x4 b = patch_column<e>(patch);
 #pragma unroll
             for (int part = 0; part < kBf16Parts; ++part)
 #pragma unroll
@@ -850,10 +890,10 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     }
 }
 
-// Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces. Without
-// a list (no rows) every adapter is one segment of none.
+// Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces. KEPT: side
+// b's rows are held in 8 bits (8-byte pieces there). Without a list (no rows) every adapter is one segment of none.
 // Grid: (strips of side a then of side b, segments, rank pairs).
-template <int R, bool VEC>
+template <int R, bool VEC, bool KEPT>
 __global__ __launch_bounds__(kWgThreads) void outer_kernel(
     OuterSide a, OuterSide b, const SegInfo* __restrict__ segs, const int32_t* __restrict__ tile_rows,
     int rank, int r16) {
@@ -869,10 +909,12 @@ __global__ __launch_bounds__(kWgThreads) void outer_kernel(
     const bool second = static_cast<int>(blockIdx.x) >= a.strips;
     const OuterSide& p = second ? b : a;
     const int strip = second ? blockIdx.x - a.strips : blockIdx.x, r0 = blockIdx.z * R;
-    if (VEC || p.vec)
-        outer_segment<R, true>(p, seg, strip, r0, r16, rank, seg_rows, sum);
+    if (KEPT && second)
+        outer_segment<R, VEC, KEPT>(p, seg, strip, r0, r16, rank, seg_rows, sum);
+    else if (VEC || p.vec)
+        outer_segment<R, true, false>(p, seg, strip, r0, r16, rank, seg_rows, sum);
     else
-        outer_segment<R, false>(p, seg, strip, r0, r16, rank, seg_rows, sum);
+        outer_segment<R, false, false>(p, seg, strip, r0, r16, rank, seg_rows, sum);
 }
 
 // The segments' sums of the adapters of several, ascending, rounded to bf16, of
@@ -997,8 +1039,10 @@ hipError_t launch_expand(const Plan& p, const uint16_t* factor, int width, int r
 template <int R>
 hipError_t launch_outer_r(const Plan& p, const OuterSide& a, const OuterSide& b, int rows, int rank,
                           void* ws, hipStream_t st) {
+    const bool vec = a.vec && b.vec;
     const hipError_t e = launch_kernel(
-        a.vec && b.vec ? outer_kernel<R, true> : outer_kernel<R, false>,
+        b.x.x ? (vec ? outer_kernel<R, true, false> : outer_kernel<R, false, false>)
+              : (vec ? outer_kernel<R, true, true> : outer_kernel<R, false, true>),
         dim3(a.strips + b.strips, p.segments, (p.r16 + R - 1) / R), dim3(kWgThreads), st, a, b,
         rows ? at<SegInfo>(ws, p.segs) : nullptr, at<int32_t>(ws, p.tile_rows), rank, p.r16);
     if (e != hipSuccess || !p.several) return e;
@@ -1094,8 +1138,17 @@ hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterF
     return launch_expand(p, f.b, f.out, f.rank, f.count, base, y, vec_out, ws, st);
 }
 
-hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* u,
-                                    const int32_t* ids, const AdapterFactors& f, int rows,
+template <int THREADS>
+hipError_t launch_direct_outer(const FewSide& a, const FewSide& b, const dim3& grid, const int32_t* ids,
+                               const float* scales, int rows, int rank, hipStream_t st) {
+    const bool vec = a.vec && b.vec;
+    auto kernel = b.x.x ? (vec ? direct_outer_kernel<THREADS, true, false> : direct_outer_kernel<THREADS, false, false>)
+                        : (vec ? direct_outer_kernel<THREADS, true, true> : direct_outer_kernel<THREADS, false, true>);
+    return launch_kernel(kernel, grid, dim3(THREADS), st, a, b, ids, scales, rows, rank);
+}
+
+hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const KeptRows& kept,
+                                    const float* u, const int32_t* ids, const AdapterFactors& f, int rows,
                                     const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                                     bool vec_in, bool vec_out, void* ws, hipStream_t st) {
     hipError_t e;
@@ -1111,15 +1164,12 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                           dim3(direct_splits(f.in), rows), dim3(kWgThreads), st, partial, splits, ids,
                           f.a, f.scales, f.in, f.rank, f.count, base, dx, inner);
         if (e != hipSuccess) return e;
-        const FewSide side_b{dy, u, db, f.out, direct_splits(f.out), vec_out};
-        const FewSide side_a{x, inner, da, f.in, direct_splits(f.in), vec_in};
+        const FewSide side_b{{dy, {}}, u, db, f.out, direct_splits(f.out), vec_out};
+        const FewSide side_a{{x, kept}, inner, da, f.in, direct_splits(f.in), vec_in};
         const dim3 grid(side_b.chunks + side_a.chunks, f.count, (f.rank + kFewRanks - 1) / kFewRanks);
-        const bool vec = vec_in && vec_out;
-        if (many_groups(grid))
-            return launch_kernel(vec ? direct_outer_kernel<256, true> : direct_outer_kernel<256, false>,
-                                 grid, dim3(256), st, side_b, side_a, ids, f.scales, rows, f.rank);
-        return launch_kernel(vec ? direct_outer_kernel<512, true> : direct_outer_kernel<512, false>,
-                             grid, dim3(512), st, side_b, side_a, ids, f.scales, rows, f.rank);
+        return many_groups(grid)
+                   ? launch_direct_outer<256>(side_b, side_a, grid, ids, f.scales, rows, f.rank, st)
+                   : launch_direct_outer<512>(side_b, side_a, grid, ids, f.scales, rows, f.rank, st);
     }
     const Plan p = make_plan(rows, f.in, f.out, f.rank, f.count, true);
     if ((e = launch_route(ids, rows, f.count, true, at<int32_t>(ws, p.offsets),
@@ -1138,9 +1188,9 @@ hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const
                            p.several)))
         return e;
     auto strips = [](int width) { return (width + kStrip - 1) / kStrip; };
-    const OuterSide side_b{dy, at<uint16_t>(ws, p.u_rank), db, at<float>(ws, p.sums_b), f.out,
+    const OuterSide side_b{{dy, {}}, at<uint16_t>(ws, p.u_rank), db, at<float>(ws, p.sums_b), f.out,
                            strips(f.out), vec_out};
-    const OuterSide side_a{x, at<uint16_t>(ws, p.by_rank), da, at<float>(ws, p.sums_a), f.in,
+    const OuterSide side_a{{x, kept}, at<uint16_t>(ws, p.by_rank), da, at<float>(ws, p.sums_a), f.in,
                            strips(f.in), vec_in};
     if ((e = p.r16 == 1 ? launch_outer_r<1>(p, side_b, side_a, rows, f.rank, ws, st)
                         : launch_outer_r<2>(p, side_b, side_a, rows, f.rank, ws, st)))

@@ -4,8 +4,10 @@
 
 #include "checks.hpp"
 #include "groups.hpp"
+#include "kept.hpp"
 #include "launch.hpp"
 #include "trellis_grouped.h"
+#include "trellis_mlp.h"
 
 using trellis::aligned;
 using trellis::status_of;
@@ -61,6 +63,30 @@ bool all16(const void* p, const void* q, const void* r) {
 int check_workspace(const void* workspace, size_t bytes, size_t need) {
     if (!aligned(workspace, 16)) return TRELLIS_ERR_ALIGN;
     return need && (!workspace || bytes < need) ? TRELLIS_ERR_WORKSPACE : TRELLIS_OK;
+}
+
+// Both forms of the gradient: x as bf16 rows, or `kept` (then x is null);
+// rows_of_x is whichever holds the rows.
+int adapters_backward(const uint16_t* dy, const uint16_t* x, const void* rows_of_x,
+                      const trellis::KeptRows& kept, const float* u, const int32_t* ids, int32_t rows,
+                      const trellis_adapter_set* f, const uint16_t* base, uint16_t* dx, uint16_t* da,
+                      uint16_t* db, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_adapters(f, rows);
+    if (st) return st;
+    if (!da || !db || (rows && (!dy || !rows_of_x || !u || !ids || !dx))) return TRELLIS_ERR_NULL;
+    if ((st = check_factors(f))) return st;
+    if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(u, 4) || !aligned(ids, 4) ||
+        !aligned(base, 2) || !aligned(dx, 2) || !aligned(da, 2) || !aligned(db, 2))
+        return TRELLIS_ERR_ALIGN;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              trellis::adapters_workspace_bytes(rows, f->in_features, f->out_features, f->rank,
+                                                                f->count, true))))
+        return st;
+    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && all16(dx, da, nullptr) &&
+                        aligned(kept.codes, 8);
+    const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, db);
+    return status_of(trellis::launch_adapters_backward(dy, x, kept, u, ids, factors(f), rows, base,
+                                                       dx, da, db, vec_in, vec_out, workspace, stream));
 }
 
 }  // namespace
@@ -158,20 +184,17 @@ int trellis_adapters_backward(const uint16_t* dy, const uint16_t* x, const float
                               const int32_t* ids, int32_t rows, const trellis_adapter_set* f,
                               const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
-    int st = check_adapters(f, rows);
-    if (st) return st;
-    if (!da || !db || (rows && (!dy || !x || !u || !ids || !dx))) return TRELLIS_ERR_NULL;
-    if ((st = check_factors(f))) return st;
-    if (!aligned(dy, 2) || !aligned(x, 2) || !aligned(u, 4) || !aligned(ids, 4) ||
-        !aligned(base, 2) || !aligned(dx, 2) || !aligned(da, 2) || !aligned(db, 2))
-        return TRELLIS_ERR_ALIGN;
-    if ((st = check_workspace(workspace, workspace_bytes,
-                              trellis_adapters_workspace_bytes(f, rows, 1))))
-        return st;
-    const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && all16(dx, da, nullptr);
-    const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, db);
-    return status_of(trellis::launch_adapters_backward(dy, x, u, ids, factors(f), rows, base, dx, da,
-                                                       db, vec_in, vec_out, workspace, stream));
+    return adapters_backward(dy, x, x, {}, u, ids, rows, f, base, dx, da, db, workspace, workspace_bytes,
+                             stream);
+}
+
+int trellis_adapters_backward_kept(const uint16_t* dy, const trellis_kept* x, const float* u,
+                                   const int32_t* ids, int32_t rows, const trellis_adapter_set* f,
+                                   const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const trellis::KeptRows kept = x ? trellis::KeptRows{x->codes, x->exponents} : trellis::KeptRows{};
+    return adapters_backward(dy, nullptr, kept.exponents ? kept.codes : nullptr, kept, u, ids, rows, f,
+                             base, dx, da, db, workspace, workspace_bytes, stream);
 }
 
 size_t trellis_experts_workspace_bytes(const trellis_geometry* g, int32_t rows, int32_t experts) {

@@ -9,6 +9,8 @@
 
 namespace trellis {
 
+struct KeptRows;  // kept.hpp
+
 constexpr int kMaxGroups = 1024;
 constexpr int kMaxSlots = 1 << 21;
 constexpr int kMaxKeys = kMaxGroups + 1;  // one more for the slots outside every group
@@ -49,8 +51,9 @@ size_t adapters_workspace_bytes(int rows, int in, int out, int rank, int count, 
 hipError_t launch_adapters(const uint16_t* x, const int32_t* ids, const AdapterFactors& f, int rows,
                            const uint16_t* base, uint16_t* y, float* u, bool vec_in, bool vec_out,
                            void* ws, hipStream_t st);
-hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const float* u,
-                                    const int32_t* ids, const AdapterFactors& f, int rows,
+// x: bf16, or, where it is null, `kept`.
+hipError_t launch_adapters_backward(const uint16_t* dy, const uint16_t* x, const KeptRows& kept,
+                                    const float* u, const int32_t* ids, const AdapterFactors& f, int rows,
                                     const uint16_t* base, uint16_t* dx, uint16_t* da, uint16_t* db,
                                     bool vec_in, bool vec_out, void* ws, hipStream_t st);
 

@@ -1,4 +1,4 @@
-"""ctypes binding over libtrellis.so (include/trellis.h, trellis_grouped.h).
+"""ctypes binding over libtrellis.so (include/trellis.h, trellis_grouped.h, trellis_mlp.h).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI. PyTorch supplies device memory and the stream.
@@ -46,7 +46,9 @@ EXPORTED = ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_
             "trellis_route_workspace_bytes", "trellis_dispatch", "trellis_combine",
             "trellis_combine_backward", "trellis_adapters", "trellis_adapters_backward",
             "trellis_adapters_workspace_bytes", "trellis_experts",
-            "trellis_experts_workspace_bytes")
+            "trellis_experts_workspace_bytes", "trellis_experts_mlp",
+            "trellis_experts_mlp_workspace_bytes", "trellis_keep", "trellis_restore",
+            "trellis_swiglu", "trellis_swiglu_backward", "trellis_adapters_backward_kept")
 PROBE_PAIR_B64, PROBE_COPIES8_B32, PROBE_SINGLE_B32 = 0, 1, 2
 
 
@@ -93,7 +95,17 @@ class AdapterSet(C.Structure):
                 ("out_features", C.c_int32)]
 
 
+class ExpertSet(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("lut", C.c_void_p), ("g", Geometry)]
+
+
+class _KeptRows(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("exponents", C.c_void_p)]
+
+
 _AP = C.POINTER(AdapterSet)
+_EP = C.POINTER(ExpertSet)
+_KP = C.POINTER(_KeptRows)
 _i32 = C.c_int32
 _lib.trellis_adapters.argtypes = [_vp, _vp, _i32, _AP, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
 _lib.trellis_adapters_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _AP, _vp, _vp, _vp, _vp, _vp,
@@ -109,11 +121,22 @@ _lib.trellis_route_workspace_bytes.restype = C.c_size_t
 _lib.trellis_dispatch.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp, _vp]
 _lib.trellis_combine.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]
 _lib.trellis_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]
+_lib.trellis_experts_mlp.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _EP, _EP, _vp, _vp, C.c_size_t, _vp]
+_lib.trellis_experts_mlp_workspace_bytes.argtypes = [_i32, _i32, _i32, _EP, _EP]
+_lib.trellis_experts_mlp_workspace_bytes.restype = C.c_size_t
+_lib.trellis_keep.argtypes = [_vp, _i32, _i32, _KP, _vp]
+_lib.trellis_restore.argtypes = [_KP, _i32, _i32, _vp, _vp]
+_lib.trellis_swiglu.argtypes = [_vp, _i32, _i32, _vp, _KP, _vp]
+_lib.trellis_swiglu_backward.argtypes = [_vp, _vp, _KP, _i32, _i32, _vp, _vp, _vp]
+_lib.trellis_adapters_backward_kept.argtypes = [_vp, _KP, _vp, _vp, _i32, _AP, _vp, _vp, _vp, _vp, _vp,
+                                                C.c_size_t, _vp]
 for _f in ("trellis_lut_upload", "trellis_gemv", "trellis_gemv_dual", "trellis_gemv_scatter",
            "trellis_prefill", "trellis_prefill_dual", "trellis_gate_up_swiglu", "trellis_expand",
            "trellis_repack", "trellis_gemv_scatter_static", "trellis_route", "trellis_dispatch",
            "trellis_combine", "trellis_combine_backward", "trellis_adapters",
-           "trellis_adapters_backward", "trellis_experts"):
+           "trellis_adapters_backward", "trellis_experts", "trellis_experts_mlp", "trellis_keep",
+           "trellis_restore", "trellis_swiglu", "trellis_swiglu_backward",
+           "trellis_adapters_backward_kept"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -588,12 +611,17 @@ def adapters_backward(dy, x, u, ids, a, b, scales, base=None, dx=None, da=None, 
                       workspace=None, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients (dx, da, db) of adapters from dy [rows, out] with the forward
     pass's u: dx = base + a[i]^T g with g = scales[i] * b[i] dy, da and db whole
-    (zeros for adapters without rows), all bf16. dx may be `base`."""
-    dev = _device(x)
+    (zeros for adapters without rows), all bf16. dx may be `base`. x: the forward
+    pass's, as bf16 rows or as `keep` put them away."""
+    dev = _device(dy)
     f = _adapter_set(a, b, scales, dev)
-    rows = _dims("x", x, 2)[0]
+    rows = _dims("dy", dy, 2)[0]
     _want("dy", dy, torch.bfloat16, (rows, f.out_features), dev)
-    _want("x", x, torch.bfloat16, (rows, f.in_features), dev)
+    kept = isinstance(x, Kept)
+    if kept:
+        _want_kept("x", x, rows, f.in_features, dev)
+    else:
+        _want("x", x, torch.bfloat16, (rows, f.in_features), dev)
     _want("u", u, torch.float32, (rows, f.rank), dev)
     _want("ids", ids, torch.int32, (rows,), dev)
     if base is not None:
@@ -602,7 +630,7 @@ def adapters_backward(dy, x, u, ids, a, b, scales, base=None, dx=None, da=None, 
     with _on(stream, dev):
         given = {"dx": dx, "da": da, "db": db, "workspace": workspace}
         if dx is None:
-            dx = torch.empty_like(x)
+            dx = dy.new_empty((rows, f.in_features))
         if da is None:
             da = torch.empty_like(a)
         if db is None:
@@ -610,11 +638,186 @@ def adapters_backward(dy, x, u, ids, a, b, scales, base=None, dx=None, da=None, 
         _want("dx", dx, torch.bfloat16, (rows, f.in_features), dev)
         _want("da", da, torch.bfloat16, a.shape, dev)
         _want("db", db, torch.bfloat16, b.shape, dev)
-        ws, ws_bytes, keep = _workspace("trellis_adapters_backward", nbytes, workspace, x)
+        ws, ws_bytes, hold = _workspace("trellis_adapters_backward", nbytes, workspace, dy)
         same = base is not None and base.data_ptr() == dx.data_ptr()
-        _apart(given, {"dy": dy, "x": x, "u": u, "ids": ids, "a": a, "b": b, "scales": scales,
+        rows_of_x = _kept_parts("x", x) if kept else {"x": x}
+        _apart(given, {"dy": dy, **rows_of_x, "u": u, "ids": ids, "a": a, "b": b, "scales": scales,
                        "base": None if same else base})
-        _check("trellis_adapters_backward", _lib.trellis_adapters_backward(
-            dy.data_ptr(), x.data_ptr(), u.data_ptr(), ids.data_ptr(), rows, C.byref(f), _ptr(base),
-            dx.data_ptr(), da.data_ptr(), db.data_ptr(), ws, ws_bytes, _handle(dev)))
+        fn, where = "trellis_adapters_backward", None
+        if kept:
+            fn, where = "trellis_adapters_backward_kept", C.byref(_kept_rows(x))
+        _check(fn, getattr(_lib, fn)(
+            dy.data_ptr(), where if kept else x.data_ptr(), u.data_ptr(), ids.data_ptr(), rows,
+            C.byref(f), _ptr(base), dx.data_ptr(), da.data_ptr(), db.data_ptr(), ws, ws_bytes,
+            _handle(dev)))
     return dx, da, db
+
+
+# ---- around an MLP or a layer of experts (trellis_mlp.h) ----------------------
+
+
+class Kept(NamedTuple):
+    """bf16 rows held in 8 bits (trellis_keep)."""
+
+    codes: torch.Tensor      # int8 [rows, width]
+    exponents: torch.Tensor  # uint8 [rows, ceil(width / 32)], one per 32 values
+
+
+def _kept_rows(k: Kept) -> _KeptRows:
+    return _KeptRows(k.codes.data_ptr(), k.exponents.data_ptr())
+
+
+def _kept_parts(name: str, k: Kept) -> dict:
+    return {f"{name}.codes": k.codes, f"{name}.exponents": k.exponents}
+
+
+def _want_kept(name: str, k: Kept, rows: int, width: int, device: int) -> None:
+    _want(f"{name}.codes", k.codes, torch.int8, (rows, width), device)
+    _want(f"{name}.exponents", k.exponents, torch.uint8, (rows, -(-width // 32)), device)
+
+
+def _new_kept(like: torch.Tensor, rows: int, width: int) -> Kept:
+    return Kept(like.new_empty((rows, width), dtype=torch.int8),
+                like.new_empty((rows, -(-width // 32)), dtype=torch.uint8))
+
+
+def keep(x, kept: Kept | None = None, stream=None) -> Kept:
+    """bf16 rows x [rows, width] put away in 8 bits: 32 adjacent values of a row share
+    an exponent, and each is off by at most 1/256 of the group's largest magnitude."""
+    rows, width = _dims("x", x, 2)
+    dev = _device(x)
+    _want("x", x, torch.bfloat16, (rows, width), dev)
+    with _on(stream, dev):
+        if kept is None:
+            kept = _new_kept(x, rows, width)
+        else:
+            _want_kept("kept", kept, rows, width, dev)
+            _apart(_kept_parts("kept", kept), {"x": x})
+        _check("trellis_keep", _lib.trellis_keep(x.data_ptr(), rows, width, C.byref(_kept_rows(kept)),
+                                                 _handle(dev)))
+    return kept
+
+
+def restore(kept: Kept, out=None, stream=None) -> torch.Tensor:
+    """The bf16 rows that `kept` stands for."""
+    rows, width = _dims("kept.codes", kept.codes, 2)
+    dev = _device(kept.codes)
+    _want_kept("kept", kept, rows, width, dev)
+    with _on(stream, dev):
+        if out is None:
+            out = kept.codes.new_empty((rows, width), dtype=torch.bfloat16)
+        else:
+            _want("out", out, torch.bfloat16, (rows, width), dev)
+            _apart({"out": out}, _kept_parts("kept", kept))
+        _check("trellis_restore", _lib.trellis_restore(C.byref(_kept_rows(kept)), rows, width,
+                                                       out.data_ptr(), _handle(dev)))
+    return out
+
+
+def swiglu(gu, h=None, keep=False, kept: Kept | None = None,
+           stream=None) -> tuple[torch.Tensor, Kept | None]:
+    """(h, kept): h = silu(g) * u for gu [rows, 2 * inter], a row being [g, u]. kept: gu
+    in 8 bits for swiglu_backward (rows g and u apart: [2 * rows, inter]), None unless
+    given or `keep`."""
+    rows, width = _dims("gu", gu, 2)
+    if width % 2:
+        raise ValueError(f"gu: expected rows [g, u] of even length, got shape {tuple(gu.shape)}")
+    inter = width // 2
+    dev = _device(gu)
+    _want("gu", gu, torch.bfloat16, (rows, width), dev)
+    with _on(stream, dev):
+        if h is not None:
+            _want("h", h, torch.bfloat16, (rows, inter), dev)
+        if kept is not None:
+            _want_kept("kept", kept, 2 * rows, inter, dev)
+        if h is not None or kept is not None:
+            parts = _kept_parts("kept", kept) if kept is not None else {}
+            _apart({"h": h, **parts}, {"gu": gu})
+        if h is None:
+            h = gu.new_empty((rows, inter))
+        if kept is None and keep:
+            kept = _new_kept(gu, 2 * rows, inter)
+        _check("trellis_swiglu", _lib.trellis_swiglu(
+            gu.data_ptr(), rows, inter, h.data_ptr(),
+            None if kept is None else C.byref(_kept_rows(kept)), _handle(dev)))
+    return h, kept
+
+
+def swiglu_backward(dh, gu, dgu=None, h=None, again=False,
+                    stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(dgu, h): the gradient of swiglu from dh [rows, inter], and h once more, None
+    unless given or `again`. gu: bf16 [rows, 2 * inter], or as swiglu kept it."""
+    rows, inter = _dims("dh", dh, 2)
+    dev = _device(dh)
+    _want("dh", dh, torch.bfloat16, (rows, inter), dev)
+    kept = isinstance(gu, Kept)
+    if kept:
+        _want_kept("gu", gu, 2 * rows, inter, dev)
+    else:
+        _want("gu", gu, torch.bfloat16, (rows, 2 * inter), dev)
+    with _on(stream, dev):
+        if dgu is not None:
+            _want("dgu", dgu, torch.bfloat16, (rows, 2 * inter), dev)
+        if h is not None:
+            _want("h", h, torch.bfloat16, (rows, inter), dev)
+        if dgu is not None or h is not None:
+            _apart({"dgu": dgu, "h": h},
+                   {"dh": dh, **(_kept_parts("gu", gu) if kept else {"gu": gu})})
+        if dgu is None:
+            dgu = dh.new_empty((rows, 2 * inter))
+        if h is None and again:
+            h = torch.empty_like(dh)
+        _check("trellis_swiglu_backward", _lib.trellis_swiglu_backward(
+            dh.data_ptr(), None if kept else gu.data_ptr(),
+            C.byref(_kept_rows(gu)) if kept else None, rows, inter, dgu.data_ptr(), _ptr(h),
+            _handle(dev)))
+    return dgu, h
+
+
+def _expert_set(name: str, w: tuple, geom: Geometry, n: int, device: int) -> ExpertSet:
+    codes, scales, lut = w
+    stored, cols = ((geom.out_features, geom.in_features) if geom.axis == 1
+                    else (geom.in_features, geom.out_features))
+    _want(f"{name} scales", scales, torch.float32, (n, stored), device)
+    _want(f"{name} lut", lut, torch.float32, (1 << 12,), device)
+    _want(f"{name} codes", codes, torch.int32, codes.shape, device)
+    if codes.dim() < 1 or codes.shape[0] != n or codes.numel() != n * stored * cols * geom.k // 32:
+        raise ValueError(f"{name} codes: expected {n} experts of {stored} x {cols} weights of "
+                         f"{geom.k} bits, got {tuple(codes.shape)}")
+    return ExpertSet(codes.data_ptr(), scales.data_ptr(), lut.data_ptr(), geom)
+
+
+def experts_mlp(x, ids, weights, up, down, g_up, g_down, out=None, workspace=None,
+                stream=None) -> torch.Tensor:
+    """A whole layer of experts for up to 32 tokens: out [tokens, hidden] = the sum over
+    the experts e that a token chose of Wd_e bf16(w silu(Wg_e x) * (Wu_e x)). x: bf16
+    [tokens, hidden]; ids: int32 [tokens, top_k] (others than [0, experts): no choice);
+    weights: float32 [tokens, top_k], or None for ones. up and down: (codes, scales, lut)
+    as for experts, with g_up of axis 1, hidden -> 2 * inter (the gate's rows, then the
+    up's) and g_down of either axis, inter -> hidden. With one expert it is a dense MLP."""
+    gu, gd = _geom(g_up), _geom(g_down)
+    tokens, top_k = _dims("ids", ids, 2)
+    dev = _device(x)
+    _want("x", x, torch.bfloat16, (tokens, gu.in_features), dev)
+    _want("ids", ids, torch.int32, (tokens, top_k), dev)
+    if weights is not None:
+        _want("weights", weights, torch.float32, (tokens, top_k), dev)
+    n = _dims("up scales", up[1], 2)[0]
+    su, sd = _expert_set("up", up, gu, n, dev), _expert_set("down", down, gd, n, dev)
+    fn = "trellis_experts_mlp"
+    nbytes = _lib.trellis_experts_mlp_workspace_bytes(tokens, top_k, n, C.byref(su), C.byref(sd))
+    with _on(stream, dev):
+        ws, ws_bytes, hold = _workspace(fn, nbytes, workspace, x)
+        if out is not None or workspace is not None:
+            if out is not None:
+                _want("out", out, torch.bfloat16, (tokens, gu.in_features), dev)
+            _apart({"out": out, "workspace": workspace},
+                   {"x": x, "ids": ids, "weights": weights, "up codes": up[0], "up scales": up[1],
+                    "up lut": up[2], "down codes": down[0], "down scales": down[1],
+                    "down lut": down[2]})
+        if out is None:
+            out = torch.empty_like(x)
+        _check(fn, _lib.trellis_experts_mlp(
+            x.data_ptr(), ids.data_ptr(), _ptr(weights), tokens, top_k, n, C.byref(su), C.byref(sd),
+            out.data_ptr(), ws, ws_bytes, _handle(dev)))
+    return out
