@@ -13,7 +13,7 @@
 //     is formed. h is stored in the second product's operand order.
 //   down: a workgroup takes a strip of output columns and a part of the contraction;
 //     its waves take steps in turn.
-//   sum: adds the parts.
+//     The last workgroup of a strip to arrive adds the parts.
 #include "common.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
@@ -25,45 +25,79 @@ namespace trellis {
 namespace {
 
 constexpr int kUnitCols = 8;  // columns of h per unit: 8 gate and 8 up rows
-constexpr int kPartFloats = 5 * 1024;
+constexpr int kChunk = 4;     // units of a wave at a time
+constexpr int kUpPartFloats = 4096;  // 16 columns of 32 tokens of 8 waves
+constexpr int kAhead = 2;     // operands whose codebook values are read ahead
+constexpr int kMeet = 2;      // what a meeting of units costs, in quarter rounds of blocks
 
 // ---- the chosen experts -------------------------------------------------------
 
+constexpr int kMaxSlots = kLayerTokens * kLayerChoices;
+constexpr int kSlotsPerThread = (kMaxSlots + kExThreads - 1) / kExThreads;
+
 struct Chosen {
-    uint32_t mask[kMaxGroups];   // by expert: the tokens that chose it
-    uint16_t expert[kMaxGroups]; // ascending
-    int first[kMaxGroups / kWave + 1];
+    uint32_t mask[kMaxGroups];    // by expert: the tokens that chose it
+    uint16_t expert[kMaxGroups];  // the chosen, ascending
 };
 
-// Fills `s` from the tokens' ids; every thread of the workgroup calls it. Returns
-// the number of chosen experts. An id outside [0, experts) chooses none.
-__device__ __forceinline__ int find_chosen(Chosen& s, const int32_t* __restrict__ ids, int tokens,
-                                           int top_k, int experts) {
+// A thread's share of the tokens' choices, on their way from memory.
+struct Slots {
+    int id[kSlotsPerThread];  // -1 behind the last
+};
+__device__ __forceinline__ Slots load_slots(const int32_t* __restrict__ ids, int n) {
+    Slots s;
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i) s.id[i] = ids[min(static_cast<int>(threadIdx.x) + i * kExThreads, n - 1)];
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i)
+        if (static_cast<int>(threadIdx.x) + i * kExThreads >= n) s.id[i] = -1;
+    return s;
+}
+
+// Fills `s`; every thread of the workgroup calls it. Returns the number of chosen
+// experts. An id outside [0, experts) chooses none. Every wave writes the whole list
+// (the same values), so that it can read it without a barrier.
+// A slot's token is its number times `inverse` = ceil(2^32 / top_k), upper half (exact
+// for so few; 0 stands for top_k = 1).
+__device__ __forceinline__ int find_chosen(Chosen& s, const Slots& slots, uint32_t inverse, int experts) {
     const int tid = threadIdx.x, lane = tid & 63;
     for (int e = tid; e < experts; e += kExThreads) s.mask[e] = 0;
     __syncthreads();
-    for (int i = tid; i < tokens * top_k; i += kExThreads) {
-        const int e = ids[i];
-        if (static_cast<uint32_t>(e) < static_cast<uint32_t>(experts)) atomicOr(&s.mask[e], 1u << (i / top_k));
-    }
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i)
+        if (static_cast<uint32_t>(slots.id[i]) < static_cast<uint32_t>(experts))
+            atomicOr(&s.mask[slots.id[i]],
+                     1u << (inverse ? __umulhi(tid + i * kExThreads, inverse) : tid + i * kExThreads));
     __syncthreads();
-    for (int e0 = tid - lane; e0 < experts; e0 += kExThreads) {
-        const uint64_t live = __ballot(e0 + lane < experts && s.mask[e0 + lane] != 0);
-        if (lane == 0) s.first[e0 / kWave + 1] = __popcll(live);
-    }
-    if (tid == 0) s.first[0] = 0;
-    __syncthreads();
-    const int chunks = (experts + kWave - 1) / kWave;
-    if (tid == 0)
-        for (int i = 0; i < chunks; ++i) s.first[i + 1] += s.first[i];
-    __syncthreads();
-    for (int e0 = tid - lane; e0 < experts; e0 += kExThreads) {
+    int n = 0;
+    for (int e0 = 0; e0 < experts; e0 += kWave) {
         const bool mine = e0 + lane < experts && s.mask[e0 + lane] != 0;
         const uint64_t live = __ballot(mine);
-        if (mine) s.expert[s.first[e0 / kWave] + __popcll(live & ((1ull << lane) - 1))] = static_cast<uint16_t>(e0 + lane);
+        if (mine) s.expert[n + __popcll(live & ((1ull << lane) - 1))] = static_cast<uint16_t>(e0 + lane);
+        n += __popcll(live);
     }
-    __syncthreads();
-    return s.first[chunks];
+    wave_lds_sync();
+    return n;
+}
+
+// The tokens' choices with their weights.
+struct Choice {
+    int id;
+    float weight;
+};
+
+// A token's weight of expert e: the sum over its choices of it, ascending. Eight
+// choices are read at a time, without a wait between.
+__device__ __forceinline__ float weight_of(const Choice* given, int token, int top_k, int e) {
+    float sum = 0.f;
+    for (int k0 = 0; k0 < top_k; k0 += 8) {
+        Choice v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = given[token * top_k + min(k0 + k, top_k - 1)];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += k0 + k < top_k && v[k].id == e ? v[k].weight : 0.f;
+    }
+    return sum;
 }
 
 // ---- operand order of h ---------------------------------------------------------
@@ -75,10 +109,10 @@ __device__ __forceinline__ int find_chosen(Chosen& s, const int32_t* __restrict_
 __host__ __device__ __forceinline__ int h_pieces(int inter) { return (inter + 31) / 32; }
 
 template <int MT>
-__device__ __forceinline__ size_t h_at(int at, int pieces, int axis, int col, int token) {
-    const int piece = axis == 1 ? col / 256 * 8 + col % 64 / 8 : col / 32;
-    const int c = axis == 1 ? col % 256 / 64 : col % 32 / 8;
-    return (((static_cast<size_t>(at) * pieces + piece) * MT + token / 16) * kWave + 16 * c + token % 16) * 8 +
+__device__ __forceinline__ size_t h_at(uint32_t at, uint32_t pieces, int axis, uint32_t col, uint32_t token) {
+    const uint32_t piece = axis == 1 ? col / 256 * 8 + col % 64 / 8 : col / 32;
+    const uint32_t c = axis == 1 ? col % 256 / 64 : col % 32 / 8;
+    return ((static_cast<size_t>(at) * pieces + piece) * MT + token / 16) * (kWave * 8) + (16 * c + token % 16) * 8 +
            col % 8;
 }
 
@@ -95,123 +129,261 @@ struct UpArgs {
     CodeLayout lay;
     uint64_t words;
     uint16_t* h;
+    uint32_t inverse; // ceil(2^32 / top_k)
+    int per;          // units of an expert
+    int strips;       // of the down product, whose arrivals start at zero
+    uint32_t* arrived;
+    int round, meet;  // units that meet in LDS at once, and what a chunk's meetings cost
 };
 
+__device__ __forceinline__ uint16_t h_value(float weight, float g, float u) {
+    return round_bf16(weight * (g / (1.f + expf(-g)) * u));
+}
+
+// How the eight waves share a workgroup's units: 2^w of them a unit's blocks, in
+// teams that share the units. The fewest rounds of blocks win; several waves to a unit
+// pay for meeting in LDS (`meet` quarter rounds a chunk).
+__device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
+    int best = 0, least = INT32_MAX;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int each = (units + (kExWaves >> w) - 1) >> (3 - w);
+        const int cost = 4 * ((nb + (1 << w) - 1) >> w) * each + (w ? (each + kChunk - 1) / kChunk * meet : 0);
+        if (cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return best;
+}
+
+// This workgroup's units. A wave takes `kChunk` units of its team at a time through
+// its blocks: the tokens' operands of a block serve all of them. A unit's next words
+// are loaded as soon as its last ones are decoded.
 template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
-    __shared__ float parts[kPartFloats];
+    __shared__ float parts[kUpPartFloats];
     __shared__ Chosen chosen;
+    __shared__ Choice given[kMaxSlots];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, c = lane >> 4;
+    const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
+    float weight[kSlotsPerThread];
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i) {
+        weight[i] = 1.f;
+        if (p.weights) weight[i] = p.weights[min(tid + i * kExThreads, p.tokens * p.top_k - 1)];
+    }
+    if (blockIdx.x == 0)
+        for (int i = tid; i < p.strips; i += kExThreads) p.arrived[i] = 0;
     typename ExTable<K>::Table::Src src;
     ExTable<K>::Table::fetch(src, p.lut);
-    const int live = __builtin_amdgcn_readfirstlane(find_chosen(chosen, p.ids, p.tokens, p.top_k, p.experts));
-    const int nb = p.hidden / kT, per = (p.inter + kUnitCols - 1) / kUnitCols;
-    const int64_t units = static_cast<int64_t>(live) * per;
-    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    const int live = find_chosen(chosen, slots, p.inverse, p.experts);
+    const int nb = p.hidden / kT, per = p.per, all = live * per;
+    const int share = all / static_cast<int>(gridDim.x), rest = all - share * static_cast<int>(gridDim.x);
+    const int u0 = static_cast<int>(blockIdx.x) * share + min(static_cast<int>(blockIdx.x), rest);
+    const int units = share + (static_cast<int>(blockIdx.x) < rest);
+    if (units == 0) return;
+    const int round = min(kChunk, p.round);  // units that meet at once
+    const int lw = log_ways_for(units, nb, p.meet), ways = 1 << lw, lt = 3 - lw;
+    const int way = wave & (ways - 1), team = wave >> lw;
+    auto team_first = [&](int t) { return u0 + ((units * t) >> lt); };
+    const int first = team_first(team), end = team_first(team + 1);
+    const int chunks = (((units + (1 << lt) - 1) >> lt) + kChunk - 1) / kChunk;
+
+    uint32_t w[kChunk][2 * K + 1];
+    float sc[kChunk];
+    u32x4 a[MT][8];
+    const uint16_t* x[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        x[m] = p.x + static_cast<size_t>(min(16 * m + j, p.tokens - 1)) * p.hidden + 64 * c;
+    auto load_x = [&](int b) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                a[m][s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
+    };
+    // a unit's rows are a uniform address for gate and up plus a lane's offset
+    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale) {
+        const uint32_t* gate = p.codes + e * p.words + block_word<K>(p.lay, col0, b);
+        const uint32_t* up = gate + static_cast<uint64_t>(p.inter) * p.lay.row_words;
+        const float* sg = p.scales + static_cast<size_t>(e) * (2 * p.inter) + col0;
+        const int row = min(j & 7, p.inter - 1 - col0);
+        load_run64<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words), 3 - c,
+                      words);
+        scale = sg[j < 8 ? row : row + p.inter];
+    };
+    floatx4 acc[kChunk][MT] = {};
+    // the wave's place in its team's units and blocks, and unit u's expert and columns.
+    // Loads without a branch: the workgroup's last unit stands for those that are not.
+    int u = first, b = min(way, nb - 1), at = first / per, in = first - at * per;
+    {
+        int v = min(first, u0 + units - 1), va = at, vi = in, e[kChunk], col0[kChunk];
+        if (v != first) va = v / per, vi = v - va * per;
+#pragma unroll
+        for (int g = 0; g < kChunk; ++g) {
+            e[g] = chosen.expert[va];
+            col0[g] = vi * kUnitCols;
+            const bool more = v + 1 < u0 + units;
+            v += more;
+            vi += more;
+            if (vi == per) {
+                vi = 0;
+                ++va;
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < kChunk; ++g)
+            load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g]);
+        load_x(b);
+    }
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i) {
+        const int s = tid + i * kExThreads;
+        if (s >= p.tokens * p.top_k) continue;
+        given[s] = {slots.id[i], weight[i]};
+    }
     ExTable<K>::Table::store(src, tab);
     __syncthreads();
-
-    // Units of a phase: their sums of all waves, [unit][wave][token][16], fill `parts`.
-    const int unit_floats = 16 * p.tokens, phase_units = kPartFloats / (kExWaves * unit_floats);
-    const int tasks = (u1 - u0) * nb, phase_tasks = phase_units * nb;
-    struct Work {
-        uint32_t w[2 * K + 1];
-        float sc;
-        u32x4 a[MT][8];
-    };
-    auto load = [&](Work& q, int t) {
-        const int u = u0 + t / nb, b = t % nb;
-        const int at = u / per, col0 = (u - at * per) * kUnitCols;
-        const int e = __builtin_amdgcn_readfirstlane(chosen.expert[at]);
-        const int row = min(col0 + (j & 7), p.inter - 1) + (j < 8 ? 0 : p.inter);
-        load_run64<K>(p.codes + e * p.words + block_word<K>(p.lay, row, b), 3 - c, q.w);
-        q.sc = p.scales[static_cast<size_t>(e) * (2 * p.inter) + row];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const uint16_t* x = p.x + static_cast<size_t>(min(16 * m + j, p.tokens - 1)) * p.hidden +
-                                static_cast<size_t>(b) * kT + 64 * c;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) q.a[m][s] = *reinterpret_cast<const u32x4*>(x + 8 * s);
+    auto one = [&] {
+        constexpr int D = kAhead;
+        int nu = u, next = b + ways;
+        if (next >= nb) {
+            next = way;
+            nu = u + kChunk;
         }
-    };
-    floatx4 acc[MT] = {};
-    int phase = 0, unit = -1;  // unit: whose sums `acc` holds
-    auto put = [&] {
-        if (unit < 0) return;
-        float* o = parts + ((unit - phase * phase_units) * kExWaves + wave) * unit_floats + j;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (16 * m + 4 * c + i < p.tokens) o[16 * (16 * m + 4 * c + i)] = acc[m][i];
-            acc[m] = floatx4{};
+        const int n = min(kChunk, end - u);
+        const bool reload = nu < end && next != b;
+        int na = at, ni = in + (nu - u);
+        while (ni >= per) {
+            ni -= per;
+            ++na;
         }
-        unit = -1;
-    };
-    // Sums of a phase's units, the waves in the order of their first blocks, and h.
-    auto finish = [&] {
-        put();
-        __syncthreads();
-        const int n = min(phase_units, u1 - u0 - phase * phase_units);
-        for (int i = tid; i < n * p.tokens * kUnitCols; i += kExThreads) {
-            const int col = i % kUnitCols, m = i / kUnitCols % p.tokens, v = i / kUnitCols / p.tokens;
-            const int lu = phase * phase_units + v, at = (u0 + lu) / per;
-            const int out = (u0 + lu - at * per) * kUnitCols + col, e = chosen.expert[at];
-            if (!((chosen.mask[e] >> m) & 1)) continue;
-            float g = 0.f, u = 0.f;
-            for (int k = 0; k < min(nb, kExWaves); ++k) {
-                const float* o = parts + (v * kExWaves + (lu * nb + k) % kExWaves) * unit_floats + 16 * m + col;
-                g += o[0];
-                u += o[8];
+        const int next_at = na, next_in = ni;
+        Gathered<pair> v[D + 1];
+        static_for<0, D>([&](auto ic) { v[decltype(ic)::value] = gather_tab<K, decltype(ic)::value, pair, rep>(w[0], tab); });
+        static_for<0, kChunk>([&](auto gc) {
+            constexpr int g = decltype(gc)::value;
+            if (g >= n) return;
+            static_for<0, 8>([&](auto ic) {
+                constexpr int S = decltype(ic)::value, A = S + D, i = 8 * g + S;
+                __builtin_amdgcn_s_setprio(2);
+                if constexpr (A < 8) {
+                    v[(i + D) % (D + 1)] = gather_tab<K, A, pair, rep>(w[g], tab);
+                } else if constexpr (g + 1 < kChunk) {
+                    if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, A - 8, pair, rep>(w[g + 1], tab);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                const u32x4 f = pack_fragment(v[i % (D + 1)], sc[g]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[g][m] = mfma16x16x32(as_bf16x8(a[m][S]), as_bf16x8(f), acc[g][m]);
+            });
+            // the next block's operands before the last unit's words: they are waited for
+            // first, and a wait is for all loads before
+            if (reload && g + 1 == n) load_x(next);
+            if (nu + g < end)
+                load_codes(__builtin_amdgcn_readfirstlane(chosen.expert[na]), ni * kUnitCols, next, w[g], sc[g]);
+            if (++ni == per) {
+                ni = 0;
+                ++na;
             }
-            float w = 0.f;
-            for (int k = 0; k < p.top_k; ++k)
-                if (p.ids[m * p.top_k + k] == e) w += p.weights ? p.weights[m * p.top_k + k] : 1.f;
-            const float hv = w * (g / (1.f + expf(-g)) * u);
-            p.h[h_at<MT>(at, h_pieces(p.inter), p.axis_down, out, m)] = out < p.inter ? round_bf16(hv) : uint16_t{0};
-        }
-        __syncthreads();
-        ++phase;
-    };
-    auto multiply = [&](const Work& q) {
-        Gathered<pair> v[2];
-        v[0] = gather_tab<K, 0, pair, rep>(q.w, tab);
-        static_for<0, 8>([&](auto sc) {
-            constexpr int S = decltype(sc)::value;
-            __builtin_amdgcn_s_setprio(2);
-            if constexpr (S + 1 < 8) v[(S + 1) & 1] = gather_tab<K, S + 1, pair, rep>(q.w, tab);
-            __builtin_amdgcn_s_setprio(0);
-            const u32x4 f = pack_fragment(v[S & 1], q.sc);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m] = mfma16x16x32(as_bf16x8(q.a[m][S]), as_bf16x8(f), acc[m]);
         });
+        u = nu;
+        b = next;
+        at = next_at;
+        in = next_in;
     };
-    const int phases = (u1 - u0 + phase_units - 1) / phase_units;
-    auto one = [&](Work& now, Work& next, int t) {
-        while (phase < t / phase_tasks) finish();
-        if (t / nb != unit) {
-            put();
-            unit = t / nb;
+    auto put = [&](int expert, int col, int token, uint16_t v) {
+        p.h[h_at<MT>(expert, h_pieces(p.inter), p.axis_down, col, token)] = col < p.inter ? v : uint16_t{0};
+    };
+    // h of the chunk from `from` on: of a whole unit per wave from registers (lanes j
+    // and j + 8 hold its gate and up; lane l the weight of token l) ...
+    auto finish_alone = [&](int from) {
+        int fa = from / per, fi = from - fa * per, known = -1;
+        float mine = 0.f;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int g = 0; g < kChunk; ++g) {
+            if (from + g >= end) break;
+            if (fa != known) {
+                const int e = chosen.expert[fa];
+                mask = chosen.mask[e];
+                mine = weight_of(given, min(lane, p.tokens - 1), p.top_k, e);
+                known = fa;
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int token = 16 * m + 4 * c + i;
+                    const float up = __shfl_xor(acc[g][m][i], 8), weight = __shfl(mine, token);
+                    if (j < 8 && ((mask >> token) & 1))
+                        put(fa, fi * kUnitCols + j, token, h_value(weight, acc[g][m][i], up));
+                }
+            if (++fi == per) {
+                fi = 0;
+                ++fa;
+            }
         }
-        if (t + kExWaves < tasks) load(next, t + kExWaves);
-        multiply(now);
     };
-    Work q[2];
-    int t = wave;
-    if (t < tasks) load(q[0], t);
-    while (t < tasks) {
-        one(q[0], q[1], t);
-        t += kExWaves;
-        if (t >= tasks) break;
-        one(q[1], q[0], t);
-        t += kExWaves;
+    // ... or from the ways' sums in LDS, in their order.
+    auto finish_together = [&](int chunk) {
+        for (int r0 = 0; r0 < kChunk; r0 += round) {
+#pragma unroll
+            for (int g = 0; g < kChunk; ++g) {
+                if (g < r0 || g >= r0 + round) continue;
+                float* o = parts + ((g - r0) * kExWaves + wave) * 16 * p.tokens + j;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int token = 16 * m + 4 * c + i;
+                        if (token < p.tokens) o[16 * token] = acc[g][m][i];
+                    }
+            }
+            __syncthreads();
+            const uint32_t col = tid % kUnitCols, tokens = p.tokens;
+            for (uint32_t i = tid / kUnitCols; i < (round * tokens) << lt; i += kExThreads / kUnitCols) {
+                const uint32_t t = i & ((1 << lt) - 1), q = (i >> lt) / tokens, token = (i >> lt) - q * tokens;
+                const int unit = team_first(t) + kChunk * chunk + r0 + static_cast<int>(q);
+                if (r0 + static_cast<int>(q) >= kChunk || unit >= team_first(t + 1)) continue;
+                const uint32_t expert = static_cast<uint32_t>(unit) / static_cast<uint32_t>(per);
+                const int e = chosen.expert[expert];
+                const float* o = parts + ((q * kExWaves + (t << lw)) * tokens + token) * 16 + col;
+                float gate[kExWaves], up[kExWaves];
+#pragma unroll
+                for (int k = 0; k < kExWaves; ++k) {
+                    const uint32_t at_k = 16 * tokens * min(k, ways - 1);
+                    gate[k] = o[at_k];
+                    up[k] = o[at_k + 8];
+                }
+                const float weight = weight_of(given, token, p.top_k, e);
+#pragma unroll
+                for (int k = 1; k < kExWaves; ++k) {
+                    gate[0] += k < ways ? gate[k] : 0.f;
+                    up[0] += k < ways ? up[k] : 0.f;
+                }
+                if ((chosen.mask[e] >> token) & 1)
+                    put(expert, (unit - expert * per) * kUnitCols + col, token, h_value(weight, gate[0], up[0]));
+            }
+            if (chunk + 1 < chunks || r0 + round < kChunk) __syncthreads();
+        }
+    };
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int from = first + kChunk * chunk;
+        for (int s = way; s < nb && from < end; s += ways) one();
+        if (ways == 1) finish_alone(from);
+        else finish_together(chunk);
+#pragma unroll
+        for (int g = 0; g < kChunk; ++g)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[g][m] = floatx4{};
     }
-    while (phase < phases) finish();
 }
 
 // ---- down -----------------------------------------------------------------------
@@ -225,8 +397,11 @@ struct DownArgs {
     const float* lut;
     CodeLayout lay;
     uint64_t words;
-    int strips, ways;  // strips of columns, parts of the contraction
-    float* partial;    // [way][tokens][hidden]
+    uint32_t inverse;   // ceil(2^32 / top_k)
+    int strips, ways;   // strips of columns, parts of the contraction
+    float* partial;     // [way][tokens][hidden]
+    uint32_t* arrived;  // [strip] workgroups whose part is there
+    uint16_t* out;
 };
 
 // A wave's sums over its tasks (an expert's and piece's, `steps` pieces each), the
@@ -250,33 +425,74 @@ struct Sums {
     }
 };
 
-// The waves' sums of a strip of COLS columns, in wave order, to the workgroup's
-// part: each(f) gives f(token, column, value). `sums` takes the table's place.
+// The waves' sums of a strip of COLS columns, in wave order, are the workgroup's part:
+// each(f) gives f(token, column, value). `sums` takes the table's place. The last
+// workgroup of a strip to arrive adds the parts, in their order, whichever it is. Parts
+// and arrivals are device-scope accesses, which no die's L2 keeps to itself, and a wave
+// waits until its parts are in memory before its workgroup arrives: fences instead,
+// which write a whole L2 back, took 35 to 50 us of a call, a kernel of its own for the
+// sums 2.4 to 4.8 us and the host's launch.
 template <int COLS, typename F>
 __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way, F&& each) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     __syncthreads();  // the table is read
     each([&](int token, int col, float v) {
         if (token < p.tokens) sums[(wave * p.tokens + token) * COLS + col] = v;
     });
     __syncthreads();
-    for (int i = threadIdx.x; i < p.tokens * COLS; i += kExThreads) {
-        const int token = i / COLS, col = strip * COLS + i % COLS;
-        float v = 0.f;
+    const int n = p.tokens * COLS;
+    auto sum_of = [&](int i) {
+        float v[kExWaves];
 #pragma unroll
-        for (int w = 0; w < kExWaves; ++w) v += sums[w * p.tokens * COLS + i];
-        if (col < p.hidden) p.partial[(static_cast<size_t>(way) * p.tokens + token) * p.hidden + col] = v;
+        for (int w = 0; w < kExWaves; ++w) v[w] = sums[w * n + i];
+#pragma unroll
+        for (int w = 1; w < kExWaves; ++w) v[0] += v[w];
+        return v[0];
+    };
+    const int col0 = strip * COLS;
+    if (p.ways == 1) {
+        for (int i = tid; i < n; i += kExThreads) {
+            const int col = col0 + i % COLS;
+            if (col < p.hidden) p.out[(i / COLS) * p.hidden + col] = round_bf16(sum_of(i));
+        }
+        return;
+    }
+    // parts in strips: [strip][way][token][COLS]
+    float* parts = p.partial + static_cast<size_t>(strip) * p.ways * n;
+    for (int i = tid; i < n; i += kExThreads)
+        __hip_atomic_store(parts + way * n + i, sum_of(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __shared__ uint32_t before;
+    if (tid == 0)
+        before = __hip_atomic_fetch_add(p.arrived + strip, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before != static_cast<uint32_t>(p.ways) - 1) return;
+    for (int i = tid; i < n; i += kExThreads) {
+        float v = 0.f;
+        for (int w0 = 0; w0 < p.ways; w0 += 8) {
+            float q[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                q[w] = __hip_atomic_load(parts + min(w0 + w, p.ways - 1) * n + i, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) v += w0 + w < p.ways ? q[w] : 0.f;
+        }
+        const int col = col0 + i % COLS;
+        if (col < p.hidden) p.out[(i / COLS) * p.hidden + col] = round_bf16(v);
     }
 }
 
 // The tasks of this workgroup, wave by wave: load(work, at, piece) of the next one
 // is in flight while multiply(work) runs; `at` numbers the chosen experts.
-template <typename Work, typename Load, typename Multiply, typename Close>
+template <typename Work, typename Load, typename Between, typename Multiply, typename Close>
 __device__ __forceinline__ void run_tasks(int first, int end, int pieces, int wave, Load&& load,
-                                          Multiply&& multiply, Close&& close) {
+                                          Between&& between, Multiply&& multiply, Close&& close) {
     Work q[2];
     int t = first + wave, at = t / pieces;
     if (t < end) load(q[0], at, t - at * pieces);
+    between();
     auto one = [&](Work& now, Work& next) {
         const int nt = t + kExWaves, nat = nt / pieces;
         if (nt < end) load(next, nat, nt - nat * pieces);
@@ -303,11 +519,10 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
     typename ExTable<K>::Table::Src src;
     ExTable<K>::Table::fetch(src, p.lut);
-    const int live = __builtin_amdgcn_readfirstlane(find_chosen(chosen, p.ids, p.tokens, p.top_k, p.experts));
-    ExTable<K>::Table::store(src, tab);
-    __syncthreads();
+    const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int strip = blockIdx.x / p.ways, way = blockIdx.x % p.ways, nb = p.inter / kT;
     const int64_t tasks = static_cast<int64_t>(live) * nb;
     struct Work {
@@ -334,6 +549,10 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
             for (int s = 0; s < 8; ++s)
 #pragma unroll
                 for (int m = 0; m < MT; ++m) q.a[m][s] = ha[(s * MT + m) * kWave];
+        },
+        [&] {
+            ExTable<K>::Table::store(src, tab);
+            __syncthreads();
         },
         [&](const Work& q) {
             Gathered<pair> v[2];
@@ -367,11 +586,10 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
     typename ExTable<K>::Table::Src src;
     ExTable<K>::Table::fetch(src, p.lut);
-    const int live = __builtin_amdgcn_readfirstlane(find_chosen(chosen, p.ids, p.tokens, p.top_k, p.experts));
-    ExTable<K>::Table::store(src, tab);
-    __syncthreads();
+    const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int strip = blockIdx.x / p.ways, way = blockIdx.x % p.ways, steps = h_pieces(p.inter);
     const int64_t tasks = static_cast<int64_t>(live) * steps;
     struct Work {
@@ -416,6 +634,10 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
                 q.sc[i] = s.scales[r];
             }
         },
+        [&] {
+            ExTable<K>::Table::store(src, tab);
+            __syncthreads();
+        },
         [&](const Work& q) {
             Pieces<K, CL> ps;
             ps.set(q.q, first.sh);
@@ -443,34 +665,25 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
     });
 }
 
-// out = the parts' sum, ascending.
-__global__ __launch_bounds__(256) void layer_sum_kernel(const float* __restrict__ partial, int ways, int n,
-                                                        uint16_t* __restrict__ out) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int w = 0; w < ways; ++w) v += partial[static_cast<size_t>(w) * n + i];
-    out[i] = round_bf16(v);
-}
-
 // ---- launches ---------------------------------------------------------------------
 
 struct LayerPlan {
-    int strips, ways;
-    size_t partial, bytes;
+    int strips, cols, ways;
+    size_t arrived, partial, bytes;
 };
 
 LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, int axis_down) {
     LayerPlan p;
-    const int cols = axis_down == 1 ? kDownCols1 : kDownCols0;
-    p.strips = (hidden + cols - 1) / cols;
+    p.cols = axis_down == 1 ? kDownCols1 : kDownCols0;
+    p.strips = (hidden + p.cols - 1) / p.cols;
     p.ways = cu_count() / p.strips;
     if (p.ways < 1) p.ways = 1;
     const size_t chosen = tokens * top_k < experts ? tokens * top_k : experts;
     const size_t operands = tokens > 16 ? 2 : 1;
-    p.partial = chosen * h_pieces(inter) * operands * kWave * 16;
-    p.bytes = p.partial + static_cast<size_t>(p.ways) * tokens * hidden * sizeof(float);
+    p.arrived = chosen * h_pieces(inter) * operands * kWave * 16;
+    p.partial = p.arrived + (static_cast<size_t>(p.strips) * sizeof(uint32_t) + 255) / 256 * 256;
+    p.bytes = p.partial;
+    if (p.ways > 1) p.bytes += static_cast<size_t>(p.strips) * p.ways * tokens * p.cols * sizeof(float);
     return p;
 }
 
@@ -498,19 +711,25 @@ hipError_t launch_layer(const LayerArgs& a, void* ws, hipStream_t st) {
     const int hidden = u.in, inter = d.in;
     const LayerPlan plan = layer_plan(a.tokens, a.top_k, u.experts, hidden, inter, d.axis);
     uint16_t* h = static_cast<uint16_t*>(ws);
+    uint32_t* arrived = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + plan.arrived);
     float* partial = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.partial);
-    const UpArgs up{a.x,    a.ids,   a.weights, a.tokens, a.top_k, u.experts, hidden, inter,
-                    d.axis, u.codes, u.scales,  u.lut,    u.lay,   u.words,   h};
-    hipError_t e = u.k == 2 ? launch_up<2>(up, st) : u.k == 3 ? launch_up<3>(up, st) : launch_up<4>(up, st);
+    const uint32_t inverse = a.top_k == 1 ? 0 : static_cast<uint32_t>(((uint64_t{1} << 32) + a.top_k - 1) / a.top_k);
+    // a unit's sums of eight waves: 16 columns of every token
+    int round = kUpPartFloats / (kExWaves * 16 * a.tokens);
+    if (round > kChunk) round = kChunk;
+    const UpArgs up{a.x,     a.ids,   a.weights, a.tokens, a.top_k, u.experts, hidden,  inter,
+                    d.axis,  u.codes, u.scales,  u.lut,    u.lay,   u.words,   h,       inverse,
+                    (inter + kUnitCols - 1) / kUnitCols,   plan.strips,        arrived, round,
+                    kMeet * ((kChunk + round - 1) / round)};
+    const hipError_t e = u.k == 2   ? launch_up<2>(up, st)
+                         : u.k == 3 ? launch_up<3>(up, st)
+                                    : launch_up<4>(up, st);
     if (e != hipSuccess) return e;
-    const DownArgs down{h,       a.ids,    a.tokens, a.top_k, d.experts, hidden,      inter,     d.codes,
-                        d.scales, d.lut,   d.lay,    d.words, plan.strips, plan.ways, partial};
-    e = d.k == 2   ? launch_down<2>(down, d.axis, st)
-        : d.k == 3 ? launch_down<3>(down, d.axis, st)
-                   : launch_down<4>(down, d.axis, st);
-    if (e != hipSuccess) return e;
-    const int n = a.tokens * hidden;
-    return launch_kernel(layer_sum_kernel, dim3((n + 255) / 256), dim3(256), st, partial, plan.ways, n, a.out);
+    const DownArgs down{h,     a.ids,   a.tokens, a.top_k, d.experts,   hidden,    inter,   d.codes, d.scales,
+                        d.lut, d.lay,   d.words,  inverse, plan.strips, plan.ways, partial, arrived, a.out};
+    return d.k == 2   ? launch_down<2>(down, d.axis, st)
+           : d.k == 3 ? launch_down<3>(down, d.axis, st)
+                      : launch_down<4>(down, d.axis, st);
 }
 
 }  // namespace trellis
