@@ -132,6 +132,102 @@ __device__ __forceinline__ Piece<KEPT> load_piece(const WideRows& p, int row, in
     }
 }
 
+// 8 rows of a lane's 8 columns in a strip of 128 (lane (j, c): rows of its c), as
+// loaded. In 8 bits the strip's four exponents of a row are one word, which lane j
+// loads of row j: one load for the patch instead of eight.
+struct KeptPatch {
+    u32x2 codes[8];
+    uint32_t exponents;
+    uint32_t shift;  // where they start in the word; 32: a row of zeros
+};
+struct WidePatch {
+    u32x4 row[8];
+};
+template <bool KEPT>
+using Patch = std::conditional_t<KEPT, KeptPatch, WidePatch>;
+
+// rows: this lane's 8 row numbers in LDS, negative: zeros.
+template <bool VEC, bool KEPT>
+__device__ __forceinline__ void load_patch(Patch<KEPT>& v, const WideRows& p, const int* rows, int col, int width) {
+    if constexpr (!KEPT) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v.row[i] = load8<VEC>(p.x + static_cast<size_t>(max(rows[i], 0)) * width, col, width, rows[i] >= 0);
+    } else {
+        const int j = threadIdx.x & 15, first = (col - 8 * j) / kKeptGroup;  // of the strip's groups
+        const int groups = (width + kKeptGroup - 1) / kKeptGroup, row = rows[j & 7];
+        const uint8_t* at = p.kept.exponents + static_cast<size_t>(max(row, 0)) * groups;
+        if constexpr (VEC) {
+            // Without a branch, so that a wait counts the loads behind it: columns past
+            // the row read its last ones, and rows of zeros, whose rank-long values are
+            // zeros, any row's codes, with an exponent that makes them finite.
+            typedef uint32_t u32_any __attribute__((aligned(1)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v.codes[i] = *reinterpret_cast<const u32x2*>(
+                    p.kept.codes + static_cast<size_t>(max(rows[i], 0)) * width + min(col, width - 8));
+            const int from = min(first, groups - 4);
+            v.exponents = *reinterpret_cast<const u32_any*>(at + from);
+            v.shift = row < 0 ? 32 : 8 * (first - from);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v.codes[i] = u32x2{0u, 0u};
+                if (rows[i] >= 0 && col < width)
+                    v.codes[i] = load_codes(p.kept.codes + static_cast<size_t>(rows[i]) * width + col, width - col);
+            }
+            v.exponents = 0;
+            v.shift = 0;
+            if (row >= 0)
+                for (int g = 0; g < 4 && first + g < groups; ++g)
+                    v.exponents |= static_cast<uint32_t>(at[first + g]) << (8 * g);
+        }
+    }
+}
+
+// The columns of an 8 x 8 patch of such rows (word d: rows 2 d and 2 d + 1). Rows in 8
+// bits go from codes to a column's operand directly: made bf16 rows first, they took 56
+// registers more, which left one wave per SIMD where two fit. Both sums of 4096 rows of
+// 5120 -> 17408 at rank 32, us: 81 so, 61 directly, 61 with one load of exponents
+// instead of eight, 52 with all loads made unconditionally; 53 for bf16 rows.
+template <bool KEPT>
+struct Columns {
+    const u32x4 (&row)[8];
+    __device__ __forceinline__ explicit Columns(const WidePatch& p) : row(p.row) {}
+    template <int Q>
+    __device__ __forceinline__ u32x4 at() const {
+        return patch_column<Q>(row);
+    }
+};
+template <>
+struct Columns<true> {
+    const u32x2 (&codes)[8];
+    float step[8];
+    __device__ __forceinline__ explicit Columns(const KeptPatch& p) : codes(p.codes) {
+        // lane i of a row of 16 holds row i's four exponents, a lane's columns lie in
+        // group j / 4 of the strip
+        const uint32_t shift = (threadIdx.x & 12) << 1;
+        const int mine = static_cast<int>(p.shift < 32 ? p.exponents >> p.shift : 0);
+        static_for<0, 8>([&](auto ic) {
+            constexpr int i = decltype(ic)::value, row_newbcast = 0x150;
+            const int four = __builtin_amdgcn_mov_dpp(mine, row_newbcast + i, 0xF, 0xF, true);
+            step[i] = kept_step((static_cast<uint32_t>(four) >> shift) & 255u);
+        });
+    }
+    template <int Q>
+    __device__ __forceinline__ u32x4 at() const {
+        u32x4 r;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const float lo = static_cast<float>(static_cast<int8_t>(codes[2 * d][Q / 4] >> (8 * (Q % 4))));
+            const float hi = static_cast<float>(static_cast<int8_t>(codes[2 * d + 1][Q / 4] >> (8 * (Q % 4))));
+            r[d] = __builtin_amdgcn_perm(__float_as_uint(hi * step[2 * d + 1]), __float_as_uint(lo * step[2 * d]),
+                                         0x07060302u);
+        }
+        return r;
+    }
+};
+
 // ---- few rows ----------------------------------------------------------------
 
 constexpr int kDirectCols = 512;  // columns of x per workgroup: 64 lanes x 8
@@ -807,15 +903,13 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     // This wave's 32-row halves of the segment's tiles wave, wave + 4, ...; the
     // next half's rows are loaded while one is multiplied.
     struct Half {
-        Piece<KEPT> patch[8];
+        Patch<KEPT> patch;
         u32x4 a[R][kBf16Parts];
     };
     auto load = [&](Half& q, int step) {
         const int t = wave + kWgWaves * (step >> 1), h = step & 1;
         const int* trow = seg_rows + t * kTileRows + 32 * h + 8 * c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q.patch[i] = load_piece<VEC, KEPT>(p.x, max(trow[i], 0), col, width, trow[i] >= 0);
+        load_patch<VEC, KEPT>(q.patch, p.x, trow, col, width);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -827,12 +921,10 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
     };
     floatx4 acc[R][8] = {};
     auto multiply = [&](const Half& q) {
-        u32x4 patch[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) patch[i] = piece_values(q.patch[i]);
+        const Columns<KEPT> columns(q.patch);
         static_for<0, 8>([&](auto qc) {
             constexpr int e = decltype(qc)::value;
-            const u32x4 b = patch_column<e>(patch);
+            const u32x4 b = columns.template at<e>();
 #pragma unroll
             for (int part = 0; part < kBf16Parts; ++part)
 #pragma unroll
@@ -894,7 +986,7 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
 // b's rows are held in 8 bits (8-byte pieces there). Without a list (no rows) every adapter is one segment of none.
 // Grid: (strips of side a then of side b, segments, rank pairs).
 template <int R, bool VEC, bool KEPT>
-__global__ __launch_bounds__(kWgThreads) void outer_kernel(
+__global__ __launch_bounds__(kWgThreads, KEPT ? 2 : 1) void outer_kernel(
     OuterSide a, OuterSide b, const SegInfo* __restrict__ segs, const int32_t* __restrict__ tile_rows,
     int rank, int r16) {
     __shared__ __attribute__((aligned(16))) float sum[16 * R * kStrip];

@@ -83,7 +83,7 @@ int adapters_backward(const uint16_t* dy, const uint16_t* x, const void* rows_of
                                                                 f->count, true))))
         return st;
     const bool vec_in = f->in_features % 8 == 0 && all16(x, f->a, base) && all16(dx, da, nullptr) &&
-                        aligned(kept.codes, 8);
+                        (!kept.codes || (aligned(kept.codes, 8) && f->in_features > 3 * trellis::kKeptGroup));
     const bool vec_out = f->out_features % 8 == 0 && all16(dy, f->b, db);
     return status_of(trellis::launch_adapters_backward(dy, x, kept, u, ids, factors(f), rows, base,
                                                        dx, da, db, vec_in, vec_out, workspace, stream));
