@@ -98,38 +98,22 @@ __device__ __forceinline__ Parts3 split3(float w) {
     return {{hi, mid, rest - mid}};
 }
 
-// 8 values of a wide row as loaded, and as bf16: a row of bf16, or (KEPT) one held
-// in 8 bits, whose codes and exponent stay as they are until the values are used.
-struct KeptPiece {
-    u32x2 codes;
-    uint32_t exponent;
-};
-__device__ __forceinline__ u32x4 piece_values(const u32x4& v) { return v; }
-__device__ __forceinline__ u32x4 piece_values(const KeptPiece& v) { return kept_values(v.codes, v.exponent); }
-
-// Where the wide rows of one of the outer products are: `x`, or `kept` if x is null.
+// Where the wide rows of one of the outer products are: `x`, or, if it is null (KEPT),
+// `kept`, rows held in 8 bits.
 struct WideRows {
     const uint16_t* x;
     KeptRows kept;
 };
 
-template <bool KEPT>
-using Piece = std::conditional_t<KEPT, KeptPiece, u32x4>;
-
+// 8 values of a row; see load8.
 template <bool VEC, bool KEPT>
-__device__ __forceinline__ Piece<KEPT> load_piece(const WideRows& p, int row, int col, int width, bool live) {
-    if constexpr (!KEPT) {
-        return load8<VEC>(p.x + static_cast<size_t>(row) * width, col, width, live);
-    } else {
-        KeptPiece v = {{0u, 0u}, 0u};
-        if (live && col < width) {
-            const size_t groups = (width + kKeptGroup - 1) / kKeptGroup;
-            const int8_t* at = p.kept.codes + static_cast<size_t>(row) * width + col;
-            v.codes = VEC ? *reinterpret_cast<const u32x2*>(at) : load_codes(at, width - col);
-            v.exponent = p.kept.exponents[row * groups + col / kKeptGroup];
-        }
-        return v;
-    }
+__device__ __forceinline__ u32x4 load_wide(const WideRows& p, int row, int col, int width) {
+    if constexpr (!KEPT) return load8<VEC>(p.x + static_cast<size_t>(row) * width, col, width, true);
+    if (col >= width) return u32x4{0u, 0u, 0u, 0u};
+    const size_t groups = (width + kKeptGroup - 1) / kKeptGroup;
+    const int8_t* at = p.kept.codes + static_cast<size_t>(row) * width + col;
+    const u32x2 codes = VEC ? *reinterpret_cast<const u32x2*>(at) : load_codes(at, width - col);
+    return kept_values(codes, p.kept.exponents[row * groups + col / kKeptGroup]);
 }
 
 // 8 rows of a lane's 8 columns in a strip of 128 (lane (j, c): rows of its c), as
@@ -459,7 +443,7 @@ __device__ __forceinline__ void add_rows(const FewSide& p, int col, int n, int w
                                          float (&acc)[kFewRanks][8]) {
 #pragma unroll 4
     for (int i = wave; i < n; i += WAVES) {
-        const u32x4 v = piece_values(load_piece<VEC, KEPT>(p.x, list[i], col, p.width, true));
+        const u32x4 v = load_wide<VEC, KEPT>(p.x, list[i], col, p.width);
         float e[8];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {

@@ -100,6 +100,41 @@ __device__ __forceinline__ float weight_of(const Choice* given, int token, int t
     return sum;
 }
 
+// The decode table of ExTable (the same bytes), staged by 16-byte pieces in a row:
+// lanes that write both pieces of an entry, 32 bytes apart, take twice the banks' time,
+// which a call of few tokens feels. Piece q is half q % 2 of codebook entry q / 2 in
+// eight copies, or for k = 2 two entries of the pair table: (LUT[q / 2], LUT[2 q']) and
+// (LUT[q / 2], LUT[2 q' + 1]), q' = q % 2048.
+template <int K>
+struct LayerTable {
+    static constexpr int floats = ExTable<K>::Table::floats, n = floats / 4 / kExThreads;
+    static_assert(n * 4 * kExThreads == floats && floats == 8 * kLutEntries, "whole pieces per thread");
+    float a[n];
+    floatx2 b[K == 2 ? 4 : 1];
+
+    __device__ __forceinline__ void fetch(const float* lut) {
+        using gf32 = const __attribute__((address_space(1))) float*;
+        using gf32x2 = const __attribute__((address_space(1))) floatx2*;
+        gf32 l = (gf32)lut;  // opaque, or the loads sink to their use
+        asm volatile("" : "+s"(l));
+#pragma unroll
+        for (int i = 0; i < n; ++i) a[i] = l[threadIdx.x / 2 + kExThreads / 2 * i];
+        if constexpr (K == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = reinterpret_cast<gf32x2>(l)[threadIdx.x + kExThreads * i];
+        }
+    }
+    __device__ __forceinline__ void store(float* __restrict__ tab) const {
+        floatx4* dst = reinterpret_cast<floatx4*>(tab) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float v = a[i];
+            if constexpr (K == 2) dst[kExThreads * i] = floatx4{v, b[i % 4].x, v, b[i % 4].y};
+            else dst[kExThreads * i] = floatx4{v, v, v, v};
+        }
+    }
+};
+
 // ---- operand order of h ---------------------------------------------------------
 
 // h of the chosen expert number `at` in the order that the down product reads:
@@ -163,7 +198,7 @@ __device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
 template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
-    __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
+    __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ float parts[kUpPartFloats];
     __shared__ Chosen chosen;
     __shared__ Choice given[kMaxSlots];
@@ -179,8 +214,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     }
     if (blockIdx.x == 0)
         for (int i = tid; i < p.strips; i += kExThreads) p.arrived[i] = 0;
-    typename ExTable<K>::Table::Src src;
-    ExTable<K>::Table::fetch(src, p.lut);
+    LayerTable<K> table;
+    table.fetch(p.lut);
     const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int nb = p.hidden / kT, per = p.per, all = live * per;
     const int share = all / static_cast<int>(gridDim.x), rest = all - share * static_cast<int>(gridDim.x);
@@ -248,7 +283,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         if (s >= p.tokens * p.top_k) continue;
         given[s] = {slots.id[i], weight[i]};
     }
-    ExTable<K>::Table::store(src, tab);
+    table.store(tab);
     __syncthreads();
     auto one = [&] {
         constexpr int D = kAhead;
@@ -457,10 +492,14 @@ __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int str
         }
         return;
     }
-    // parts in strips: [strip][way][token][COLS]
-    float* parts = p.partial + static_cast<size_t>(strip) * p.ways * n;
-    for (int i = tid; i < n; i += kExThreads)
-        __hip_atomic_store(parts + way * n + i, sum_of(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // parts in strips, two columns a word: [strip][way][token][COLS]
+    uint64_t* parts = reinterpret_cast<uint64_t*>(p.partial + static_cast<size_t>(strip) * p.ways * n);
+    auto pair_of = [](float a, float b) {
+        return static_cast<uint64_t>(__float_as_uint(a)) | static_cast<uint64_t>(__float_as_uint(b)) << 32;
+    };
+    for (int i = tid; i < n / 2; i += kExThreads)
+        __hip_atomic_store(parts + way * (n / 2) + i, pair_of(sum_of(2 * i), sum_of(2 * i + 1)), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     __shared__ uint32_t before;
@@ -468,19 +507,26 @@ __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int str
         before = __hip_atomic_fetch_add(p.arrived + strip, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (before != static_cast<uint32_t>(p.ways) - 1) return;
-    for (int i = tid; i < n; i += kExThreads) {
-        float v = 0.f;
-        for (int w0 = 0; w0 < p.ways; w0 += 8) {
-            float q[8];
+    constexpr int kAtOnce = 16;  // a strip of 128 columns of 2048 has 16 parts
+    for (int i = tid; i < n / 2; i += kExThreads) {
+        float v0 = 0.f, v1 = 0.f;
+        for (int w0 = 0; w0 < p.ways; w0 += kAtOnce) {
+            uint64_t q[kAtOnce];
 #pragma unroll
-            for (int w = 0; w < 8; ++w)
-                q[w] = __hip_atomic_load(parts + min(w0 + w, p.ways - 1) * n + i, __ATOMIC_RELAXED,
+            for (int w = 0; w < kAtOnce; ++w)
+                q[w] = __hip_atomic_load(parts + min(w0 + w, p.ways - 1) * (n / 2) + i, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) v += w0 + w < p.ways ? q[w] : 0.f;
+            for (int w = 0; w < kAtOnce; ++w) {
+                const bool there = w0 + w < p.ways;
+                v0 += there ? __uint_as_float(static_cast<uint32_t>(q[w])) : 0.f;
+                v1 += there ? __uint_as_float(static_cast<uint32_t>(q[w] >> 32)) : 0.f;
+            }
         }
-        const int col = col0 + i % COLS;
-        if (col < p.hidden) p.out[(i / COLS) * p.hidden + col] = round_bf16(v);
+        // hidden is a multiple of 256: both columns are there
+        const int col = col0 + 2 * i % COLS;
+        if (col < p.hidden)
+            *reinterpret_cast<uint32_t*>(p.out + (2 * i / COLS) * p.hidden + col) = pack_bf16(v0, v1);
     }
 }
 
@@ -515,13 +561,13 @@ template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     constexpr int G = kDownGroups;
-    __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
+    __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
-    typename ExTable<K>::Table::Src src;
-    ExTable<K>::Table::fetch(src, p.lut);
+    LayerTable<K> table;
+    table.fetch(p.lut);
     const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int strip = blockIdx.x / p.ways, way = blockIdx.x % p.ways, nb = p.inter / kT;
     const int64_t tasks = static_cast<int64_t>(live) * nb;
@@ -551,7 +597,7 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
                 for (int m = 0; m < MT; ++m) q.a[m][s] = ha[(s * MT + m) * kWave];
         },
         [&] {
-            ExTable<K>::Table::store(src, tab);
+            table.store(tab);
             __syncthreads();
         },
         [&](const Work& q) {
@@ -582,13 +628,13 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
 template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
     constexpr int CL = 8;
-    __shared__ __attribute__((aligned(16))) float tab[ExTable<K>::Table::floats];
+    __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
-    typename ExTable<K>::Table::Src src;
-    ExTable<K>::Table::fetch(src, p.lut);
+    LayerTable<K> table;
+    table.fetch(p.lut);
     const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int strip = blockIdx.x / p.ways, way = blockIdx.x % p.ways, steps = h_pieces(p.inter);
     const int64_t tasks = static_cast<int64_t>(live) * steps;
@@ -635,7 +681,7 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
             }
         },
         [&] {
-            ExTable<K>::Table::store(src, tab);
+            table.store(tab);
             __syncthreads();
         },
         [&](const Work& q) {
