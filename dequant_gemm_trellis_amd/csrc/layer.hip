@@ -249,8 +249,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         const uint32_t* up = gate + static_cast<uint64_t>(p.inter) * p.lay.row_words;
         const float* sg = p.scales + static_cast<size_t>(e) * (2 * p.inter) + col0;
         const int row = min(j & 7, p.inter - 1 - col0);
-        load_run64<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words), 3 - c,
-                      words);
+        load_run64_words<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words),
+                            3 - c, words);
         scale = sg[j < 8 ? row : row + p.inter];
     };
     floatx4 acc[kChunk][MT] = {};
@@ -301,17 +301,22 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         }
         const int next_at = na, next_in = ni;
         Gathered<pair> v[D + 1];
-        static_for<0, D>([&](auto ic) { v[decltype(ic)::value] = gather_tab<K, decltype(ic)::value, pair, rep>(w[0], tab); });
+        // operands 7 to 0: the word behind a run, its neighbour's first, is in the last
+        static_for<0, D>([&](auto ic) {
+            constexpr int A = decltype(ic)::value;
+            v[A] = gather_tab<K, 7 - A, pair, rep>(w[0], tab);
+        });
         static_for<0, kChunk>([&](auto gc) {
             constexpr int g = decltype(gc)::value;
             if (g >= n) return;
+            w[g][2 * K] = next_run_word(w[g][0]);
             static_for<0, 8>([&](auto ic) {
-                constexpr int S = decltype(ic)::value, A = S + D, i = 8 * g + S;
+                constexpr int I = decltype(ic)::value, S = 7 - I, A = I + D, i = 8 * g + I;
                 __builtin_amdgcn_s_setprio(2);
                 if constexpr (A < 8) {
-                    v[(i + D) % (D + 1)] = gather_tab<K, A, pair, rep>(w[g], tab);
+                    v[(i + D) % (D + 1)] = gather_tab<K, 7 - A, pair, rep>(w[g], tab);
                 } else if constexpr (g + 1 < kChunk) {
-                    if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, A - 8, pair, rep>(w[g + 1], tab);
+                    if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, 15 - A, pair, rep>(w[g + 1], tab);
                 }
                 __builtin_amdgcn_s_setprio(0);
                 const u32x4 f = pack_fragment(v[i % (D + 1)], sc[g]);
@@ -587,7 +592,7 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
             const int e = __builtin_amdgcn_readfirstlane(chosen.expert[at]);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                load_run64<K>(p.codes + e * p.words + block_word<K>(p.lay, rows[g], b), 3 - c, q.w[g]);
+                load_run64_words<K>(p.codes + e * p.words + block_word<K>(p.lay, rows[g], b), 3 - c, q.w[g]);
                 q.sc[g] = p.scales[static_cast<size_t>(e) * p.hidden + rows[g]];
             }
             const u32x4* ha = h + (static_cast<size_t>(at) * nb + b) * 8 * MT * kWave;
@@ -600,13 +605,15 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
             table.store(tab);
             __syncthreads();
         },
-        [&](const Work& q) {
+        [&](Work& q) {
             Gathered<pair> v[2];
-            v[0] = gather_tab<K, 0, pair, rep>(q.w[0], tab);
+            v[0] = gather_tab<K, 7, pair, rep>(q.w[0], tab);
+#pragma unroll
+            for (int g = 0; g < G; ++g) q.w[g][2 * K] = next_run_word(q.w[g][0]);
             static_for<0, 8 * G>([&](auto ic) {
-                constexpr int i = decltype(ic)::value, S = i / G, g = i % G, n = i + 1;
+                constexpr int i = decltype(ic)::value, S = 7 - i / G, g = i % G, n = i + 1;
                 __builtin_amdgcn_s_setprio(2);
-                if constexpr (n < 8 * G) v[n & 1] = gather_tab<K, n / G, pair, rep>(q.w[n % G], tab);
+                if constexpr (n < 8 * G) v[n & 1] = gather_tab<K, 7 - n / G, pair, rep>(q.w[n % G], tab);
                 __builtin_amdgcn_s_setprio(0);
                 const u32x4 f = pack_fragment(v[i & 1], q.sc[g]);
 #pragma unroll
