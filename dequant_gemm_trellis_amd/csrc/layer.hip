@@ -244,14 +244,15 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
                 a[m][s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
     };
     // a unit's rows are a uniform address for gate and up plus a lane's offset
-    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale) {
+    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale,
+                          bool other) {  // another unit than the words' last
         const uint32_t* gate = p.codes + e * p.words + block_word<K>(p.lay, col0, b);
         const uint32_t* up = gate + static_cast<uint64_t>(p.inter) * p.lay.row_words;
         const float* sg = p.scales + static_cast<size_t>(e) * (2 * p.inter) + col0;
         const int row = min(j & 7, p.inter - 1 - col0);
         load_run64_words<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words),
                             3 - c, words);
-        scale = sg[j < 8 ? row : row + p.inter];
+        if (other) scale = sg[j < 8 ? row : row + p.inter];
     };
     floatx4 acc[kChunk][MT] = {};
     // the wave's place in its team's units and blocks, and unit u's expert and columns.
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         }
 #pragma unroll
         for (int g = 0; g < kChunk; ++g)
-            load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g]);
+            load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
         load_x(b);
     }
 #pragma unroll
@@ -327,7 +328,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
             // first, and a wait is for all loads before
             if (reload && g + 1 == n) load_x(next);
             if (nu + g < end)
-                load_codes(__builtin_amdgcn_readfirstlane(chosen.expert[na]), ni * kUnitCols, next, w[g], sc[g]);
+                load_codes(__builtin_amdgcn_readfirstlane(chosen.expert[na]), ni * kUnitCols, next, w[g], sc[g],
+                           nu != u);
             if (++ni == per) {
                 ni = 0;
                 ++na;
