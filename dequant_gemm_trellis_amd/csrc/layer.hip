@@ -1,5 +1,5 @@
 // A whole layer of experts for few tokens (trellis_experts_mlp):
-//   h_e[m] = bf16( w_e[m] silu(Wg_e x[m]) (Wu_e x[m]) ),
+//   h_e[m] = w_e[m] silu(Wg_e x[m]) (Wu_e x[m]),
 //   out[m] = bf16( sum over the experts e that m chose of Wd_e h_e[m] ).
 //
 // With few tokens nearly all work is decoding, and a decoded operand meets 16
@@ -28,6 +28,7 @@ constexpr int kUnitCols = 8;  // columns of h per unit: 8 gate and 8 up rows
 constexpr int kChunk = 4;     // units of a wave at a time
 constexpr int kUpPartFloats = 4096;  // 16 columns of 32 tokens of 8 waves
 constexpr int kAhead = 2;     // operands whose codebook values are read ahead
+constexpr int kHalvedTokens = 8;  // up to which h is held as two bf16 parts
 constexpr int kMeet = 2;      // what a meeting of units costs, in quarter rounds of blocks
 
 // ---- the chosen experts -------------------------------------------------------
@@ -171,8 +172,23 @@ struct UpArgs {
     int round, meet;  // units that meet in LDS at once, and what a chunk's meetings cost
 };
 
-__device__ __forceinline__ uint16_t h_value(float weight, float g, float u) {
-    return round_bf16(weight * (g / (1.f + expf(-g)) * u));
+__device__ __forceinline__ float h_value(float weight, float g, float u) {
+    return weight * (g / (1.f + expf(-g)) * u);
+}
+
+// Up to kHalvedTokens tokens leave half of a 16-row operand free: h goes there as two
+// bf16 parts, the upper 8 bits of its mantissa (cut off) and the rest rounded, token m's
+// in rows m and m + 8, at no cost. With more tokens it is rounded to bf16: half a step,
+// about as much as the rounding of the result (a relative error of 2.3e-3 against 1.7e-3).
+// The parts have one sign and are not zero (nor h itself: then the lower one is 2^-24 of
+// the upper), so that an infinite weight gives the infinity that it gives h.
+struct Halves {
+    uint16_t upper, lower;
+};
+__device__ __forceinline__ Halves halves_of(float h) {
+    const float upper = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u), rest = h - upper;
+    const float lower = !__builtin_isfinite(h) ? upper : rest == 0.f ? upper * 0x1p-24f : rest;
+    return {static_cast<uint16_t>(__float_as_uint(upper) >> 16), round_bf16(lower)};
 }
 
 // How the eight waves share a workgroup's units: 2^w of them a unit's blocks, in
@@ -340,8 +356,16 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         at = next_at;
         in = next_in;
     };
-    auto put = [&](int expert, int col, int token, uint16_t v) {
-        p.h[h_at<MT>(expert, h_pieces(p.inter), p.axis_down, col, token)] = col < p.inter ? v : uint16_t{0};
+    auto put = [&](int expert, int col, int token, float v) {
+        if (col >= p.inter) v = 0.f;
+        uint16_t* o = p.h + h_at<MT>(expert, h_pieces(p.inter), p.axis_down, col, token);
+        if (MT == 1 && p.tokens <= kHalvedTokens) {
+            const Halves parts = halves_of(v);
+            o[0] = parts.upper;
+            o[8 * kHalvedTokens] = parts.lower;  // 8 lanes on
+        } else {
+            o[0] = round_bf16(v);
+        }
     };
     // h of the chunk from `from` on: of a whole unit per wave from registers (lanes j
     // and j + 8 hold its gate and up; lane l the weight of token l) ...
@@ -467,20 +491,45 @@ struct Sums {
     }
 };
 
-// The waves' sums of a strip of COLS columns, in wave order, are the workgroup's part:
-// each(f) gives f(token, column, value). `sums` takes the table's place. The last
+// The rows of the operand that hold the tokens of a mask.
+__device__ __forceinline__ uint32_t rows_of(const DownArgs& p, uint32_t mask) {
+    return p.tokens <= kHalvedTokens ? mask | mask << kHalvedTokens : mask;
+}
+
+// The waves' sums of a strip of COLS columns, in wave order, are the workgroup's part; a
+// lane's column n is at(n). `sums` takes the table's place. The last
 // workgroup of a strip to arrive adds the parts, in their order, whichever it is. Parts
 // and arrivals are device-scope accesses, which no die's L2 keeps to itself, and a wave
 // waits until its parts are in memory before its workgroup arrives: fences instead,
 // which write a whole L2 back, took 35 to 50 us of a call, a kernel of its own for the
 // sums 2.4 to 4.8 us and the host's launch.
-template <int COLS, typename F>
-__device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way, F&& each) {
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+template <int COLS, int N, int MT, typename F>
+__device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way,
+                                         const floatx4 (&total)[N][MT], F&& at) {
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = (tid & 63) >> 4;
     __syncthreads();  // the table is read
-    each([&](int token, int col, float v) {
-        if (token < p.tokens) sums[(wave * p.tokens + token) * COLS + col] = v;
-    });
+    const bool halved = MT == 1 && p.tokens <= kHalvedTokens;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (16 * m + i >= p.tokens) continue;  // nor any lane's
+            const int token = 16 * m + 4 * c + i;
+            float v[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                v[n] = total[n][m][i];
+                if (halved) {  // row token + 8 is 32 lanes on
+                    const uint32_t bits = __float_as_uint(v[n]);
+                    v[n] += __uint_as_float(__builtin_amdgcn_permlane32_swap(bits, bits, false, false)[1]);
+                }
+            }
+            if (token < p.tokens) {
+                float* o = sums + (wave * p.tokens + token) * COLS;
+#pragma unroll
+                for (int n = 0; n < N; ++n) o[at(n)] = v[n];
+            }
+        }
     __syncthreads();
     const int n = p.tokens * COLS;
     auto sum_of = [&](int i) {
@@ -623,15 +672,8 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
                     sums.now[g][m] = mfma16x16x32(as_bf16x8(q.a[m][S]), as_bf16x8(f), sums.now[g][m]);
             });
         },
-        [&](int at) { sums.close(chosen.mask[chosen.expert[at]], c); });
-    put_part<kDownCols1>(tab, p, strip, way, [&](auto&& f) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f(16 * m + 4 * c + i, 16 * g + j, sums.total[g][m][i]);
-    });
+        [&](int at) { sums.close(rows_of(p, chosen.mask[chosen.expert[at]]), c); });
+    put_part<kDownCols1>(tab, p, strip, way, sums.total, [&](int n) { return 16 * n + j; });
 }
 
 template <int K, int MT>
@@ -709,15 +751,8 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
                     sums.now[e][m] = mfma16x16x32(as_bf16x8(q.a[m]), as_bf16x8(f), sums.now[e][m]);
             });
         },
-        [&](int at) { sums.close(chosen.mask[chosen.expert[at]], c); });
-    put_part<kDownCols0>(tab, p, strip, way, [&](auto&& f) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < CL; ++e)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f(16 * m + 4 * c + i, CL * j + e, sums.total[e][m][i]);
-    });
+        [&](int at) { sums.close(rows_of(p, chosen.mask[chosen.expert[at]]), c); });
+    put_part<kDownCols0>(tab, p, strip, way, sums.total, [&](int n) { return CL * j + n; });
 }
 
 // ---- launches ---------------------------------------------------------------------

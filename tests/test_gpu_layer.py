@@ -5,8 +5,9 @@ Bounds, value by value, with eps = 2^-24 (float32) and half a bf16 step 2^-8 of 
 value: a product's float32 sum of n terms is off by at most n eps times the sum of
 the terms' magnitudes (in any order); g's error reaches h by at most 1.1 w |u|
 (silu's slope is below 1.1), u's by w |silu(g)|; h's own float32 work (exp,
-division, three products) adds 16 eps of it, and its rounding half a step; out has
-all that times |Wd|, its own sums, and half a step.
+division, three products) adds 16 eps of it, and its rounding half a step (up to 8
+tokens: the half step 2^-8 of what is left behind its upper 8 bits, 2^-7 of it); out
+has all that times |Wd|, its own sums, and half a step.
 """
 import numpy as np
 import pytest
@@ -67,7 +68,7 @@ class Layer:
         """(out, bound) in float64."""
         tokens = len(self.ids)
         out = torch.zeros((tokens, self.hidden), dtype=torch.float64)
-        bound = torch.zeros_like(out)
+        bound, size_of_sums = torch.zeros_like(out), torch.zeros_like(out)
         for e in range(self.experts):
             mine = self.ids == e
             m = mine.any(1).nonzero()[:, 0]
@@ -81,11 +82,12 @@ class Layer:
             dg, du = size.chunk(2, dim=1)
             silu = g * torch.sigmoid(g)
             h = w * silu * u
-            off = w.abs() * (1.1 * (u.abs() + du) * dg + silu.abs() * du) + h.abs() * (HALF + 16 * EPS)
+            off = w.abs() * (1.1 * (u.abs() + du) * dg + silu.abs() * du) + h.abs() * ((HALF if tokens > 8 else 2.0 ** -15) + 16 * EPS)
             out[m] += h @ wd.T
-            bound[m] += (off + (self.inter + 8) * EPS * h.abs()) @ wd.abs().T
+            bound[m] += (off + 2 * (self.inter + 8) * EPS * h.abs()) @ wd.abs().T
+            size_of_sums[m] += h.abs() @ wd.abs().T
         # the experts' sums meet in float32, and the whole is rounded once
-        return out, (bound + 40 * EPS * bound / HALF) * (1 + HALF) + HALF * out.abs()
+        return out, (bound + 40 * EPS * size_of_sums) * (1 + HALF) + HALF * out.abs()
 
     def cuda(self, weighted=True):
         def dev(m):
