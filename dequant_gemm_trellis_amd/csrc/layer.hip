@@ -291,8 +291,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         }
 #pragma unroll
         for (int g = 0; g < kChunk; ++g)
-            load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
-        load_x(b);
+            if (g == 0 || first + g < end)
+                load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
     }
 #pragma unroll
     for (int i = 0; i < kSlotsPerThread; ++i) {
@@ -302,6 +302,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     }
     table.store(tab);
     __syncthreads();
+    load_x(b);
     auto one = [&] {
         constexpr int D = kAhead;
         int nu = u, next = b + ways;

@@ -683,7 +683,7 @@ def _new_kept(like: torch.Tensor, rows: int, width: int) -> Kept:
 
 def keep(x, kept: Kept | None = None, stream=None) -> Kept:
     """bf16 rows x [rows, width] put away in 8 bits: 32 adjacent values of a row share
-    an exponent, and each is off by at most 1/256 of the group's largest magnitude."""
+    an exponent, and each is off by at most 1/128 of the group's largest magnitude."""
     rows, width = _dims("x", x, 2)
     dev = _device(x)
     _want("x", x, torch.bfloat16, (rows, width), dev)

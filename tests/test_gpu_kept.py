@@ -61,7 +61,7 @@ def test_keep_and_restore(gpu_lib, rows, width):
     assert torch.equal(kept.codes.cpu(), codes)
     back = gpu_lib.restore(kept)
     assert torch.equal(back.cpu(), ref.restore(codes, exponents))
-    # half a step of 2^(E - 133), and 1/256 of the largest magnitude (where E >= 1)
+    # half a step of 2^(E - 133), 1/128 of the largest magnitude where E >= 1
     e = exponents.double().repeat_interleave(32, dim=1)[:, :width]
     assert bool(((back.cpu().double() - x.double()).abs() <= torch.exp2(e - 134)).all())
 
