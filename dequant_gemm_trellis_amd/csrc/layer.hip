@@ -208,12 +208,72 @@ __device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
     return best;
 }
 
+// The choices with their weights into LDS (a barrier follows before they are read).
+__device__ __forceinline__ void stage_choices(Choice* given, const Slots& slots, const UpArgs& p) {
+#pragma unroll
+    for (int i = 0; i < kSlotsPerThread; ++i) {
+        const int s = threadIdx.x + i * kExThreads;
+        if (s >= p.tokens * p.top_k) continue;
+        given[s] = {slots.id[i], p.weights ? p.weights[s] : 1.f};
+    }
+}
+
+// The sums of n units over a block of 256 inputs: their words and scales in registers,
+// the tokens' operands in `a`. after(unit) is called as soon as a unit's words and, if it
+// is the last, the operands are done with.
+template <int K, int MT, typename After>
+__device__ __forceinline__ void decode_units(uint32_t (&w)[kChunk][2 * K + 1], const float (&sc)[kChunk],
+                                             const u32x4 (&a)[MT][8], floatx4 (&acc)[kChunk][MT], int n,
+                                             const float* tab, After&& after) {
+    constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
+    constexpr int D = kAhead;
+    Gathered<pair> v[D + 1];
+    // operands 7 to 0: the word behind a run, its neighbour's first, is in the last
+    static_for<0, D>([&](auto ic) {
+        constexpr int A = decltype(ic)::value;
+        v[A] = gather_tab<K, 7 - A, pair, rep>(w[0], tab);
+    });
+    static_for<0, kChunk>([&](auto gc) {
+        constexpr int g = decltype(gc)::value;
+        if (g >= n) return;
+        w[g][2 * K] = next_run_word(w[g][0]);
+        static_for<0, 8>([&](auto ic) {
+            constexpr int I = decltype(ic)::value, S = 7 - I, A = I + D, i = 8 * g + I;
+            __builtin_amdgcn_s_setprio(2);
+            if constexpr (A < 8) {
+                v[(i + D) % (D + 1)] = gather_tab<K, 7 - A, pair, rep>(w[g], tab);
+            } else if constexpr (g + 1 < kChunk) {
+                if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, 15 - A, pair, rep>(w[g + 1], tab);
+            }
+            __builtin_amdgcn_s_setprio(0);
+            const u32x4 f = pack_fragment(v[i % (D + 1)], sc[g]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[g][m] = mfma16x16x32(as_bf16x8(a[m][S]), as_bf16x8(f), acc[g][m]);
+        });
+        after(gc);
+    });
+}
+
+// A unit's words of block b and its scales: its rows are a uniform address for gate and
+// up plus a lane's offset.
+template <int K>
+__device__ __forceinline__ void load_unit(const UpArgs& p, int e, int col0, int b, uint32_t (&words)[2 * K + 1],
+                                          float& scale, bool other) {  // another unit than the words' last
+    const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
+    const uint32_t* gate = p.codes + e * p.words + block_word<K>(p.lay, col0, b);
+    const uint32_t* up = gate + static_cast<uint64_t>(p.inter) * p.lay.row_words;
+    const float* sg = p.scales + static_cast<size_t>(e) * (2 * p.inter) + col0;
+    const int row = min(j & 7, p.inter - 1 - col0);
+    load_run64_words<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words),
+                        3 - c, words);
+    if (other) scale = sg[j < 8 ? row : row + p.inter];
+}
+
 // This workgroup's units. A wave takes `kChunk` units of its team at a time through
 // its blocks: the tokens' operands of a block serve all of them. A unit's next words
 // are loaded as soon as its last ones are decoded.
 template <int K, int MT>
 __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
-    constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ float parts[kUpPartFloats];
     __shared__ Chosen chosen;
@@ -222,12 +282,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, c = lane >> 4;
     const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
-    float weight[kSlotsPerThread];
-#pragma unroll
-    for (int i = 0; i < kSlotsPerThread; ++i) {
-        weight[i] = 1.f;
-        if (p.weights) weight[i] = p.weights[min(tid + i * kExThreads, p.tokens * p.top_k - 1)];
-    }
+    stage_choices(given, slots, p);
     if (blockIdx.x == 0)
         for (int i = tid; i < p.strips; i += kExThreads) p.arrived[i] = 0;
     LayerTable<K> table;
@@ -259,16 +314,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
             for (int s = 0; s < 8; ++s)
                 a[m][s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
     };
-    // a unit's rows are a uniform address for gate and up plus a lane's offset
-    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale,
-                          bool other) {  // another unit than the words' last
-        const uint32_t* gate = p.codes + e * p.words + block_word<K>(p.lay, col0, b);
-        const uint32_t* up = gate + static_cast<uint64_t>(p.inter) * p.lay.row_words;
-        const float* sg = p.scales + static_cast<size_t>(e) * (2 * p.inter) + col0;
-        const int row = min(j & 7, p.inter - 1 - col0);
-        load_run64_words<K>((j < 8 ? gate : up) + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.lay.row_words),
-                            3 - c, words);
-        if (other) scale = sg[j < 8 ? row : row + p.inter];
+    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale, bool other) {
+        load_unit<K>(p, e, col0, b, words, scale, other);
     };
     floatx4 acc[kChunk][MT] = {};
     // the wave's place in its team's units and blocks, and unit u's expert and columns.
@@ -294,17 +341,10 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
             if (g == 0 || first + g < end)
                 load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
     }
-#pragma unroll
-    for (int i = 0; i < kSlotsPerThread; ++i) {
-        const int s = tid + i * kExThreads;
-        if (s >= p.tokens * p.top_k) continue;
-        given[s] = {slots.id[i], weight[i]};
-    }
     table.store(tab);
     __syncthreads();
     load_x(b);
     auto one = [&] {
-        constexpr int D = kAhead;
         int nu = u, next = b + ways;
         if (next >= nb) {
             next = way;
@@ -318,29 +358,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
             ++na;
         }
         const int next_at = na, next_in = ni;
-        Gathered<pair> v[D + 1];
-        // operands 7 to 0: the word behind a run, its neighbour's first, is in the last
-        static_for<0, D>([&](auto ic) {
-            constexpr int A = decltype(ic)::value;
-            v[A] = gather_tab<K, 7 - A, pair, rep>(w[0], tab);
-        });
-        static_for<0, kChunk>([&](auto gc) {
+        decode_units<K>(w, sc, a, acc, n, tab, [&](auto gc) {
             constexpr int g = decltype(gc)::value;
-            if (g >= n) return;
-            w[g][2 * K] = next_run_word(w[g][0]);
-            static_for<0, 8>([&](auto ic) {
-                constexpr int I = decltype(ic)::value, S = 7 - I, A = I + D, i = 8 * g + I;
-                __builtin_amdgcn_s_setprio(2);
-                if constexpr (A < 8) {
-                    v[(i + D) % (D + 1)] = gather_tab<K, 7 - A, pair, rep>(w[g], tab);
-                } else if constexpr (g + 1 < kChunk) {
-                    if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, 15 - A, pair, rep>(w[g + 1], tab);
-                }
-                __builtin_amdgcn_s_setprio(0);
-                const u32x4 f = pack_fragment(v[i % (D + 1)], sc[g]);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) acc[g][m] = mfma16x16x32(as_bf16x8(a[m][S]), as_bf16x8(f), acc[g][m]);
-            });
             // the next block's operands before the last unit's words: they are waited for
             // first, and a wait is for all loads before
             if (reload && g + 1 == n) load_x(next);
@@ -450,6 +469,135 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         for (int g = 0; g < kChunk; ++g)
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[g][m] = floatx4{};
+    }
+}
+
+// Many tokens of which each expert has few: a tile is up to 16 tokens of one expert, of
+// its own operands, where all tokens would take two. A wave takes units of its own; none
+// waits for another. h is stored for two operands of tokens, as the other kernel does.
+struct Tiles {
+    uint16_t tile[kMaxGroups + kMaxSlots / 17];  // 2 (number of the chosen expert) + (tokens 16 ...)
+};
+
+// Every wave writes the whole list, as find_chosen does.
+__device__ __forceinline__ int find_tiles(Tiles& s, const Chosen& chosen, int live) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int at0 = 0; at0 < live; at0 += kWave) {
+        const int at = at0 + lane, tokens = at < live ? __popc(chosen.mask[chosen.expert[at]]) : 0;
+        const uint64_t one = __ballot(tokens > 0), two = __ballot(tokens > 16), below = (1ull << lane) - 1;
+        const int first = n + __popcll(one & below) + __popcll(two & below);
+        if (tokens > 0) s.tile[first] = static_cast<uint16_t>(2 * at);
+        if (tokens > 16) s.tile[first + 1] = static_cast<uint16_t>(2 * at + 1);
+        n += __popcll(one) + __popcll(two);
+    }
+    wave_lds_sync();
+    return n;
+}
+
+// The place of the set bit number n (from 0) of a mask that has it.
+__device__ __forceinline__ int set_bit(uint32_t mask, int n) {
+    int at = 0;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) {
+        const int below = __popc((mask >> at) & ((1u << w) - 1u));
+        if (n >= below) {
+            n -= below;
+            at += w;
+        }
+    }
+    return at;
+}
+
+template <int K>
+__global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
+    __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
+    __shared__ Chosen chosen;
+    __shared__ Tiles tiles;
+    __shared__ Choice given[kMaxSlots];
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, c = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Slots slots = load_slots(p.ids, p.tokens * p.top_k);
+    stage_choices(given, slots, p);
+    if (blockIdx.x == 0)
+        for (int i = tid; i < p.strips; i += kExThreads) p.arrived[i] = 0;
+    LayerTable<K> table;
+    table.fetch(p.lut);
+    const int live = find_tiles(tiles, chosen, find_chosen(chosen, slots, p.inverse, p.experts));
+    table.store(tab);
+    __syncthreads();
+    const int nb = p.hidden / kT, per = p.per, waves = static_cast<int>(gridDim.x) * kExWaves;
+    // a workgroup's waves take units far apart, so that all workgroups have as many
+    const int64_t units = static_cast<int64_t>(live) * per;
+    const int turn = wave * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    int u = static_cast<int>(units * turn / waves);
+    const int end = static_cast<int>(units * (turn + 1) / waves);
+    if (u == end) return;
+
+    uint32_t w[kChunk][2 * K + 1];
+    float sc[kChunk];
+    u32x4 a[1][8];
+    int at = u / per, in = u - at * per, n, e, token, rows;
+    const uint16_t* x;
+    // the tile of the chunk at u: its expert, rows and (lane j) the row's token
+    auto enter = [&] {
+        n = min(min(kChunk, end - u), per - in);
+        const int tile = tiles.tile[at];
+        e = __builtin_amdgcn_readfirstlane(chosen.expert[tile >> 1]);
+        const uint32_t mask = chosen.mask[e];
+        const int skip = 16 * (tile & 1);
+        rows = min(16, __popc(mask) - skip);
+        token = set_bit(mask, skip + min(j, rows - 1));
+        x = p.x + static_cast<size_t>(token) * p.hidden + 64 * c;
+    };
+    auto load_x = [&](int b) {
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            a[0][s] = *reinterpret_cast<const u32x4*>(x + static_cast<size_t>(b) * kT + 8 * s);
+    };
+    auto load_first = [&] {  // block 0 of the chunk's units
+        load_x(0);
+        static_for<0, kChunk>([&](auto gc) {
+            constexpr int g = decltype(gc)::value;
+            if (g < n) load_unit<K>(p, e, (in + g) * kUnitCols, 0, w[g], sc[g], true);
+        });
+    };
+    enter();
+    load_first();
+    for (;;) {
+        floatx4 acc[kChunk][1] = {};
+        for (int b = 0; b < nb; ++b)
+            decode_units<K>(w, sc, a, acc, n, tab, [&](auto gc) {
+                constexpr int g = decltype(gc)::value;
+                if (b + 1 == nb) return;
+                if (g + 1 == n) load_x(b + 1);
+                load_unit<K>(p, e, (in + g) * kUnitCols, b + 1, w[g], sc[g], false);
+            });
+        const int done_at = tiles.tile[at] >> 1, done_in = in, done = n, done_rows = rows, done_token = token;
+        const float mine = weight_of(given, token, p.top_k, e);
+        u += n;
+        if (u < end) {
+            in += n;
+            if (in == per) {
+                in = 0;
+                ++at;
+            }
+            enter();
+            load_first();
+        }
+#pragma unroll
+        for (int g = 0; g < kChunk; ++g) {
+            if (g >= done) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 4 * c + i, t = __shfl(done_token, row), col = (done_in + g) * kUnitCols + j;
+                const float up = __shfl_xor(acc[g][0][i], 8), weight = __shfl(mine, row);
+                if (j < 8 && row < done_rows)
+                    p.h[h_at<2>(done_at, h_pieces(p.inter), p.axis_down, col, t)] =
+                        col < p.inter ? round_bf16(h_value(weight, acc[g][0][i], up)) : uint16_t{0};
+            }
+        }
+        if (u == end) return;
     }
 }
 
@@ -778,10 +926,16 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
     return p;
 }
 
+// More than 16 tokens as tiles where an expert has kListedTokens of them or fewer on
+// average (it may have two tiles), else all tokens in two operands.
+constexpr int kListedTokens = 8;
+
 template <int K>
 hipError_t launch_up(const UpArgs& p, hipStream_t st) {
-    return launch_kernel(p.tokens > 16 ? layer_up_kernel<K, 2> : layer_up_kernel<K, 1>, dim3(cu_count()),
-                         dim3(kExThreads), st, p);
+    auto kernel = p.tokens <= 16                                          ? layer_up_kernel<K, 1>
+                  : p.tokens * p.top_k <= kListedTokens * p.experts ? layer_up_listed_kernel<K>
+                                                                          : layer_up_kernel<K, 2>;
+    return launch_kernel(kernel, dim3(cu_count()), dim3(kExThreads), st, p);
 }
 
 template <int K>

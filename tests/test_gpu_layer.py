@@ -111,7 +111,8 @@ SIZES = [
     (9, 3, 5, 768, 512, 4, 2, 1), (31, 32, 40, 256, 9, 3, 3, 0), (3, 5, 1024, 256, 31, 2, 4, 0),
     (32, 1, 1, 512, 1, 2, 3, 0), (7, 2, 6, 2304, 256, 3, 4, 1), (24, 2, 3, 768, 100, 2, 2, 0),
     (13, 4, 15, 1280, 272, 4, 4, 0), (4, 1, 1, 1280, 1000, 3, 3, 0), (20, 1, 1, 1024, 768, 2, 4, 1),
-    (32, 8, 9, 8448, 40, 2, 3, 0),
+    (32, 8, 9, 8448, 40, 2, 3, 0), (32, 8, 64, 768, 256, 3, 3, 1), (18, 3, 200, 1280, 52, 4, 2, 0),
+    (32, 2, 8, 2048, 8, 2, 2, 0), (29, 1, 300, 256, 300, 3, 4, 0),
 ]
 
 
@@ -119,6 +120,18 @@ SIZES = [
 def test_layer(gpu_lib, size):
     say(f"layer {size}")
     p = Layer(1, *size)
+    check(gpu_lib.experts_mlp(*p.cuda()), *p.want())
+
+
+@pytest.mark.parametrize("popular", [16, 17, 25, 32])
+@pytest.mark.parametrize("k,axis,inter", [(2, 1, 256), (3, 0, 44), (4, 0, 3)])
+def test_one_expert_has_most(gpu_lib, popular, k, axis, inter):
+    """Many tokens of few per expert, but for one that 16, 17 or all of them chose: it
+    has one tile of tokens or two."""
+    say(f"layer, {popular} of 32 tokens for one expert, k={k}")
+    p = Layer(16, 32, 2, 24, 512, inter, k, k, axis)
+    p.ids[:, 0] = torch.where(torch.randperm(32, generator=torch.Generator().manual_seed(popular)) < popular, 5, -1)
+    p.ids[:, 1] = torch.arange(32) % 24
     check(gpu_lib.experts_mlp(*p.cuda()), *p.want())
 
 
@@ -155,7 +168,7 @@ def test_no_tokens(gpu_lib):
     assert gpu_lib.experts_mlp(*p.cuda()).shape == (0, 256)
 
 
-@pytest.mark.parametrize("size", [(6, 2, 8, 512, 100, 3, 3, 0), (20, 2, 8, 512, 256, 2, 4, 1)])
+@pytest.mark.parametrize("size", [(6, 2, 8, 512, 100, 3, 3, 0), (20, 2, 8, 512, 256, 2, 4, 1), (20, 3, 6, 512, 100, 2, 4, 0)])
 def test_not_finite_stays_where_it_is(gpu_lib, size):
     """NaN in one token's row, and an expert of infinite weights, reach only the tokens
     that have them."""
@@ -177,15 +190,15 @@ def test_not_finite_stays_where_it_is(gpu_lib, size):
     check(out[clean.cuda()], want[clean], bound[clean])
 
 
+@pytest.mark.parametrize("tokens", [5, 12, 20])
 @pytest.mark.parametrize("inter", [33, 300, 40])
-def test_infinite_last_row(gpu_lib, inter):
+def test_infinite_last_row(gpu_lib, inter, tokens):
     """The last stored row of a partial step may be infinite: its column of h makes
     infinities of it, and nothing makes NaN."""
-    p = Layer(7, 5, 2, 4, 256, inter, 3, 3, 0)
+    p = Layer(7, tokens, 2, 4, 256, inter, 3, 3, 0)
     say(f"layer, infinite last row, inter {inter}")
     p.down["scales"][:, inter - 1] = np.inf
     p.down["lut"][p.down["lut"] == 0] = 1.0
-    out = gpu_lib.experts_mlp(*p.cuda())
     # h of the last column: sums of infinities of both signs are NaN, so one expert each
     p.ids[:, 1] = -1
     out = gpu_lib.experts_mlp(*p.cuda())
