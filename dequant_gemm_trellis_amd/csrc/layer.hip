@@ -927,14 +927,19 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
 }
 
 // More than 16 tokens as tiles where an expert has kListedTokens of them or fewer on
-// average (it may have two tiles), else all tokens in two operands.
-constexpr int kListedTokens = 8;
+// average (one may have two tiles), else all tokens in two operands. The whole layer of
+// 2048 -> 768, us (tiles / all tokens), 32 tokens with 8 choices at k = 3: 64 experts (4
+// tokens each) 82 / 96, 32 experts 58 / 61, 24 experts 56 / 59, 16 experts 54 / 52 (k =
+// 2: 47 / 50); with 4 of 8 experts 39 / 33; one expert 39 / 27. Up to 16 tokens all are
+// one operand anyway: 62 / 62 for 64 experts, 36 / 34 for 16, 80 / 73 for 15 of 5120 ->
+// 1280, where the units are too few to give every wave its own.
+constexpr int kListedTokens = 12;
 
 template <int K>
 hipError_t launch_up(const UpArgs& p, hipStream_t st) {
-    auto kernel = p.tokens <= 16                                          ? layer_up_kernel<K, 1>
+    auto kernel = p.tokens <= 16                                    ? layer_up_kernel<K, 1>
                   : p.tokens * p.top_k <= kListedTokens * p.experts ? layer_up_listed_kernel<K>
-                                                                          : layer_up_kernel<K, 2>;
+                                                                    : layer_up_kernel<K, 2>;
     return launch_kernel(kernel, dim3(cu_count()), dim3(kExThreads), st, p);
 }
 
