@@ -219,12 +219,13 @@ __device__ __forceinline__ void stage_choices(Choice* given, const Slots& slots,
 }
 
 // The sums of n units over a block of 256 inputs: their words and scales in registers,
-// the tokens' operands in `a`. after(unit) is called as soon as a unit's words and, if it
-// is the last, the operands are done with.
-template <int K, int MT, typename After>
+// the tokens' operands in `a`. during(unit) is called when a unit's words are there and
+// its first operand is multiplied, after(unit) when they are done with, and the operands
+// behind the last.
+template <int K, int MT, typename During, typename After>
 __device__ __forceinline__ void decode_units(uint32_t (&w)[kChunk][2 * K + 1], const float (&sc)[kChunk],
                                              const u32x4 (&a)[MT][8], floatx4 (&acc)[kChunk][MT], int n,
-                                             const float* tab, After&& after) {
+                                             const float* tab, During&& during, After&& after) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
     constexpr int D = kAhead;
     Gathered<pair> v[D + 1];
@@ -239,16 +240,15 @@ __device__ __forceinline__ void decode_units(uint32_t (&w)[kChunk][2 * K + 1], c
         w[g][2 * K] = next_run_word(w[g][0]);
         static_for<0, 8>([&](auto ic) {
             constexpr int I = decltype(ic)::value, S = 7 - I, A = I + D, i = 8 * g + I;
-            __builtin_amdgcn_s_setprio(2);
             if constexpr (A < 8) {
                 v[(i + D) % (D + 1)] = gather_tab<K, 7 - A, pair, rep>(w[g], tab);
             } else if constexpr (g + 1 < kChunk) {
                 if (g + 1 < n) v[(i + D) % (D + 1)] = gather_tab<K, 15 - A, pair, rep>(w[g + 1], tab);
             }
-            __builtin_amdgcn_s_setprio(0);
             const u32x4 f = pack_fragment(v[i % (D + 1)], sc[g]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[g][m] = mfma16x16x32(as_bf16x8(a[m][S]), as_bf16x8(f), acc[g][m]);
+            if constexpr (I == 0) during(gc);
         });
         after(gc);
     });
@@ -307,15 +307,9 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
         x[m] = p.x + static_cast<size_t>(min(16 * m + j, p.tokens - 1)) * p.hidden + 64 * c;
-    auto load_x = [&](int b) {
+    auto load_x = [&](int b, u32x4 (&o)[8], int m = 0) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                a[m][s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
-    };
-    auto load_codes = [&](int e, int col0, int b, uint32_t (&words)[2 * K + 1], float& scale, bool other) {
-        load_unit<K>(p, e, col0, b, words, scale, other);
+        for (int s = 0; s < 8; ++s) o[s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
     };
     floatx4 acc[kChunk][MT] = {};
     // the wave's place in its team's units and blocks, and unit u's expert and columns.
@@ -339,11 +333,12 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
 #pragma unroll
         for (int g = 0; g < kChunk; ++g)
             if (g == 0 || first + g < end)
-                load_codes(__builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
+                load_unit<K>(p, __builtin_amdgcn_readfirstlane(e[g]), col0[g], b, w[g], sc[g], true);
     }
     table.store(tab);
     __syncthreads();
-    load_x(b);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) load_x(b, a[m], m);
     auto one = [&] {
         int nu = u, next = b + ways;
         if (next >= nb) {
@@ -358,19 +353,24 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
             ++na;
         }
         const int next_at = na, next_in = ni;
-        decode_units<K>(w, sc, a, acc, n, tab, [&](auto gc) {
-            constexpr int g = decltype(gc)::value;
-            // the next block's operands before the last unit's words: they are waited for
-            // first, and a wait is for all loads before
-            if (reload && g + 1 == n) load_x(next);
-            if (nu + g < end)
-                load_codes(__builtin_amdgcn_readfirstlane(chosen.expert[na]), ni * kUnitCols, next, w[g], sc[g],
-                           nu != u);
-            if (++ni == per) {
-                ni = 0;
-                ++na;
-            }
-        });
+        decode_units<K>(
+            w, sc, a, acc, n, tab, [](auto) {},
+            [&](auto gc) {
+                constexpr int g = decltype(gc)::value;
+                // the next block's operands before the last unit's words: they are waited
+                // for first, and a wait is for all loads before
+                if (reload && g + 1 == n) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) load_x(next, a[m], m);
+                }
+                if (nu + g < end)
+                    load_unit<K>(p, __builtin_amdgcn_readfirstlane(chosen.expert[na]), ni * kUnitCols, next, w[g],
+                                 sc[g], nu != u);
+                if (++ni == per) {
+                    ni = 0;
+                    ++na;
+                }
+            });
         u = nu;
         b = next;
         at = next_at;
@@ -550,13 +550,16 @@ __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
         token = set_bit(mask, skip + min(j, rows - 1));
         x = p.x + static_cast<size_t>(token) * p.hidden + 64 * c;
     };
-    auto load_x = [&](int b) {
+    auto load_x = [&](int b, u32x4 (&o)[8]) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-            a[0][s] = *reinterpret_cast<const u32x4*>(x + static_cast<size_t>(b) * kT + 8 * s);
+        for (int s = 0; s < 8; ++s) o[s] = *reinterpret_cast<const u32x4*>(x + static_cast<size_t>(b) * kT + 8 * s);
+    };
+    auto load_words = [&](auto gc, int b) {
+        constexpr int g = decltype(gc)::value;
+        load_unit<K>(p, e, (in + g) * kUnitCols, b, w[g], sc[g], false);
     };
     auto load_first = [&] {  // block 0 of the chunk's units
-        load_x(0);
+        load_x(0, a[0]);
         static_for<0, kChunk>([&](auto gc) {
             constexpr int g = decltype(gc)::value;
             if (g < n) load_unit<K>(p, e, (in + g) * kUnitCols, 0, w[g], sc[g], true);
@@ -564,15 +567,37 @@ __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
     };
     enter();
     load_first();
+    // The next block's words of a unit are loaded during the unit behind it, the last one's
+    // during the next block's first, and the operands ahead of both: a wait for words is
+    // for every load before, as some are under conditions, and none of them is younger
+    // than a unit's decoding then (the first product of 32 tokens of 64 experts 33.5 us; with
+    // the loads right behind a unit, as in the kernel for fewer tokens, 37.8; that one
+    // lost by this order, 49 to 56 us for 13 tokens of 15 experts 5120 -> 1280).
     for (;;) {
         floatx4 acc[kChunk][1] = {};
-        for (int b = 0; b < nb; ++b)
-            decode_units<K>(w, sc, a, acc, n, tab, [&](auto gc) {
-                constexpr int g = decltype(gc)::value;
-                if (b + 1 == nb) return;
-                if (g + 1 == n) load_x(b + 1);
-                load_unit<K>(p, e, (in + g) * kUnitCols, b + 1, w[g], sc[g], false);
-            });
+        for (int b = 0; b < nb; ++b) {
+            const bool more = b + 1 < nb;
+            u32x4 ahead[8];
+            decode_units<K>(
+                w, sc, a, acc, n, tab,
+                [&](auto gc) {
+                    constexpr int g = decltype(gc)::value;
+                    if constexpr (g == 0) {
+                        if (more) load_x(b + 1, ahead);
+                        static_for<1, kChunk>([&](auto lc) {
+                            if (b && decltype(lc)::value + 1 == n) load_words(lc, b);
+                        });
+                    } else if (more) {
+                        load_words(std::integral_constant<int, g - 1>{}, b + 1);
+                    }
+                },
+                [&](auto gc) {
+                    if (!more || decltype(gc)::value + 1 != n) return;
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) a[0][s] = ahead[s];
+                    if (n == 1) load_words(gc, b + 1);
+                });
+        }
         const int done_at = tiles.tile[at] >> 1, done_in = in, done = n, done_rows = rows, done_token = token;
         const float mine = weight_of(given, token, p.top_k, e);
         u += n;
