@@ -2,18 +2,24 @@
 //   h_e[m] = w_e[m] silu(Wg_e x[m]) (Wu_e x[m]),
 //   out[m] = bf16( sum over the experts e that m chose of Wd_e h_e[m] ).
 //
-// With few tokens nearly all work is decoding, and a decoded operand meets 16
-// rows in one matrix instruction at no cost. So no token is sorted or moved: every
-// expert that anyone chose is decoded once and multiplied with all tokens, and
-// what a token did not choose is left out of its sums (not multiplied by zero: an
-// infinite weight of another's expert must not reach it). The second product is
-// one long contraction over all chosen experts.
-//   up: units of 8 gate and 8 up rows of an expert, dealt evenly to the workgroups;
-//     a unit's blocks go to the eight waves in turn, whose sums meet in LDS, where h
-//     is formed. h is stored in the second product's operand order.
+// With few tokens nearly all work is decoding, through random reads of a codebook table
+// in LDS, which bound it; a decoded operand meets 16 rows in one matrix instruction at no
+// cost. So up to 16 tokens none is sorted or moved: every expert that anyone chose is
+// decoded once and multiplied with all tokens, and what a token did not choose is left
+// out of its sums (not multiplied by zero: an infinite weight of another's expert must
+// not reach it). The second product is one long contraction over all chosen experts.
+//   up: units of 8 gate and 8 up rows of an expert, dealt evenly to the workgroups,
+//     whose waves share units or a unit's blocks, as takes fewer rounds; several waves'
+//     sums meet in LDS. h is stored in the second product's operand order. More than 16
+//     tokens go as tiles of an expert's own, if there is work for them.
 //   down: a workgroup takes a strip of output columns and a part of the contraction;
-//     its waves take steps in turn.
-//     The last workgroup of a strip to arrive adds the parts.
+//     its waves take steps in turn. The last workgroup of a strip to arrive adds the parts.
+//
+// MI355X, 64 experts 2048 -> 768 -> 2048, 8 choices a token, us in the two kernels: one
+// token at k = 3 11.8 + 10.7 (37.7 M weights, 5.9 us at the codebook reads' rate; about
+// 4.5 us of each kernel is the choice of experts, the table and the first loads), 32
+// tokens at k = 2, 3 33 + 25 (49 experts chosen, 231 M weights). 15 experts 5120 -> 1280,
+// 13 tokens, k = 4: 45 + 27 (255 M weights).
 #include "common.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
@@ -208,6 +214,21 @@ __device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
     return best;
 }
 
+// h of a token in a column of the chosen expert number `at`; columns behind the last are
+// zeros there.
+template <int MT>
+__device__ __forceinline__ void put_h(const UpArgs& p, int at, int col, int token, float v) {
+    if (col >= p.inter) v = 0.f;
+    uint16_t* o = p.h + h_at<MT>(at, h_pieces(p.inter), p.axis_down, col, token);
+    if (MT == 1 && p.tokens <= kHalvedTokens) {
+        const Halves parts = halves_of(v);
+        o[0] = parts.upper;
+        o[8 * kHalvedTokens] = parts.lower;  // 8 lanes on
+    } else {
+        o[0] = round_bf16(v);
+    }
+}
+
 // The choices with their weights into LDS (a barrier follows before they are read).
 __device__ __forceinline__ void stage_choices(Choice* given, const Slots& slots, const UpArgs& p) {
 #pragma unroll
@@ -376,17 +397,6 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         at = next_at;
         in = next_in;
     };
-    auto put = [&](int expert, int col, int token, float v) {
-        if (col >= p.inter) v = 0.f;
-        uint16_t* o = p.h + h_at<MT>(expert, h_pieces(p.inter), p.axis_down, col, token);
-        if (MT == 1 && p.tokens <= kHalvedTokens) {
-            const Halves parts = halves_of(v);
-            o[0] = parts.upper;
-            o[8 * kHalvedTokens] = parts.lower;  // 8 lanes on
-        } else {
-            o[0] = round_bf16(v);
-        }
-    };
     // h of the chunk from `from` on: of a whole unit per wave from registers (lanes j
     // and j + 8 hold its gate and up; lane l the weight of token l) ...
     auto finish_alone = [&](int from) {
@@ -409,7 +419,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
                     const int token = 16 * m + 4 * c + i;
                     const float up = __shfl_xor(acc[g][m][i], 8), weight = __shfl(mine, token);
                     if (j < 8 && ((mask >> token) & 1))
-                        put(fa, fi * kUnitCols + j, token, h_value(weight, acc[g][m][i], up));
+                        put_h<MT>(p, fa, fi * kUnitCols + j, token, h_value(weight, acc[g][m][i], up));
                 }
             if (++fi == per) {
                 fi = 0;
@@ -455,7 +465,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
                     up[0] += k < ways ? up[k] : 0.f;
                 }
                 if ((chosen.mask[e] >> token) & 1)
-                    put(expert, (unit - expert * per) * kUnitCols + col, token, h_value(weight, gate[0], up[0]));
+                    put_h<MT>(p, expert, (unit - expert * per) * kUnitCols + col, token, h_value(weight, gate[0], up[0]));
             }
             if (chunk + 1 < chunks || r0 + round < kChunk) __syncthreads();
         }
@@ -472,9 +482,9 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     }
 }
 
-// Many tokens of which each expert has few: a tile is up to 16 tokens of one expert, of
-// its own operands, where all tokens would take two. A wave takes units of its own; none
-// waits for another. h is stored for two operands of tokens, as the other kernel does.
+// More than 16 tokens of which each expert has few: a tile is up to 16 tokens of one
+// expert, one operand where all tokens would take two. A wave takes units of its own;
+// none waits for another. h is stored for two operands of tokens, as the other kernel does.
 struct Tiles {
     uint16_t tile[kMaxGroups + kMaxSlots / 17];  // 2 (number of the chosen expert) + (tokens 16 ...)
 };
@@ -511,6 +521,7 @@ __device__ __forceinline__ int set_bit(uint32_t mask, int n) {
 
 template <int K>
 __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
+    constexpr int MT = 2;  // operands of tokens in h
     __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     __shared__ Tiles tiles;
@@ -618,8 +629,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
                 const int row = 4 * c + i, t = __shfl(done_token, row), col = (done_in + g) * kUnitCols + j;
                 const float up = __shfl_xor(acc[g][0][i], 8), weight = __shfl(mine, row);
                 if (j < 8 && row < done_rows)
-                    p.h[h_at<2>(done_at, h_pieces(p.inter), p.axis_down, col, t)] =
-                        col < p.inter ? round_bf16(h_value(weight, acc[g][0][i], up)) : uint16_t{0};
+                    put_h<MT>(p, done_at, col, t, h_value(weight, acc[g][0][i], up));
             }
         }
         if (u == end) return;
@@ -952,19 +962,24 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
 }
 
 // More than 16 tokens as tiles where an expert has kListedTokens of them or fewer on
-// average (one may have two tiles), else all tokens in two operands. The whole layer of
-// 2048 -> 768, us (tiles / all tokens), 32 tokens with 8 choices at k = 3: 64 experts (4
-// tokens each) 82 / 96, 32 experts 58 / 61, 24 experts 56 / 59, 16 experts 54 / 52 (k =
-// 2: 47 / 50); with 4 of 8 experts 39 / 33; one expert 39 / 27. Up to 16 tokens all are
-// one operand anyway: 62 / 62 for 64 experts, 36 / 34 for 16, 80 / 73 for 15 of 5120 ->
-// 1280, where the units are too few to give every wave its own.
-constexpr int kListedTokens = 12;
+// average (beyond 16 it has two tiles, and is decoded twice) and the experts have units
+// for half of the waves, else all tokens in two operands. The whole layer of 2048 -> 768,
+// us (tiles / all tokens), 32 tokens with 8 choices: 64 experts (4 tokens each) at k = 3
+// 78 / 96, 20 experts (13 each) 55 / 62, 16 experts 54 / 55, 12 experts (21 each) at k = 2
+// 42 / 46; with 4 of 8 experts (16 each, 768 units) 39 / 33; one expert 39 / 27, and one
+// of 5120 -> 5120 70 / 50. Up to 16 tokens all are one operand anyway: 60 / 62 for 16
+// tokens of 64 experts, but 53 / 50 for 8 tokens and 77 / 74 for 13 of 15 experts 5120 ->
+// 1280, where waves that share units have more even work.
+constexpr int kListedTokens = 20;
 
 template <int K>
 hipError_t launch_up(const UpArgs& p, hipStream_t st) {
-    auto kernel = p.tokens <= 16                                    ? layer_up_kernel<K, 1>
-                  : p.tokens * p.top_k <= kListedTokens * p.experts ? layer_up_listed_kernel<K>
-                                                                    : layer_up_kernel<K, 2>;
+    const int slots = p.tokens * p.top_k;
+    const int64_t units = static_cast<int64_t>(slots < p.experts ? slots : p.experts) * p.per;
+    const bool listed = slots <= kListedTokens * p.experts && 2 * units >= cu_count() * kExWaves;
+    auto kernel = p.tokens <= 16 ? layer_up_kernel<K, 1>
+                  : listed       ? layer_up_listed_kernel<K>
+                                 : layer_up_kernel<K, 2>;
     return launch_kernel(kernel, dim3(cu_count()), dim3(kExThreads), st, p);
 }
 

@@ -112,7 +112,8 @@ SIZES = [
     (32, 1, 1, 512, 1, 2, 3, 0), (7, 2, 6, 2304, 256, 3, 4, 1), (24, 2, 3, 768, 100, 2, 2, 0),
     (13, 4, 15, 1280, 272, 4, 4, 0), (4, 1, 1, 1280, 1000, 3, 3, 0), (20, 1, 1, 1024, 768, 2, 4, 1),
     (32, 8, 9, 8448, 40, 2, 3, 0), (32, 8, 64, 768, 256, 3, 3, 1), (18, 3, 200, 1280, 52, 4, 2, 0),
-    (32, 2, 8, 2048, 8, 2, 2, 0), (29, 1, 300, 256, 300, 3, 4, 0),
+    (32, 2, 8, 2048, 8, 2, 2, 0), (29, 1, 300, 256, 300, 3, 4, 0), (17, 8, 64, 512, 129, 2, 4, 0),
+    (32, 32, 55, 256, 150, 2, 3, 0),
 ]
 
 
@@ -124,10 +125,10 @@ def test_layer(gpu_lib, size):
 
 
 @pytest.mark.parametrize("popular", [16, 17, 25, 32])
-@pytest.mark.parametrize("k,axis,inter", [(2, 1, 256), (3, 0, 44), (4, 0, 3)])
+@pytest.mark.parametrize("k,axis,inter", [(2, 1, 512), (3, 0, 348), (4, 0, 345), (3, 0, 3)])
 def test_one_expert_has_most(gpu_lib, popular, k, axis, inter):
     """Many tokens of few per expert, but for one that 16, 17 or all of them chose: it
-    has one tile of tokens or two."""
+    has one tile of tokens or two (but in the narrow case, where all are two operands)."""
     say(f"layer, {popular} of 32 tokens for one expert, k={k}")
     p = Layer(16, 32, 2, 24, 512, inter, k, k, axis)
     p.ids[:, 0] = torch.where(torch.randperm(32, generator=torch.Generator().manual_seed(popular)) < popular, 5, -1)
@@ -142,7 +143,8 @@ def test_block_pairs(gpu_lib, size):
     check(gpu_lib.experts_mlp(*p.cuda()), *p.want())
 
 
-@pytest.mark.parametrize("size", [(3, 4, 6, 256, 40, 3, 3, 0), (30, 6, 5, 512, 256, 2, 4, 1)])
+@pytest.mark.parametrize("size", [(3, 4, 6, 256, 40, 3, 3, 0), (30, 6, 5, 512, 256, 2, 4, 1),
+                                  (30, 6, 48, 256, 180, 3, 2, 0)])
 @pytest.mark.parametrize("weighted", [True, False])
 def test_same_expert_twice_and_none(gpu_lib, size, weighted):
     """Ids that occur more than once in a token, and ids that choose none."""
@@ -168,7 +170,8 @@ def test_no_tokens(gpu_lib):
     assert gpu_lib.experts_mlp(*p.cuda()).shape == (0, 256)
 
 
-@pytest.mark.parametrize("size", [(6, 2, 8, 512, 100, 3, 3, 0), (20, 2, 8, 512, 256, 2, 4, 1), (20, 3, 6, 512, 100, 2, 4, 0)])
+@pytest.mark.parametrize("size", [(6, 2, 8, 512, 100, 3, 3, 0), (20, 2, 8, 512, 256, 2, 4, 1), (20, 3, 6, 512, 100, 2, 4, 0),
+                                  (20, 3, 48, 256, 200, 3, 3, 0)])
 def test_not_finite_stays_where_it_is(gpu_lib, size):
     """NaN in one token's row, and an expert of infinite weights, reach only the tokens
     that have them."""
@@ -218,7 +221,8 @@ def test_workspace_holds_anything(gpu_lib):
             assert torch.equal(gpu_lib.experts_mlp(*args, workspace=ws), want)
 
 
-@pytest.mark.parametrize("size", [(1, 8, 64, 512, 300, 3, 3, 0), (32, 4, 16, 512, 256, 2, 2, 1)])
+@pytest.mark.parametrize("size", [(1, 8, 64, 512, 300, 3, 3, 0), (32, 4, 16, 512, 256, 2, 2, 1),
+                                  (32, 4, 40, 256, 216, 4, 3, 0)])
 def test_captured_and_replayed(gpu_lib, size):
     """Replays with other tokens and other experts, between the program's own calls."""
     p = Layer(9, *size)
