@@ -5,6 +5,10 @@
 // A lane takes 8 adjacent columns of a row (of both halves of [g, u]), four lanes a
 // group of 32, whose largest exponent they exchange in registers: no LDS, no second
 // pass. Rows of any length start at any boundary: a wide access needs none.
+//
+// MI355X, us: [g, u] of 4096 x 17408 to h and 8 bits 100, and back through the gradient
+// 100 (575 MB each, 5.75 TB/s, where a large copy reaches 5.2 to 5.5); 4096 x 5120 kept
+// 12.9, restored 11.3; rows of odd length, 811 x 4111 with h made again, 10.8 (40 MB).
 #include "common.hpp"
 #include "groups.hpp"
 #include "kept.hpp"

@@ -440,3 +440,55 @@ def test_a_training_step(gpu_lib):
         assert size.shape == want.shape
     assert bool(da2.isfinite().all()) and bool(db2.isfinite().all()) and bool(dx.isfinite().all())
     assert bool(db1.isfinite().all())
+
+
+def test_a_layer_of_experts(gpu_lib):
+    """A layer of experts, forward and backward, as a training run has it: [g, u] in 8 bits
+    between the passes. The result and dx against float64: their norms' error is that of
+    the bf16 roundings on the way (each below half a step of its value)."""
+    from dequant_gemm_trellis_amd import synth
+
+    tokens, top_k, n, hidden, inter = 50, 3, 7, 512, 256
+    say("a layer of experts, forward and backward")
+    g = np.random.default_rng(25)
+    up, up_back = synth.Shape(1, 256, 12, 3, hidden, 2 * inter), synth.Shape(0, 256, 12, 3, 2 * inter, hidden)
+    down, down_back = synth.Shape(0, 256, 12, 4, inter, hidden), synth.Shape(1, 256, 12, 4, hidden, inter)
+
+    def coded(shape):
+        codes = g.integers(0, 2 ** 32, (n, shape.rows, shape.words_per_row), dtype=np.uint32)
+        scales = g.uniform(0.5, 1.5, (n, shape.rows)) * shape.in_features ** -0.5
+        return (torch.from_numpy(codes.view(np.int32)).cuda(), torch.from_numpy(scales.astype(np.float32)).cuda(),
+                torch.from_numpy(g.standard_normal(4096).astype(np.float32)).cuda())
+
+    wu, wd = coded(up), coded(down)
+    x = torch.from_numpy(g.standard_normal((tokens, hidden))).to(torch.bfloat16).cuda()
+    dz = torch.from_numpy(g.standard_normal((tokens, hidden))).to(torch.bfloat16).cuda()
+    ids = torch.from_numpy(np.stack([g.permutation(n)[:top_k] for _ in range(tokens)]).astype(np.int32)).cuda()
+    w = torch.from_numpy(g.uniform(0.1, 1, (tokens, top_k)).astype(np.float32)).cuda()
+    r = gpu_lib.route(ids, n)
+    gu = gpu_lib.experts(gpu_lib.dispatch(x, r), r.offsets, *wu, up)
+    h, kept = gpu_lib.swiglu(gu, keep=True)
+    ys = gpu_lib.experts(h, r.offsets, *wd, down)
+    z = gpu_lib.combine(ys, w, r)
+    dys, dw = gpu_lib.combine_backward(dz, ys, w, r)
+    dgu, again = gpu_lib.swiglu_backward(gpu_lib.experts(dys, r.offsets, *wd, down_back), kept, again=True)
+    dx = gpu_lib.combine(gpu_lib.experts(dgu, r.offsets, *wu, up_back), None, r)
+    # the same in float64 from the rows that each step had
+    held = gpu_lib.restore(kept).reshape(gu.shape).double().cpu()
+    near(h, ref.swiglu(gu.double().cpu()), forward_slack(gu.double().cpu()))
+    near(again, ref.swiglu(held), forward_slack(held))
+    want_z, want_dx = torch.zeros((tokens, hidden)).double(), torch.zeros((tokens, hidden)).double()
+    place = r.position.cpu()
+    for m in range(tokens):
+        for k in range(top_k):
+            e, s = int(ids[m, k]), int(place[m, k])
+            we = gpu_lib.expand(wd[0][e], wd[1][e], wd[2], down).double().cpu()      # [inter, hidden]
+            ue = gpu_lib.expand(wu[0][e], wu[1][e], wu[2], up).double().cpu()        # [2 inter, hidden]
+            want_z[m] += float(w[m, k]) * (h[s].double().cpu() @ we)
+            dh = float(w[m, k]) * (dz[m].double().cpu() @ we.T)
+            want_dx[m] += ref.swiglu_backward(dh[None], held[s][None])[0] @ ue
+    # dys, dh, dgu, the products' rows and dx are rounded: five half steps at most, and the
+    # roundings of different values do not add up in the norm
+    assert float((dx.double().cpu() - want_dx).norm() / want_dx.norm()) < 5 * HALF
+    assert float((z.double().cpu() - want_z).norm() / want_z.norm()) < 2 * HALF
+    assert bool(dw.isfinite().all())
