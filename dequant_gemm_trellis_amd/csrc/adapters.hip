@@ -417,8 +417,9 @@ __global__ __launch_bounds__(kOneThreads) void direct_kernel(
 }
 
 // The gradients of an adapter's factors over few rows: a workgroup takes 512
-// columns and 4 ranks of one adapter (KEPT: side b's rows are held in 8 bits), finds its rows (ascending), and its waves
-// take them in turn: 4 ranks x 8 columns of float32 sums per lane. Of W waves,
+// columns and 4 ranks of one adapter (KEPT: side b's rows are held in 8 bits), finds
+// its rows (ascending), and its waves take them in turn: 4 ranks x 8 columns of
+// float32 sums per lane. Of W waves,
 // wave q adds wave q + W / 2's sums to its own, then the halves meet in order.
 // `inner` are the float32 rank-long values without the scale. Grid: (column
 // chunks of side a then of side b, adapters, 4 ranks each).
@@ -967,7 +968,8 @@ __device__ __forceinline__ void outer_segment(const OuterSide& p, const SegInfo&
 }
 
 // Both sums in one launch. VEC: both sides' rows are whole 16-byte pieces. KEPT: side
-// b's rows are held in 8 bits (8-byte pieces there). Without a list (no rows) every adapter is one segment of none.
+// b's rows are held in 8 bits (8-byte pieces there). Without a list (no rows) every
+// adapter is one segment of none.
 // Grid: (strips of side a then of side b, segments, rank pairs).
 template <int R, bool VEC, bool KEPT>
 __global__ __launch_bounds__(kWgThreads, KEPT ? 2 : 1) void outer_kernel(

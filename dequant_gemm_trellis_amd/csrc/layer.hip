@@ -198,14 +198,23 @@ __device__ __forceinline__ Halves halves_of(float h) {
 }
 
 // How the eight waves share a workgroup's units: 2^w of them a unit's blocks, in
-// teams that share the units. The fewest rounds of blocks win; several waves to a unit
-// pay for meeting in LDS (`meet` quarter rounds a chunk).
+// teams that share the units. The fewest rounds of blocks win, in which every wave reads
+// the tokens' operands of its blocks once a chunk: in quarter rounds 1, of two operands,
+// which do not stay ahead, 4. us of the whole layer without and with them: 32 tokens of 3
+// experts 5120 -> 5120 at k = 4 130 / 86, of one 5120 -> 17408 at k = 2 113 / 85, 16 tokens
+// of 3 experts 80 / 73; 2 for two operands left one expert 5120 -> 5120 at 48 (43), 2 for
+// one took 16 tokens of 64 experts from 62 to 64. Several waves to a unit pay for meeting
+// in LDS (`meet` a chunk: without, the first product of 32 tokens of 64 experts 2048 ->
+// 768 at k = 2 in two operands took 63 us for 54).
+template <int MT>
 __device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
+    constexpr int reads = MT == 1 ? 1 : 4;
     int best = 0, least = INT32_MAX;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const int each = (units + (kExWaves >> w) - 1) >> (3 - w);
-        const int cost = 4 * ((nb + (1 << w) - 1) >> w) * each + (w ? (each + kChunk - 1) / kChunk * meet : 0);
+        const int chunks = (each + kChunk - 1) / kChunk;
+        const int cost = ((nb + (1 << w) - 1) >> w) * (4 * each + reads * chunks) + (w ? chunks * meet : 0);
         if (cost < least) {
             least = cost;
             best = w;
@@ -315,7 +324,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
     const int units = share + (static_cast<int>(blockIdx.x) < rest);
     if (units == 0) return;
     const int round = min(kChunk, p.round);  // units that meet at once
-    const int lw = log_ways_for(units, nb, p.meet), ways = 1 << lw, lt = 3 - lw;
+    const int lw = log_ways_for<MT>(units, nb, p.meet), ways = 1 << lw, lt = 3 - lw;
     const int way = wave & (ways - 1), team = wave >> lw;
     auto team_first = [&](int t) { return u0 + ((units * t) >> lt); };
     const int first = team_first(team), end = team_first(team + 1);
@@ -333,8 +342,8 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
         for (int s = 0; s < 8; ++s) o[s] = *reinterpret_cast<const u32x4*>(x[m] + static_cast<size_t>(b) * kT + 8 * s);
     };
     floatx4 acc[kChunk][MT] = {};
-    // the wave's place in its team's units and blocks, and unit u's expert and columns.
-    // Loads without a branch: the workgroup's last unit stands for those that are not.
+    // the wave's place in its team's units and blocks, and unit u's expert and columns (a
+    // team without a unit loads the workgroup's last, and does not use it)
     int u = first, b = min(way, nb - 1), at = first / per, in = first - at * per;
     {
         int v = min(first, u0 + units - 1), va = at, vi = in, e[kChunk], col0[kChunk];
@@ -649,7 +658,7 @@ struct DownArgs {
     uint64_t words;
     uint32_t inverse;   // ceil(2^32 / top_k)
     int strips, ways;   // strips of columns, parts of the contraction
-    float* partial;     // [way][tokens][hidden]
+    float* partial;     // [strip][way][token][columns of a strip]
     uint32_t* arrived;  // [strip] workgroups whose part is there
     uint16_t* out;
 };
@@ -681,12 +690,13 @@ __device__ __forceinline__ uint32_t rows_of(const DownArgs& p, uint32_t mask) {
 }
 
 // The waves' sums of a strip of COLS columns, in wave order, are the workgroup's part; a
-// lane's column n is at(n). `sums` takes the table's place. The last
-// workgroup of a strip to arrive adds the parts, in their order, whichever it is. Parts
-// and arrivals are device-scope accesses, which no die's L2 keeps to itself, and a wave
-// waits until its parts are in memory before its workgroup arrives: fences instead,
-// which write a whole L2 back, took 35 to 50 us of a call, a kernel of its own for the
-// sums 2.4 to 4.8 us and the host's launch.
+// lane's column n is at(n). `sums` takes the table's place. The last workgroup of a strip
+// to arrive adds the parts, in their order, whichever it is. Parts and arrivals are
+// device-scope accesses, which no die's L2 keeps to itself, and a wave waits until its
+// parts are in memory before its workgroup arrives: with fences instead, which write a
+// whole L2 back, the kernel took 44 and 88 us for 1 and 32 tokens of 64 experts where it
+// takes 11.5 and 27; a kernel of its own for the sums took 2.4 to 5.3 us and the host's
+// launch.
 template <int COLS, int N, int MT, typename F>
 __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way,
                                          const floatx4 (&total)[N][MT], F&& at) {
@@ -962,21 +972,23 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
 }
 
 // More than 16 tokens as tiles where an expert has kListedTokens of them or fewer on
-// average (beyond 16 it has two tiles, and is decoded twice) and the experts have units
-// for half of the waves, else all tokens in two operands. The whole layer of 2048 -> 768,
-// us (tiles / all tokens), 32 tokens with 8 choices: 64 experts (4 tokens each) at k = 3
-// 78 / 96, 20 experts (13 each) 55 / 62, 16 experts 54 / 55, 12 experts (21 each) at k = 2
-// 42 / 46; with 4 of 8 experts (16 each, 768 units) 39 / 33; one expert 39 / 27, and one
-// of 5120 -> 5120 70 / 50. Up to 16 tokens all are one operand anyway: 60 / 62 for 16
-// tokens of 64 experts, but 53 / 50 for 8 tokens and 77 / 74 for 13 of 15 experts 5120 ->
-// 1280, where waves that share units have more even work.
-constexpr int kListedTokens = 20;
+// average (with more it has two tiles, and is decoded twice) and the experts have more
+// units than there are waves, else all tokens in two operands. The whole layer, us (tiles
+// / all tokens), 32 tokens with 8 choices, 2048 -> 768 at k = 3: 64 experts (4 tokens
+// each) 76 / 92, 24 experts (11 each, 2304 units) 55 / 58, 20 experts (13 each, 1920
+// units) 54 / 48, 12 experts 47 / 41; 2048 -> 1024, 4 of 16 experts (8 each, 2048 units) 53 / 48;
+// 5120 -> 5120, 4 experts (16 each, 2560 units) 111 / 117; one expert 5120 -> 17408 and 18
+// tokens 123 / 92; but 15 experts 5120 -> 1280 (17 each, 2400 units) 112 / 119 and (13
+// each) 113 / 110. Up to 16 tokens all are one operand anyway: 60 / 62 for 16 tokens of 64
+// experts, but 53 / 50 for 8 tokens and 77 / 74 for 13 of 15 experts 5120 -> 1280, where
+// waves that share units have more even work.
+constexpr int kListedTokens = 16;
 
 template <int K>
 hipError_t launch_up(const UpArgs& p, hipStream_t st) {
     const int slots = p.tokens * p.top_k;
     const int64_t units = static_cast<int64_t>(slots < p.experts ? slots : p.experts) * p.per;
-    const bool listed = slots <= kListedTokens * p.experts && 2 * units >= cu_count() * kExWaves;
+    const bool listed = slots <= kListedTokens * p.experts && units > cu_count() * kExWaves;
     auto kernel = p.tokens <= 16 ? layer_up_kernel<K, 1>
                   : listed       ? layer_up_listed_kernel<K>
                                  : layer_up_kernel<K, 2>;

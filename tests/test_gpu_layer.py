@@ -114,6 +114,13 @@ SIZES = [
     (32, 8, 9, 8448, 40, 2, 3, 0), (32, 8, 64, 768, 256, 3, 3, 1), (18, 3, 200, 1280, 52, 4, 2, 0),
     (32, 2, 8, 2048, 8, 2, 2, 0), (29, 1, 300, 256, 300, 3, 4, 0), (17, 8, 64, 512, 129, 2, 4, 0),
     (32, 32, 55, 256, 150, 2, 3, 0),
+    # more units of 8 columns than 256 compute units have waves, of few tokens each ...
+    (32, 8, 64, 256, 264, 2, 4, 0), (17, 8, 130, 256, 129, 3, 3, 0), (30, 6, 70, 512, 256, 3, 2, 1),
+    (21, 5, 40, 768, 412, 4, 2, 0), (32, 1, 300, 256, 521, 2, 3, 0), (32, 32, 70, 256, 237, 4, 4, 0),
+    # ... of many, and as many units as waves
+    (17, 3, 3, 256, 5470, 2, 2, 0), (32, 4, 16, 512, 1024, 3, 3, 1),
+    # few units a workgroup of many blocks, many units of few
+    (32, 2, 3, 5120, 700, 4, 3, 0), (16, 2, 3, 5120, 700, 2, 4, 0), (32, 1, 1, 256, 17408, 2, 2, 0),
 ]
 
 
@@ -125,10 +132,11 @@ def test_layer(gpu_lib, size):
 
 
 @pytest.mark.parametrize("popular", [16, 17, 25, 32])
-@pytest.mark.parametrize("k,axis,inter", [(2, 1, 512), (3, 0, 348), (4, 0, 345), (3, 0, 3)])
+@pytest.mark.parametrize("k,axis,inter", [(2, 1, 512), (3, 0, 348), (4, 0, 345), (3, 0, 3), (2, 1, 768),
+                                            (3, 0, 700), (4, 0, 697)])
 def test_one_expert_has_most(gpu_lib, popular, k, axis, inter):
     """Many tokens of few per expert, but for one that 16, 17 or all of them chose: it
-    has one tile of tokens or two (but in the narrow case, where all are two operands)."""
+    has one tile of tokens or two (with fewer columns than 690 all are two operands)."""
     say(f"layer, {popular} of 32 tokens for one expert, k={k}")
     p = Layer(16, 32, 2, 24, 512, inter, k, k, axis)
     p.ids[:, 0] = torch.where(torch.randperm(32, generator=torch.Generator().manual_seed(popular)) < popular, 5, -1)
@@ -136,7 +144,8 @@ def test_one_expert_has_most(gpu_lib, popular, k, axis, inter):
     check(gpu_lib.experts_mlp(*p.cuda()), *p.want())
 
 
-@pytest.mark.parametrize("size", [(2, 2, 8, 512, 512, 2, 3, 1), (18, 4, 6, 1024, 100, 3, 2, 0)])
+@pytest.mark.parametrize("size", [(2, 2, 8, 512, 512, 2, 3, 1), (18, 4, 6, 1024, 100, 3, 2, 0),
+                                  (18, 4, 40, 512, 512, 2, 4, 1)])
 def test_block_pairs(gpu_lib, size):
     say(f"layer, pairs, {size}")
     p = Layer(2, *size, il=2)
@@ -144,7 +153,7 @@ def test_block_pairs(gpu_lib, size):
 
 
 @pytest.mark.parametrize("size", [(3, 4, 6, 256, 40, 3, 3, 0), (30, 6, 5, 512, 256, 2, 4, 1),
-                                  (30, 6, 48, 256, 180, 3, 2, 0)])
+                                  (30, 6, 48, 256, 180, 3, 2, 0), (30, 6, 48, 256, 360, 3, 2, 0)])
 @pytest.mark.parametrize("weighted", [True, False])
 def test_same_expert_twice_and_none(gpu_lib, size, weighted):
     """Ids that occur more than once in a token, and ids that choose none."""
@@ -171,7 +180,7 @@ def test_no_tokens(gpu_lib):
 
 
 @pytest.mark.parametrize("size", [(6, 2, 8, 512, 100, 3, 3, 0), (20, 2, 8, 512, 256, 2, 4, 1), (20, 3, 6, 512, 100, 2, 4, 0),
-                                  (20, 3, 48, 256, 200, 3, 3, 0)])
+                                  (20, 3, 48, 256, 200, 3, 3, 0), (20, 3, 48, 256, 365, 3, 3, 0)])
 def test_not_finite_stays_where_it_is(gpu_lib, size):
     """NaN in one token's row, and an expert of infinite weights, reach only the tokens
     that have them."""
@@ -194,7 +203,7 @@ def test_not_finite_stays_where_it_is(gpu_lib, size):
 
 
 @pytest.mark.parametrize("tokens", [5, 12, 20])
-@pytest.mark.parametrize("inter", [33, 300, 40])
+@pytest.mark.parametrize("inter", [33, 300, 40, 4110])
 def test_infinite_last_row(gpu_lib, inter, tokens):
     """The last stored row of a partial step may be infinite: its column of h makes
     infinities of it, and nothing makes NaN."""
@@ -210,7 +219,7 @@ def test_infinite_last_row(gpu_lib, inter, tokens):
 
 def test_workspace_holds_anything(gpu_lib):
     """Nothing that lay in the workspace enters, NaN or other."""
-    for size in ((5, 2, 8, 512, 300, 3, 3, 0), (20, 3, 8, 512, 256, 2, 2, 1)):
+    for size in ((5, 2, 8, 512, 300, 3, 3, 0), (20, 3, 8, 512, 256, 2, 2, 1), (20, 3, 48, 256, 365, 3, 3, 0)):
         say(f"layer, workspace {size}")
         p = Layer(8, *size)
         args = p.cuda()
@@ -222,7 +231,7 @@ def test_workspace_holds_anything(gpu_lib):
 
 
 @pytest.mark.parametrize("size", [(1, 8, 64, 512, 300, 3, 3, 0), (32, 4, 16, 512, 256, 2, 2, 1),
-                                  (32, 4, 40, 256, 216, 4, 3, 0)])
+                                  (32, 4, 40, 256, 216, 4, 3, 0), (32, 4, 40, 256, 420, 4, 3, 0)])
 def test_captured_and_replayed(gpu_lib, size):
     """Replays with other tokens and other experts, between the program's own calls."""
     p = Layer(9, *size)
