@@ -16,10 +16,10 @@
 //     its waves take steps in turn. The last workgroup of a strip to arrive adds the parts.
 //
 // MI355X, 64 experts 2048 -> 768 -> 2048, 8 choices a token, us in the two kernels: one
-// token at k = 3 11.8 + 10.7 (37.7 M weights, 5.9 us at the codebook reads' rate; about
+// token at k = 3 11.9 + 10.7 (37.7 M weights, 5.9 us at the codebook reads' rate; about
 // 4.5 us of each kernel is the choice of experts, the table and the first loads), 32
-// tokens at k = 2, 3 33 + 25 (49 experts chosen, 231 M weights). 15 experts 5120 -> 1280,
-// 13 tokens, k = 4: 45 + 27 (255 M weights).
+// tokens at k = 2, 3 31 + 25 (49 experts chosen, 231 M weights). 15 experts 5120 -> 1280,
+// 13 tokens, k = 4: 46 + 27 (255 M weights).
 #include "common.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
