@@ -34,7 +34,7 @@ constexpr int kUnitCols = 8;  // columns of h per unit: 8 gate and 8 up rows
 constexpr int kChunk = 4;     // units of a wave at a time
 constexpr int kUpPartFloats = 4096;  // 16 columns of 32 tokens of 8 waves
 constexpr int kAhead = 2;     // operands whose codebook values are read ahead
-constexpr int kHalvedTokens = 8;  // up to which h is held as two bf16 parts
+constexpr int kHalvedTokens = 8;  // up to which both parts of h fit one operand
 constexpr int kMeet = 2;      // what a meeting of units costs, in quarter rounds of blocks
 
 // ---- the chosen experts -------------------------------------------------------
@@ -148,14 +148,22 @@ struct LayerTable {
 // [chosen][piece of 32 contracted values][operand][64 lanes][8].
 // Axis 0: piece s is values 32 s + 8 c ...; axis 1: piece (b, s) is values
 // 256 b + 64 c + 8 s ... (c = lane / 16).
+// A value is two bf16 parts. Up to kHalvedTokens tokens both are in one operand, token
+// m's in rows m and m + 8; with more each 16 tokens have an operand of upper parts and
+// behind it one of lower parts.
 __host__ __device__ __forceinline__ int h_pieces(int inter) { return (inter + 31) / 32; }
+__host__ __device__ __forceinline__ int h_operands(int tokens) {
+    return tokens <= kHalvedTokens ? 1 : tokens <= 16 ? 2 : 4;
+}
+// From a value's upper part to its lower one.
+__device__ __forceinline__ int h_lower(int tokens) { return 8 * (tokens <= kHalvedTokens ? kHalvedTokens : kWave); }
 
-template <int MT>
-__device__ __forceinline__ size_t h_at(uint32_t at, uint32_t pieces, int axis, uint32_t col, uint32_t token) {
+__device__ __forceinline__ size_t h_at(uint32_t at, uint32_t pieces, int operands, int axis, uint32_t col,
+                                       uint32_t token) {
     const uint32_t piece = axis == 1 ? col / 256 * 8 + col % 64 / 8 : col / 32;
     const uint32_t c = axis == 1 ? col % 256 / 64 : col % 32 / 8;
-    return ((static_cast<size_t>(at) * pieces + piece) * MT + token / 16) * (kWave * 8) + (16 * c + token % 16) * 8 +
-           col % 8;
+    return ((static_cast<size_t>(at) * pieces + piece) * operands + token / 16 * 2) * (kWave * 8) +
+           (16 * c + token % 16) * 8 + col % 8;
 }
 
 // ---- up -------------------------------------------------------------------------
@@ -182,10 +190,10 @@ __device__ __forceinline__ float h_value(float weight, float g, float u) {
     return weight * (g / (1.f + expf(-g)) * u);
 }
 
-// Up to kHalvedTokens tokens leave half of a 16-row operand free: h goes there as two
-// bf16 parts, the upper 8 bits of its mantissa (cut off) and the rest rounded, token m's
-// in rows m and m + 8, at no cost. With more tokens it is rounded to bf16: half a step,
-// about as much as the rounding of the result (a relative error of 2.3e-3 against 1.7e-3).
+// h enters the second product as two bf16 parts, the upper 8 bits of its mantissa (cut
+// off) and the rest rounded, for any number of tokens: rounded to bf16 as a whole, it
+// moved the result by about as much as the result's own rounding does (a relative error
+// of 2.3e-3 for 1.7e-3), and a token's precision went by the size of its batch.
 // The parts have one sign and are not zero (nor h itself: then the lower one is 2^-24 of
 // the upper), so that an infinite weight gives the infinity that it gives h.
 struct Halves {
@@ -225,17 +233,12 @@ __device__ __forceinline__ int log_ways_for(int units, int nb, int meet) {
 
 // h of a token in a column of the chosen expert number `at`; columns behind the last are
 // zeros there.
-template <int MT>
 __device__ __forceinline__ void put_h(const UpArgs& p, int at, int col, int token, float v) {
     if (col >= p.inter) v = 0.f;
-    uint16_t* o = p.h + h_at<MT>(at, h_pieces(p.inter), p.axis_down, col, token);
-    if (MT == 1 && p.tokens <= kHalvedTokens) {
-        const Halves parts = halves_of(v);
-        o[0] = parts.upper;
-        o[8 * kHalvedTokens] = parts.lower;  // 8 lanes on
-    } else {
-        o[0] = round_bf16(v);
-    }
+    uint16_t* o = p.h + h_at(at, h_pieces(p.inter), h_operands(p.tokens), p.axis_down, col, token);
+    const Halves parts = halves_of(v);
+    o[0] = parts.upper;
+    o[h_lower(p.tokens)] = parts.lower;
 }
 
 // The choices with their weights into LDS (a barrier follows before they are read).
@@ -428,7 +431,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
                     const int token = 16 * m + 4 * c + i;
                     const float up = __shfl_xor(acc[g][m][i], 8), weight = __shfl(mine, token);
                     if (j < 8 && ((mask >> token) & 1))
-                        put_h<MT>(p, fa, fi * kUnitCols + j, token, h_value(weight, acc[g][m][i], up));
+                        put_h(p, fa, fi * kUnitCols + j, token, h_value(weight, acc[g][m][i], up));
                 }
             if (++fi == per) {
                 fi = 0;
@@ -474,7 +477,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
                     up[0] += k < ways ? up[k] : 0.f;
                 }
                 if ((chosen.mask[e] >> token) & 1)
-                    put_h<MT>(p, expert, (unit - expert * per) * kUnitCols + col, token, h_value(weight, gate[0], up[0]));
+                    put_h(p, expert, (unit - expert * per) * kUnitCols + col, token, h_value(weight, gate[0], up[0]));
             }
             if (chunk + 1 < chunks || r0 + round < kChunk) __syncthreads();
         }
@@ -493,7 +496,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_kernel(UpArgs p) {
 
 // More than 16 tokens of which each expert has few: a tile is up to 16 tokens of one
 // expert, one operand where all tokens would take two. A wave takes units of its own;
-// none waits for another. h is stored for two operands of tokens, as the other kernel does.
+// none waits for another. h is stored by tokens, as the other kernel does.
 struct Tiles {
     uint16_t tile[kMaxGroups + kMaxSlots / 17];  // 2 (number of the chosen expert) + (tokens 16 ...)
 };
@@ -530,7 +533,6 @@ __device__ __forceinline__ int set_bit(uint32_t mask, int n) {
 
 template <int K>
 __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
-    constexpr int MT = 2;  // operands of tokens in h
     __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     __shared__ Tiles tiles;
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(kExThreads) void layer_up_listed_kernel(UpArgs p) {
                 const int row = 4 * c + i, t = __shfl(done_token, row), col = (done_in + g) * kUnitCols + j;
                 const float up = __shfl_xor(acc[g][0][i], 8), weight = __shfl(mine, row);
                 if (j < 8 && row < done_rows)
-                    put_h<MT>(p, done_at, col, t, h_value(weight, acc[g][0][i], up));
+                    put_h(p, done_at, col, t, h_value(weight, acc[g][0][i], up));
             }
         }
         if (u == end) return;
@@ -684,9 +686,10 @@ struct Sums {
     }
 };
 
-// The rows of the operand that hold the tokens of a mask.
-__device__ __forceinline__ uint32_t rows_of(const DownArgs& p, uint32_t mask) {
-    return p.tokens <= kHalvedTokens ? mask | mask << kHalvedTokens : mask;
+// The rows of the operands that hold the tokens of a mask.
+template <int P>
+__device__ __forceinline__ uint32_t rows_of(uint32_t mask) {
+    return P == 1 ? mask | mask << kHalvedTokens : mask;
 }
 
 // The waves' sums of a strip of COLS columns, in wave order, are the workgroup's part; a
@@ -697,12 +700,11 @@ __device__ __forceinline__ uint32_t rows_of(const DownArgs& p, uint32_t mask) {
 // whole L2 back, the kernel took 44 and 88 us for 1 and 32 tokens of 64 experts where it
 // takes 11.5 and 27; a kernel of its own for the sums took 2.4 to 5.3 us and the host's
 // launch.
-template <int COLS, int N, int MT, typename F>
+template <int COLS, bool HALVED, int N, int MT, typename F>
 __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way,
                                          const floatx4 (&total)[N][MT], F&& at) {
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = (tid & 63) >> 4;
     __syncthreads();  // the table is read
-    const bool halved = MT == 1 && p.tokens <= kHalvedTokens;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -713,7 +715,7 @@ __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int str
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 v[n] = total[n][m][i];
-                if (halved) {  // row token + 8 is 32 lanes on
+                if constexpr (HALVED) {  // row token + 8 is 32 lanes on
                     const uint32_t bits = __float_as_uint(v[n]);
                     v[n] += __uint_as_float(__builtin_amdgcn_permlane32_swap(bits, bits, false, false)[1]);
                 }
@@ -780,19 +782,21 @@ __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int str
     }
 }
 
-// The tasks of this workgroup, wave by wave: load(work, at, piece) of the next one
-// is in flight while multiply(work) runs; `at` numbers the chosen experts.
+// The tasks of this workgroup, wave by wave: load(work, at, piece, first) of the next one
+// is in flight while multiply(work, next, ahead) runs, which calls ahead() for it;
+// `at` numbers the chosen experts.
 template <typename Work, typename Load, typename Between, typename Multiply, typename Close>
 __device__ __forceinline__ void run_tasks(int first, int end, int pieces, int wave, Load&& load,
                                           Between&& between, Multiply&& multiply, Close&& close) {
     Work q[2];
     int t = first + wave, at = t / pieces;
-    if (t < end) load(q[0], at, t - at * pieces);
+    if (t < end) load(q[0], at, t - at * pieces, true);
     between();
     auto one = [&](Work& now, Work& next) {
         const int nt = t + kExWaves, nat = nt / pieces;
-        if (nt < end) load(next, nat, nt - nat * pieces);
-        multiply(now);
+        multiply(now, next, [&] {
+            if (nt < end) load(next, nat, nt - nat * pieces, false);
+        });
         if (nt >= end || nat != at) close(at);
         t = nt;
         at = nat;
@@ -807,10 +811,14 @@ constexpr int kDownGroups = 2;  // axis 1: 16-row groups of a strip
 constexpr int kDownCols1 = 16 * kDownGroups;
 constexpr int kDownCols0 = 128;
 
-template <int K, int MT>
+// MT operands of 16 tokens, of each P: one that holds both parts of h, or one of each.
+template <int K, int MT, int P>
 __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
     constexpr bool pair = ExTable<K>::pair, rep = ExTable<K>::rep;
-    constexpr int G = kDownGroups;
+    constexpr int G = kDownGroups, N = MT * P;
+    // A task's operands, four a step, are half of the registers: the next task's of a step
+    // come into those that this task's leave. Fewer are held for both tasks.
+    constexpr bool rolled = N == 4;
     __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
@@ -824,7 +832,13 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
     struct Work {
         uint32_t w[G][2 * K + 1];
         float sc[G];
-        u32x4 a[MT][8];
+        u32x4 a[rolled ? 1 : 8][N];
+        const u32x4* h;
+    };
+    u32x4 roll[8][N];  // by steps, the last first
+    auto load_step = [&](u32x4 (&a)[N], const u32x4* from, int s) {
+#pragma unroll
+        for (int o = 0; o < N; ++o) a[o] = from[(s * N + o) * kWave];
     };
     Sums<G, MT> sums;
     int rows[G];
@@ -833,24 +847,26 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
     const u32x4* h = reinterpret_cast<const u32x4*>(p.h) + lane;
     run_tasks<Work>(
         static_cast<int>(tasks * way / p.ways), static_cast<int>(tasks * (way + 1) / p.ways), nb, wave,
-        [&](Work& q, int at, int b) {
+        [&](Work& q, int at, int b, bool first) {
             const int e = __builtin_amdgcn_readfirstlane(chosen.expert[at]);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 load_run64_words<K>(p.codes + e * p.words + block_word<K>(p.lay, rows[g], b), 3 - c, q.w[g]);
                 q.sc[g] = p.scales[static_cast<size_t>(e) * p.hidden + rows[g]];
             }
-            const u32x4* ha = h + (static_cast<size_t>(at) * nb + b) * 8 * MT * kWave;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) q.a[m][s] = ha[(s * MT + m) * kWave];
+            q.h = h + (static_cast<size_t>(at) * nb + b) * 8 * N * kWave;
+            if constexpr (!rolled)
+                static_for<0, 8>([&](auto ic) { load_step(q.a[decltype(ic)::value], q.h, 7 - decltype(ic)::value); });
+            else if (first)
+                static_for<0, 8>([&](auto ic) { load_step(roll[decltype(ic)::value], q.h, 7 - decltype(ic)::value); });
         },
         [&] {
             table.store(tab);
             __syncthreads();
         },
-        [&](Work& q) {
+        [&](Work& q, Work& next, auto&& ahead) {
+            next.h = q.h;
+            ahead();
             Gathered<pair> v[2];
             v[0] = gather_tab<K, 7, pair, rep>(q.w[0], tab);
 #pragma unroll
@@ -861,18 +877,26 @@ __global__ __launch_bounds__(kExThreads) void layer_down1_kernel(DownArgs p) {
                 if constexpr (n < 8 * G) v[n & 1] = gather_tab<K, 7 - n / G, pair, rep>(q.w[n % G], tab);
                 __builtin_amdgcn_s_setprio(0);
                 const u32x4 f = pack_fragment(v[i & 1], q.sc[g]);
+                u32x4(&a)[N] = rolled ? roll[7 - S] : q.a[rolled ? 0 : 7 - S];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    sums.now[g][m] = mfma16x16x32(as_bf16x8(q.a[m][S]), as_bf16x8(f), sums.now[g][m]);
+                for (int o = 0; o < N; ++o)
+                    sums.now[g][o / P] = mfma16x16x32(as_bf16x8(a[o]), as_bf16x8(f), sums.now[g][o / P]);
+                if constexpr (rolled && g + 1 == G) load_step(a, next.h, S);
             });
         },
-        [&](int at) { sums.close(rows_of(p, chosen.mask[chosen.expert[at]]), c); });
-    put_part<kDownCols1>(tab, p, strip, way, sums.total, [&](int n) { return 16 * n + j; });
+        [&](int at) { sums.close(rows_of<P>(chosen.mask[chosen.expert[at]]), c); });
+    put_part<kDownCols1, P == 1>(tab, p, strip, way, sums.total, [&](int n) { return 16 * n + j; });
 }
 
-template <int K, int MT>
+template <int K, int MT, int P>
 __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
-    constexpr int CL = 8;
+    constexpr int CL = 8, N = MT * P;
+    // With two operands of tokens the sums are half of the registers, and at k < 4 the next
+    // task's operands and scales come into those that this task's leave, behind its last
+    // column, its words once this task's are taken (32 tokens x 8 of 64 experts 768 -> 2048:
+    // k = 2 31.6 us, but 49.6 with both tasks' held, which spills 37 registers; k = 3 34.5 /
+    // 39.3 and 6; k = 4 34.6 / 33.4, where both fit).
+    constexpr bool rolled = MT == 2 && K < 4;
     __shared__ __attribute__((aligned(16))) float tab[LayerTable<K>::floats];
     __shared__ Chosen chosen;
     const int lane = threadIdx.x & 63, j = lane & 15, c = lane >> 4;
@@ -883,70 +907,95 @@ __global__ __launch_bounds__(kExThreads) void layer_down0_kernel(DownArgs p) {
     const int live = find_chosen(chosen, slots, p.inverse, p.experts);
     const int strip = blockIdx.x / p.ways, way = blockIdx.x % p.ways, steps = h_pieces(p.inter);
     const int64_t tasks = static_cast<int64_t>(live) * steps;
+    struct Inputs {
+        float sc[8];
+        u32x4 a[N];
+    };
+    struct None {};
     struct Work {
         Words q;
-        float sc[8];
-        u32x4 a[MT];
+        std::conditional_t<rolled, None, Inputs> in;
+        const uint16_t* h;
+        const float* scales;
         int rows;  // stored rows of the step
     };
+    Inputs roll;
+    auto load_inputs = [&](Inputs& in, const Work& q) {
+        // 8 values of a token that lie behind the last are no values at all
+#pragma unroll
+        for (int o = 0; o < N; ++o) in.a[o] = 8 * c < q.rows ? load_at<u32x4>(q.h + o * kWave * 8, 16 * lane) : u32x4{0u, 0u, 0u, 0u};
+        if (q.rows >= 32) {
+            const floatx4 lo = load_at<floatx4_a4>(q.scales, 32 * c);
+            const floatx4 hi = load_at<floatx4_a4>(q.scales + 4, 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                in.sc[i] = lo[i];
+                in.sc[4 + i] = hi[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) in.sc[i] = q.scales[min(8 * c + i, q.rows - 1)];
+        }
+    };
     Sums<CL, MT> sums;
-    const Strip0 first = strip0<K, CL>(p.codes, p.scales, p.lay, strip * kDownCols0, j, c);
-    const u32x4* h = reinterpret_cast<const u32x4*>(p.h) + lane;
+    const Strip0 strip_at = strip0<K, CL>(p.codes, p.scales, p.lay, strip * kDownCols0, j, c);
     run_tasks<Work>(
         static_cast<int>(tasks * way / p.ways), static_cast<int>(tasks * (way + 1) / p.ways), steps, wave,
-        [&](Work& q, int at, int step) {
+        [&](Work& q, int at, int step, bool first) {
             const int e = __builtin_amdgcn_readfirstlane(chosen.expert[at]);
-            Strip0 s = first;
+            Strip0 s = strip_at;
             s.codes += e * p.words;
-            s.scales += static_cast<size_t>(e) * p.inter;
+            q.scales = s.scales + static_cast<size_t>(e) * p.inter + 32 * step;
             q.rows = p.inter - 32 * step;
-            const u32x4* ha = h + (static_cast<size_t>(at) * steps + step) * MT * kWave;
-            // 8 values of a token that lie behind the last are no values at all
-#pragma unroll
-            for (int m = 0; m < MT; ++m) q.a[m] = 8 * c < q.rows ? ha[m * kWave] : u32x4{0u, 0u, 0u, 0u};
+            q.h = p.h + (static_cast<size_t>(at) * steps + step) * (N * kWave * 8);
+            if constexpr (!rolled) load_inputs(q.in, q);
+            else if (first) load_inputs(roll, q);
             if (q.rows >= 32) {
                 load_words(q.q, s, 32 * step);
-                const floatx4 lo = load_at<floatx4_a4>(s.scales + 32 * step, 32 * c);
-                const floatx4 hi = load_at<floatx4_a4>(s.scales + 32 * step + 4, 32 * c);
+            } else {
+                const uint32_t row = static_cast<uint32_t>(32 * c * s.row_words);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q.sc[i] = lo[i];
-                    q.sc[4 + i] = hi[i];
+                for (int i = 0; i < 8; ++i) {
+                    const int r = min(32 * step + 8 * c + i, p.inter - 1);
+                    const uint32_t* w = s.codes + static_cast<uint64_t>(r) * s.row_words;
+                    q.q.a[i] = w[(s.at_a - row) / 4];
+                    q.q.b[i] = w[(s.at_b - row) / 4];
                 }
-                return;
-            }
-            const uint32_t row = static_cast<uint32_t>(32 * c * s.row_words);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = min(32 * step + 8 * c + i, p.inter - 1);
-                const uint32_t* w = s.codes + static_cast<uint64_t>(r) * s.row_words;
-                q.q.a[i] = w[(s.at_a - row) / 4];
-                q.q.b[i] = w[(s.at_b - row) / 4];
-                q.sc[i] = s.scales[r];
             }
         },
         [&] {
             table.store(tab);
             __syncthreads();
         },
-        [&](const Work& q) {
+        [&](Work& q, Work& next, auto&& ahead) {
             Pieces<K, CL> ps;
-            ps.set(q.q, first.sh);
+            next.rows = 0;
+            if constexpr (!rolled) ahead();
+            ps.set(q.q, strip_at.sh);
+            if constexpr (rolled) ahead();
             const int left = q.rows - 8 * c;  // of this lane's 8 rows
-            ps.each(q.sc, tab, [&](auto ec, u32x4 f) {
-                constexpr int e = decltype(ec)::value;
-                if (q.rows < 32) {  // rows behind the last have no weights: theirs may be infinite
+            auto multiply = [&](const Inputs& in) {
+                ps.each(in.sc, tab, [&](auto ec, u32x4 f) {
+                    constexpr int e = decltype(ec)::value;
+                    if (q.rows < 32) {  // rows behind the last have no weights: theirs may be infinite
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        f[d] &= (2 * d < left ? 0xFFFFu : 0u) | (2 * d + 1 < left ? 0xFFFF0000u : 0u);
-                }
+                        for (int d = 0; d < 4; ++d)
+                            f[d] &= (2 * d < left ? 0xFFFFu : 0u) | (2 * d + 1 < left ? 0xFFFF0000u : 0u);
+                    }
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    sums.now[e][m] = mfma16x16x32(as_bf16x8(q.a[m]), as_bf16x8(f), sums.now[e][m]);
-            });
+                    for (int o = 0; o < N; ++o)
+                        sums.now[e][o / P] = mfma16x16x32(as_bf16x8(in.a[o]), as_bf16x8(f), sums.now[e][o / P]);
+                });
+            };
+            if constexpr (!rolled) {
+                multiply(q.in);
+            } else {
+                multiply(roll);
+                if (next.rows) load_inputs(roll, next);
+            }
         },
-        [&](int at) { sums.close(rows_of(p, chosen.mask[chosen.expert[at]]), c); });
-    put_part<kDownCols0>(tab, p, strip, way, sums.total, [&](int n) { return CL * j + n; });
+        [&](int at) { sums.close(rows_of<P>(chosen.mask[chosen.expert[at]]), c); });
+    put_part<kDownCols0, P == 1>(tab, p, strip, way, sums.total, [&](int n) { return CL * j + n; });
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -963,8 +1012,7 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
     p.ways = cu_count() / p.strips;
     if (p.ways < 1) p.ways = 1;
     const size_t chosen = tokens * top_k < experts ? tokens * top_k : experts;
-    const size_t operands = tokens > 16 ? 2 : 1;
-    p.arrived = chosen * h_pieces(inter) * operands * kWave * 16;
+    p.arrived = chosen * h_pieces(inter) * h_operands(tokens) * kWave * 16;
     p.partial = p.arrived + (static_cast<size_t>(p.strips) * sizeof(uint32_t) + 255) / 256 * 256;
     p.bytes = p.partial;
     if (p.ways > 1) p.bytes += static_cast<size_t>(p.strips) * p.ways * tokens * p.cols * sizeof(float);
@@ -997,8 +1045,9 @@ hipError_t launch_up(const UpArgs& p, hipStream_t st) {
 
 template <int K>
 hipError_t launch_down(const DownArgs& p, int axis, hipStream_t st) {
-    auto kernel = axis == 1 ? (p.tokens > 16 ? layer_down1_kernel<K, 2> : layer_down1_kernel<K, 1>)
-                            : (p.tokens > 16 ? layer_down0_kernel<K, 2> : layer_down0_kernel<K, 1>);
+    auto kernel = axis == 1 ? layer_down1_kernel<K, 1, 1> : layer_down0_kernel<K, 1, 1>;
+    if (p.tokens > 16) kernel = axis == 1 ? layer_down1_kernel<K, 2, 2> : layer_down0_kernel<K, 2, 2>;
+    else if (p.tokens > kHalvedTokens) kernel = axis == 1 ? layer_down1_kernel<K, 1, 2> : layer_down0_kernel<K, 1, 2>;
     return launch_kernel(kernel, dim3(p.strips * p.ways), dim3(kExThreads), st, p);
 }
 

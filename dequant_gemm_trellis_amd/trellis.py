@@ -790,11 +790,12 @@ def _expert_set(name: str, w: tuple, geom: Geometry, n: int, device: int) -> Exp
 def experts_mlp(x, ids, weights, up, down, g_up, g_down, out=None, workspace=None,
                 stream=None) -> torch.Tensor:
     """A whole layer of experts for up to 32 tokens: out [tokens, hidden] = the sum over
-    the experts e that a token chose of Wd_e bf16(w silu(Wg_e x) * (Wu_e x)). x: bf16
-    [tokens, hidden]; ids: int32 [tokens, top_k] (others than [0, experts): no choice);
-    weights: float32 [tokens, top_k], or None for ones. up and down: (codes, scales, lut)
-    as for experts, with g_up of axis 1, hidden -> 2 * inter (the gate's rows, then the
-    up's) and g_down of either axis, inter -> hidden. With one expert it is a dense MLP."""
+    the experts e that a token chose of Wd_e (w silu(Wg_e x) * (Wu_e x)), what stands in
+    brackets held in 16 bits of mantissa. x: bf16 [tokens, hidden]; ids: int32 [tokens,
+    top_k] (others than [0, experts): no choice); weights: float32 [tokens, top_k], or None
+    for ones. up and down: (codes, scales, lut) as for experts, with g_up of axis 1, hidden
+    -> 2 * inter (the gate's rows, then the up's) and g_down of either axis, inter ->
+    hidden. With one expert it is a dense MLP."""
     gu, gd = _geom(g_up), _geom(g_down)
     tokens, top_k = _dims("ids", ids, 2)
     dev = _device(x)

@@ -43,9 +43,8 @@ typedef struct trellis_expert_set {
  * w_e[m] is the sum of its weights[m][j] (float32 [tokens][top_k]; null: ones)
  * for those j. An id outside [0, experts) chooses none; a token without a choice
  * gets zeros. Values that a token did not choose do not enter, also where they
- * are not finite. Up to 8 tokens h enters the second product as two bf16 parts (16
- * bits of its mantissa), with more it is rounded to bf16. x and out: bf16
- * [tokens][hidden], 16-byte aligned.
+ * are not finite. h enters the second product as two bf16 parts (16 bits of its
+ * mantissa). x and out: bf16 [tokens][hidden], 16-byte aligned.
  *   up:   axis 1, in = hidden, out = 2 inter: the gate's rows, then the up's
  *   down: either axis, in = inter, out = hidden (axis 1 needs inter % 256 == 0)
  * 0 <= tokens <= TRELLIS_MAX_MLP_TOKENS, 1 <= top_k <= TRELLIS_MAX_MLP_CHOICES,
