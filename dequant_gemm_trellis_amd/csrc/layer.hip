@@ -194,15 +194,17 @@ __device__ __forceinline__ float h_value(float weight, float g, float u) {
 // off) and the rest rounded, for any number of tokens: rounded to bf16 as a whole, it
 // moved the result by about as much as the result's own rounding does (a relative error
 // of 2.3e-3 for 1.7e-3), and a token's precision went by the size of its batch.
-// The parts have one sign and are not zero (nor h itself: then the lower one is 2^-24 of
-// the upper), so that an infinite weight gives the infinity that it gives h.
+// The parts of an h that is not zero have its sign and are not zero either (2^-133 at
+// least, the smallest bf16), so that an infinite weight gives the infinity that it gives h.
 struct Halves {
     uint16_t upper, lower;
 };
 __device__ __forceinline__ Halves halves_of(float h) {
-    const float upper = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u), rest = h - upper;
-    const float lower = !__builtin_isfinite(h) ? upper : rest == 0.f ? upper * 0x1p-24f : rest;
-    return {static_cast<uint16_t>(__float_as_uint(upper) >> 16), round_bf16(lower)};
+    const uint32_t bits = __float_as_uint(h);
+    const float upper = __uint_as_float(bits & 0xFFFF0000u), rest = h - upper;
+    const uint32_t least = (bits >> 16 & 0x8000u) | ((bits & 0x7FFFFFFFu) != 0);
+    const uint32_t hi = bits >> 16, lo = __builtin_isfinite(h) ? round_bf16(rest) : hi;
+    return {static_cast<uint16_t>(hi & 0x7FFFu ? hi : least), static_cast<uint16_t>(lo & 0x7FFFu ? lo : least)};
 }
 
 // How the eight waves share a workgroup's units: 2^w of them a unit's blocks, in

@@ -44,7 +44,8 @@ typedef struct trellis_expert_set {
  * for those j. An id outside [0, experts) chooses none; a token without a choice
  * gets zeros. Values that a token did not choose do not enter, also where they
  * are not finite. h enters the second product as two bf16 parts (16 bits of its
- * mantissa). x and out: bf16 [tokens][hidden], 16-byte aligned.
+ * mantissa; off by up to 2^-132 where that is more), neither of them zero unless h is.
+ * x and out: bf16 [tokens][hidden], 16-byte aligned.
  *   up:   axis 1, in = hidden, out = 2 inter: the gate's rows, then the up's
  *   down: either axis, in = inter, out = hidden (axis 1 needs inter % 256 == 0)
  * 0 <= tokens <= TRELLIS_MAX_MLP_TOKENS, 1 <= top_k <= TRELLIS_MAX_MLP_CHOICES,

@@ -73,3 +73,35 @@ def test_a_token_alone_and_in_a_batch(gpu_lib, axis, inter):
     for n in (1, 5, 12, 23):
         few = gpu_lib.experts_mlp(x[:n], ids[:n], w[:n], *rest).double().cpu()
         assert bool(((few - all32[:n]).abs() <= 2 * bound[:n]).all())
+
+
+TINY = 2.0 ** -132  # what two parts of at least 2^-133, the smallest bf16, may be off
+
+
+@pytest.mark.parametrize("exponent", [-60, -104, -110, -113, -116, -119, -122, -125, -128, -131])
+@pytest.mark.parametrize("tokens", [5, 12, 20])
+def test_small_h(gpu_lib, tokens, exponent):
+    """Weights of the tokens that leave h near the end of bf16's range: finite weights of
+    the experts give what h gives, and infinite ones the infinity that it gives."""
+    say(f"layer, h of about 2^{exponent}, {tokens} tokens")
+    p = few_inputs(33, tokens, 1, 4, 256, 33, 3, 3, 0)
+    p.w *= 2.0 ** exponent
+    p.down["scales"] *= 2.0 ** 66
+    p.down["lut"][p.down["lut"] == 0] = 1.0
+    out, bound = want(p)
+    slack = torch.stack([TINY * p.weights(p.down, int(e)).abs().sum(1) for e in p.ids[:, 0]])
+    got = gpu_lib.experts_mlp(*p.cuda())
+    assert bool(((got.double().cpu() - out).abs() <= bound + slack * (1 + HALF)).all())
+    # a token's sign of every column's infinity is that of the last column's h times the weight
+    last = 32
+    p.down["scales"][:, last] = torch.inf
+    got = gpu_lib.experts_mlp(*p.cuda()).double().cpu()
+    seen = 0
+    for m, e in enumerate(p.ids[:, 0]):
+        g, u = (p.weights(p.up, int(e)) @ p.x[m].double()).chunk(2)
+        h = (p.w[m, 0].double() * g * torch.sigmoid(g) * u)[last]
+        if h.abs() < 2.0 ** -147:  # may be zero in float32
+            continue
+        seen += 1
+        assert torch.equal(got[m], h * p.weights(p.down, int(e))[:, last])
+    assert seen > tokens // 2
