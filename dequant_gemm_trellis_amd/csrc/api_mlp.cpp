@@ -48,6 +48,12 @@ int check_rows(int32_t rows, int32_t most, int32_t width) {
     return rows * padded > TRELLIS_MAX_KEPT_VALUES ? TRELLIS_ERR_GEOMETRY : TRELLIS_OK;
 }
 
+// Rows [g, u] and what is kept of them, [2 rows][inter].
+int check_halves(int32_t rows, int32_t inter) {
+    if (rows < 0 || rows > TRELLIS_MAX_SLOTS || inter > trellis::kMaxFeatures / 2) return TRELLIS_ERR_GEOMETRY;
+    return check_rows(2 * rows, 2 * TRELLIS_MAX_SLOTS, inter);
+}
+
 int check_kept(const trellis_kept* k) {
     return !k || !k->codes || !k->exponents ? TRELLIS_ERR_NULL : TRELLIS_OK;
 }
@@ -116,9 +122,8 @@ int trellis_restore(const trellis_kept* kept, int32_t rows, int32_t width, uint1
 
 int trellis_swiglu(const uint16_t* gu, int32_t rows, int32_t inter, uint16_t* h,
                    const trellis_kept* kept, hipStream_t stream) {
-    int st = check_rows(rows, TRELLIS_MAX_SLOTS, inter);
+    int st = check_halves(rows, inter);
     if (st) return st;
-    if (inter > trellis::kMaxFeatures / 2) return TRELLIS_ERR_GEOMETRY;
     if (rows == 0) return TRELLIS_OK;
     if (!gu || !h || (kept && check_kept(kept))) return TRELLIS_ERR_NULL;
     if (!aligned(gu, 2) || !aligned(h, 2)) return TRELLIS_ERR_ALIGN;
@@ -129,9 +134,9 @@ int trellis_swiglu(const uint16_t* gu, int32_t rows, int32_t inter, uint16_t* h,
 int trellis_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const trellis_kept* kept,
                             int32_t rows, int32_t inter, uint16_t* dgu, uint16_t* h,
                             hipStream_t stream) {
-    int st = check_rows(rows, TRELLIS_MAX_SLOTS, inter);
+    int st = check_halves(rows, inter);
     if (st) return st;
-    if (inter > trellis::kMaxFeatures / 2 || (gu && kept)) return TRELLIS_ERR_GEOMETRY;
+    if (gu && kept) return TRELLIS_ERR_GEOMETRY;
     if (rows == 0) return TRELLIS_OK;
     if (!dh || !dgu || (!gu && check_kept(kept))) return TRELLIS_ERR_NULL;
     if (!aligned(dh, 2) || !aligned(gu, 2) || !aligned(dgu, 2) || !aligned(h, 2)) return TRELLIS_ERR_ALIGN;

@@ -9,6 +9,8 @@
 // MI355X, us: [g, u] of 4096 x 17408 to h and 8 bits 100, and back through the gradient
 // 100 (575 MB each, 5.75 TB/s, where a large copy reaches 5.2 to 5.5); 4096 x 5120 kept
 // 12.9, restored 11.3; rows of odd length, 811 x 4111 with h made again, 10.8 (40 MB).
+#include <algorithm>
+
 #include "common.hpp"
 #include "groups.hpp"
 #include "kept.hpp"
@@ -175,17 +177,35 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     if constexpr (AGAIN) store_values(h + row * d.width + p.col, p.left, swiglu8(g, u));
 }
 
+// A launch has fewer than 2^32 lanes, each of them 8 values of a row (of both halves of
+// [g, u]): what SwiGLU keeps of 2^34 columns has twice as many values, and comes in two.
+template <typename F>
+hipError_t by_parts(int rows, int width, F&& launch) {
+    const int64_t padded = (width + kKeptGroup - 1) / kKeptGroup * kKeptGroup;
+    const int most = static_cast<int>(std::min<int64_t>(rows, (int64_t{1} << 34) / padded));
+    for (int64_t row = 0; row < rows; row += most) {
+        const Deal d = deal(static_cast<int>(std::min<int64_t>(most, rows - row)), width);
+        const hipError_t e = launch(d, row * width, row * (d.pieces / 4));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_keep(const uint16_t* x, int rows, int width, int8_t* codes, uint8_t* exponents,
                        hipStream_t st) {
-    const Deal d = deal(rows, width);
-    return launch_kernel(keep_kernel, grid_of(d), dim3(kThreads), st, x, d, codes, exponents);
+    return by_parts(rows, width, [&](const Deal& d, int64_t at, int64_t group) {
+        return launch_kernel(keep_kernel, grid_of(d), dim3(kThreads), st, x + at, d, codes + at,
+                             exponents + group);
+    });
 }
 
 hipError_t launch_restore(const KeptRows& x, int rows, int width, uint16_t* out, hipStream_t st) {
-    const Deal d = deal(rows, width);
-    return launch_kernel(restore_kernel, grid_of(d), dim3(kThreads), st, x, d, out);
+    return by_parts(rows, width, [&](const Deal& d, int64_t at, int64_t group) {
+        return launch_kernel(restore_kernel, grid_of(d), dim3(kThreads), st,
+                             KeptRows{x.codes + at, x.exponents + group}, d, out + at);
+    });
 }
 
 hipError_t launch_swiglu(const uint16_t* gu, int rows, int inter, uint16_t* h, int8_t* codes,

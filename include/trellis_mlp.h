@@ -65,9 +65,9 @@ size_t trellis_experts_mlp_workspace_bytes(int32_t tokens, int32_t top_k, int32_
                                            const trellis_expert_set *up,
                                            const trellis_expert_set *down);
 
-/* Largest number of values of one of the calls below (rows x width, every row
- * rounded up to 32), and of rows that are kept. */
-#define TRELLIS_MAX_KEPT_VALUES (1ll << 34)
+/* Largest number of values of one of the calls below (rows x width, for SwiGLU those
+ * of [2 rows][inter], every row rounded up to 32), and of rows that are kept. */
+#define TRELLIS_MAX_KEPT_VALUES (1ll << 35)
 #define TRELLIS_MAX_KEPT_ROWS (1 << 22)
 
 /*
