@@ -6,9 +6,10 @@
 // group of 32, whose largest exponent they exchange in registers: no LDS, no second
 // pass. Rows of any length start at any boundary: a wide access needs none.
 //
-// MI355X, us: [g, u] of 4096 x 17408 to h and 8 bits 100, and back through the gradient
-// 100 (575 MB each, 5.75 TB/s, where a large copy reaches 5.2 to 5.5); 4096 x 5120 kept
-// 12.9, restored 11.3; rows of odd length, 811 x 4111 with h made again, 10.8 (40 MB).
+// MI355X, us: [g, u] of 4096 x 17408 to h and 8 bits 101, and back through the gradient
+// 100 (575 MB each, 5.7 TB/s, where a large copy reaches 5.2 to 5.5); 4096 x 5120 kept
+// 12.9, restored 11.3; the gradient of 811 x 4112 with h made again 8.1 (40 MB), of rows
+// that start off 16 bytes 10.9 (4111) and 10.2 (4110).
 #include <algorithm>
 
 #include "common.hpp"
@@ -31,8 +32,9 @@ struct Deal {
     uint32_t groups;   // workgroups of a bundle
 };
 
-// A bundle has 2048 pieces at least (or all rows), so that its last workgroup's idle
-// lanes are few. A piece's number in a bundle of several rows is below 4096, where
+// A bundle has 2048 pieces at least (or all rows), so that at most 12% of its lanes are
+// idle, in its last workgroup. They cost nothing that shows: the gradient of 811 rows of
+// 4096 (none idle) and of 4112 (10%) takes 8.2 and 8.1 us. A piece's number in a bundle of several rows is below 4096, where
 // the product with `inverse` gives the quotient exactly.
 Deal deal(int rows, int width) {
     Deal d{rows, width, 4u * static_cast<uint32_t>((width + kKeptGroup - 1) / kKeptGroup), 0, 1, 0};

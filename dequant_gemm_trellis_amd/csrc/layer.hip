@@ -3,7 +3,7 @@
 //   out[m] = bf16( sum over the experts e that m chose of Wd_e h_e[m] ).
 //
 // With few tokens nearly all work is decoding, through random reads of a codebook table
-// in LDS, which bound it; a decoded operand meets 16 rows in one matrix instruction at no
+// in LDS, its floor; a decoded operand meets 16 rows in one matrix instruction at no
 // cost. So up to 16 tokens none is sorted or moved: every expert that anyone chose is
 // decoded once and multiplied with all tokens, and what a token did not choose is left
 // out of its sums (not multiplied by zero: an infinite weight of another's expert must
@@ -18,8 +18,10 @@
 // MI355X, 64 experts 2048 -> 768 -> 2048, 8 choices a token, us in the two kernels: one
 // token at k = 3 11.9 + 10.7 (37.7 M weights, 5.9 us at the codebook reads' rate; about
 // 4.5 us of each kernel is the choice of experts, the table and the first loads), 32
-// tokens at k = 2, 3 31 + 25 (49 experts chosen, 231 M weights). 15 experts 5120 -> 1280,
-// 13 tokens, k = 4: 46 + 27 (255 M weights).
+// tokens at k = 2, 3 31 + 27 (49 experts chosen, 231 M weights). 15 experts 5120 -> 1280,
+// 13 tokens, k = 4: 46 + 28 (255 M weights). LDS is active 36 to 47% of the time in the
+// larger ones: the table leaves room for two waves per SIMD, which do not cover the
+// latency of the reads and of the loads.
 #include "common.hpp"
 #include "experts.hpp"
 #include "groups.hpp"
@@ -211,9 +213,9 @@ __device__ __forceinline__ Halves halves_of(float h) {
 // teams that share the units. The fewest rounds of blocks win, in which every wave reads
 // the tokens' operands of its blocks once a chunk: in quarter rounds 1, of two operands,
 // which do not stay ahead, 4. us of the whole layer without and with them: 32 tokens of 3
-// experts 5120 -> 5120 at k = 4 130 / 86, of one 5120 -> 17408 at k = 2 113 / 85, 16 tokens
-// of 3 experts 80 / 73; 2 for two operands left one expert 5120 -> 5120 at 48 (43), 2 for
-// one took 16 tokens of 64 experts from 62 to 64. Several waves to a unit pay for meeting
+// experts 5120 -> 5120 at k = 4 134 / 89, of one 5120 -> 17408 at k = 2 117 / 88, 16 tokens
+// of 3 experts 78 / 73; 2 for two operands left one expert 5120 -> 5120 at 50 (45), 2 for
+// one took 16 tokens of 64 experts from 63 to 64. Several waves to a unit pay for meeting
 // in LDS (`meet` a chunk: without, the first product of 32 tokens of 64 experts 2048 ->
 // 768 at k = 2 in two operands took 63 us for 54).
 template <int MT>
@@ -698,10 +700,12 @@ __device__ __forceinline__ uint32_t rows_of(uint32_t mask) {
 // lane's column n is at(n). `sums` takes the table's place. The last workgroup of a strip
 // to arrive adds the parts, in their order, whichever it is. Parts and arrivals are
 // device-scope accesses, which no die's L2 keeps to itself, and a wave waits until its
-// parts are in memory before its workgroup arrives: with fences instead, which write a
-// whole L2 back, the kernel took 44 and 88 us for 1 and 32 tokens of 64 experts where it
-// takes 11.5 and 27; a kernel of its own for the sums took 2.4 to 5.3 us and the host's
-// launch.
+// parts are in memory before its workgroup arrives. That order is the hardware's, not the
+// language's, which has none between relaxed accesses: a device-scope store of gfx950
+// writes through, vmcnt counts it until it has, and the loads behind the count pass by the
+// L2. With fences instead, which write a whole L2 back, the kernel took 44 and 88 us for 1
+// and 32 tokens of 64 experts where it then took 11.5 and 27; a kernel of its own for the
+// sums took 2.4 to 5.3 us and the host's launch.
 template <int COLS, bool HALVED, int N, int MT, typename F>
 __device__ __forceinline__ void put_part(float* sums, const DownArgs& p, int strip, int way,
                                          const floatx4 (&total)[N][MT], F&& at) {
@@ -1025,13 +1029,16 @@ LayerPlan layer_plan(int tokens, int top_k, int experts, int hidden, int inter, 
 // average (with more it has two tiles, and is decoded twice) and the experts have more
 // units than there are waves, else all tokens in two operands. The whole layer, us (tiles
 // / all tokens), 32 tokens with 8 choices, 2048 -> 768 at k = 3: 64 experts (4 tokens
-// each) 76 / 92, 24 experts (11 each, 2304 units) 55 / 58, 20 experts (13 each, 1920
-// units) 54 / 48, 12 experts 47 / 41; 2048 -> 1024, 4 of 16 experts (8 each, 2048 units) 53 / 48;
-// 5120 -> 5120, 4 experts (16 each, 2560 units) 111 / 117; one expert 5120 -> 17408 and 18
-// tokens 123 / 92; but 15 experts 5120 -> 1280 (17 each, 2400 units) 112 / 119 and (13
-// each) 113 / 110. Up to 16 tokens all are one operand anyway: 60 / 62 for 16 tokens of 64
-// experts, but 53 / 50 for 8 tokens and 77 / 74 for 13 of 15 experts 5120 -> 1280, where
+// each) 84 / 99, 24 experts (11 each, 2304 units) 57 / 60, 20 experts (13 each, 1920
+// units) 55 / 49, 12 experts 48 / 41; 2048 -> 1024, 4 of 16 experts (8 each, 2048 units) 55 / 49;
+// 5120 -> 5120, 4 experts (16 each, 2560 units) 117 / 123; one expert 5120 -> 17408 and 18
+// tokens 127 / 97; but 15 experts 5120 -> 1280 (17 each, 2400 units) 116 / 122 and (13
+// each) 117 / 114. Up to 16 tokens all are one operand anyway: 62 / 63 for 16 tokens of 64
+// experts, but 66 / 64 for 8 tokens and 77 / 74 for 13 of 15 experts 5120 -> 1280, where
 // waves that share units have more even work.
+// The host does not know how many experts are chosen, so the average is over all. Where
+// tokens choose alike it is wrong: 32 that all choose the same 8 of 64 experts 2048 -> 768
+// have two tiles of each, and the layer takes 42 where all tokens in two operands take 34.
 constexpr int kListedTokens = 16;
 
 template <int K>

@@ -795,7 +795,8 @@ def experts_mlp(x, ids, weights, up, down, g_up, g_down, out=None, workspace=Non
     top_k] (others than [0, experts): no choice); weights: float32 [tokens, top_k], or None
     for ones. up and down: (codes, scales, lut) as for experts, with g_up of axis 1, hidden
     -> 2 * inter (the gate's rows, then the up's) and g_down of either axis, inter ->
-    hidden. With one expert it is a dense MLP."""
+    hidden. With one expert it is a dense MLP, which gate_up_swiglu and prefill (or a GEMV)
+    mostly do in less time."""
     gu, gd = _geom(g_up), _geom(g_down)
     tokens, top_k = _dims("ids", ids, 2)
     dev = _device(x)

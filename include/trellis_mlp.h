@@ -49,7 +49,9 @@ typedef struct trellis_expert_set {
  *   up:   axis 1, in = hidden, out = 2 inter: the gate's rows, then the up's
  *   down: either axis, in = inter, out = hidden (axis 1 needs inter % 256 == 0)
  * 0 <= tokens <= TRELLIS_MAX_MLP_TOKENS, 1 <= top_k <= TRELLIS_MAX_MLP_CHOICES,
- * 1 <= experts <= TRELLIS_MAX_GROUPS; with experts = 1 it is a dense MLP.
+ * 1 <= experts <= TRELLIS_MAX_GROUPS; with experts = 1 it is a dense MLP, for which
+ * trellis_gate_up_swiglu and the down projection's own call, with h in bf16 between
+ * them, mostly take less time (by 7 to 28% for 5120 -> 17408 -> 5120).
  * Codes of experts that nobody chose are not read. workspace: 16-byte aligned, at
  * least trellis_experts_mlp_workspace_bytes bytes.
  */
